@@ -206,9 +206,9 @@ def _cut(x, fmt):
     b = (bits >> 23) - (6 if fmt == "int8" else 8)
     if fmt == "e4m3":
         b = b + ((bits & 0x7FFFFF) > 0x600000)
-    b = b.clamp(min=0)
+    b = b.clamp(0, 248 if fmt == "int8" else 246)            # restored values stay finite in fp32
     v = v * ((254 - b) << 23).view(torch.float32)            # 2^(127 - b)
-    v = v.round().clamp(-127, 127) if fmt == "int8" else v.to(torch.float8_e4m3fn).float()
+    v = v.round().clamp(-127, 127) if fmt == "int8" else v.clamp(-448, 448).to(torch.float8_e4m3fn).float()
     v = v * torch.where(b > 0, b << 23, 0x400000).view(torch.float32)
     return v.view(rows, -1)[:, :cols]
 
@@ -286,8 +286,8 @@ def _grid(x, fmt):
             step = torch.exp2(torch.clamp(e - 6, min=-127.0))
             q = torch.clamp(torch.round(v / step), -127, 127) * step
         else:
-            unit = torch.exp2(torch.clamp(e - 8 + (2 * m > 1.75), min=-127.0))
-            r = v / unit                                     # |r| <= 448: 3 bits behind the leading one, 2^-9 at least
+            unit = torch.exp2(torch.clamp(e - 8 + (2 * m > 1.75), min=-127.0, max=119.0))
+            r = torch.clamp(v / unit, -448, 448)             # 3 bits behind the leading one, 2^-9 at least
             own_e = torch.clamp(torch.frexp(r)[1].double() - 1, min=-6.0)
             step = torch.exp2(own_e - 3)
             q = torch.round(r / step) * step * unit
