@@ -445,6 +445,165 @@ ufp4_status ufp4_stats(const void *x, int32_t dtype, int64_t rows, int64_t cols,
 
 }  // extern "C"
 
+// ------------------------------------------------ around the grouped GEMMs
+
+namespace {
+
+inline bool valid_dtype(int32_t d) { return d == UFP4_BF16 || d == UFP4_FP32; }
+
+// A rows x width operand of the calls below, checked when it has elements.
+bool valid_rows(const void *p, int32_t dtype, int64_t rows, int64_t width, int64_t ld) {
+    if (!valid_dtype(dtype) || rows < 0 || width < 0 || ld < width) return false;
+    return rows == 0 || width == 0 || (p && aligned(p, dtype == UFP4_BF16 ? 2 : 4));
+}
+
+// rows x width < 2^38, width <= UFP4_MAX_WIDTH, rows and stride < 2^31.
+bool rows_within_limits(int64_t rows, int64_t width, int64_t ld) {
+    if (width > UFP4_MAX_WIDTH || rows > UFP4_MAX_DIM || ld > UFP4_MAX_DIM) return false;
+    return width == 0 || rows < (1LL << 38) / width;
+}
+
+ufp4_status check_plan(const ufp4_moe_plan *plan, MoePlan *m) {
+    if (!plan || plan->reserved != 0 || plan->tokens < 0 || plan->topk < 1) return UFP4_ERR_INVALID;
+    if (plan->n_experts < 1 || plan->n_experts > UFP4_MAX_GROUPS) return UFP4_ERR_INVALID;
+    if (!plan->counts || !plan->offsets || !aligned(plan->counts, 8) || !aligned(plan->offsets, 8))
+        return UFP4_ERR_INVALID;
+    if (plan->tokens > 0 && (!plan->pos || !plan->src || !aligned(plan->pos, 4) || !aligned(plan->src, 4)))
+        return UFP4_ERR_INVALID;
+    if (plan->tokens > UFP4_MAX_DIM / plan->topk) return UFP4_ERR_UNSUPPORTED;
+    *m = MoePlan{plan->pos, plan->src, plan->counts, plan->offsets, plan->tokens, plan->topk, plan->n_experts};
+    return UFP4_OK;
+}
+
+bool valid_ckpt(const ufp4_ckpt *c) {
+    if (!c || c->reserved != 0 || c->rows < 0 || c->cols < 0) return false;
+    if (c->format != UFP4_CKPT_INT8 && c->format != UFP4_CKPT_E4M3) return false;
+    return c->rows == 0 || c->cols == 0 || (c->codes && c->scales && aligned(c->codes, 16));
+}
+Ckpt ckpt_of(const ufp4_ckpt *c) { return c ? Ckpt{c->codes, c->scales} : Ckpt{nullptr, nullptr}; }
+
+}  // namespace
+
+extern "C" {
+
+ufp4_status ufp4_moe_sort(const void *ids, int32_t id_bytes, const ufp4_moe_plan *plan, ufp4_stream_t stream) {
+    MoePlan m;
+    ufp4_status st = check_plan(plan, &m);
+    if (st != UFP4_OK) return st;
+    if (id_bytes != 4 && id_bytes != 8) return UFP4_ERR_INVALID;
+    if (m.tokens > 0 && (!ids || !aligned(ids, (size_t)id_bytes))) return UFP4_ERR_INVALID;
+    return from_cuda(launch_moe_sort(ids, id_bytes, m, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ufp4_status ufp4_moe_dispatch(const void *x, int32_t dtype, int64_t hidden, int64_t ld_x, const ufp4_moe_plan *plan,
+                              void *xs, int64_t ld_xs, ufp4_stream_t stream) {
+    MoePlan m;
+    ufp4_status st = check_plan(plan, &m);
+    if (st != UFP4_OK) return st;
+    const int64_t n = m.tokens * m.topk;
+    if (!valid_rows(x, dtype, m.tokens, hidden, ld_x) || !valid_rows(xs, dtype, n, hidden, ld_xs))
+        return UFP4_ERR_INVALID;
+    if (!rows_within_limits(n, hidden, std::max(ld_x, ld_xs))) return UFP4_ERR_UNSUPPORTED;
+    if (n == 0 || hidden == 0) return UFP4_OK;
+    return from_cuda(
+        launch_moe_dispatch(x, dtype, hidden, ld_x, m, xs, ld_xs, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ufp4_status ufp4_moe_combine(const void *y, int32_t y_dtype, int64_t hidden, int64_t ld_y, const ufp4_moe_plan *plan,
+                             const float *weights, void *out, int32_t out_dtype, int64_t ld_out,
+                             ufp4_stream_t stream) {
+    MoePlan m;
+    ufp4_status st = check_plan(plan, &m);
+    if (st != UFP4_OK) return st;
+    const int64_t n = m.tokens * m.topk;
+    if (!valid_rows(y, y_dtype, n, hidden, ld_y) || !valid_rows(out, out_dtype, m.tokens, hidden, ld_out))
+        return UFP4_ERR_INVALID;
+    if (weights && !aligned(weights, 4)) return UFP4_ERR_INVALID;
+    if (!rows_within_limits(n, hidden, std::max(ld_y, ld_out))) return UFP4_ERR_UNSUPPORTED;
+    if (n == 0 || hidden == 0) return UFP4_OK;
+    return from_cuda(launch_moe_combine(y, y_dtype, hidden, ld_y, m, weights, out, out_dtype, ld_out,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ufp4_status ufp4_moe_combine_bwd(const void *dout, int32_t dout_dtype, int64_t ld_dout, const void *y,
+                                 int32_t y_dtype, int64_t ld_y, int64_t hidden, const ufp4_moe_plan *plan,
+                                 const float *weights, void *dy, int32_t dy_dtype, int64_t ld_dy, float *dw,
+                                 ufp4_stream_t stream) {
+    MoePlan m;
+    ufp4_status st = check_plan(plan, &m);
+    if (st != UFP4_OK) return st;
+    const int64_t n = m.tokens * m.topk;
+    if (!valid_rows(dout, dout_dtype, m.tokens, hidden, ld_dout) || !valid_rows(y, y_dtype, n, hidden, ld_y) ||
+        !valid_rows(dy, dy_dtype, n, hidden, ld_dy))
+        return UFP4_ERR_INVALID;
+    if (n > 0 && (!weights || !dw || !aligned(weights, 4) || !aligned(dw, 4))) return UFP4_ERR_INVALID;
+    if (!rows_within_limits(n, hidden, std::max({ld_dout, ld_y, ld_dy}))) return UFP4_ERR_UNSUPPORTED;
+    if (n == 0) return UFP4_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (hidden == 0) return from_cuda(cudaMemsetAsync(dw, 0, (size_t)n * sizeof(float), s));
+    return from_cuda(launch_moe_combine_bwd(dout, dout_dtype, ld_dout, y, y_dtype, ld_y, hidden, m, weights, dy,
+                                            dy_dtype, ld_dy, dw, s));
+}
+
+int64_t ufp4_ckpt_ld(int64_t cols) { return cols <= 0 ? 0 : ckpt_ld(cols); }
+
+int64_t ufp4_ckpt_codes_bytes(int64_t rows, int64_t cols) { return rows <= 0 || cols <= 0 ? 0 : rows * ckpt_ld(cols); }
+
+int64_t ufp4_ckpt_scales_bytes(int64_t rows, int64_t cols) {
+    return rows <= 0 || cols <= 0 ? 0 : rows * ((cols + UFP4_CKPT_BLOCK - 1) / UFP4_CKPT_BLOCK);
+}
+
+ufp4_status ufp4_ckpt_save(const void *x, int32_t dtype, int64_t ld, const ufp4_ckpt *out, ufp4_stream_t stream) {
+    if (!valid_ckpt(out) || !valid_rows(x, dtype, out->rows, out->cols, ld)) return UFP4_ERR_INVALID;
+    if (!rows_within_limits(out->rows, out->cols, ld)) return UFP4_ERR_UNSUPPORTED;
+    if (out->rows == 0 || out->cols == 0) return UFP4_OK;
+    return from_cuda(launch_ckpt_save(x, dtype, ld, ckpt_of(out), out->format, out->rows, out->cols,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ufp4_status ufp4_ckpt_load(const ufp4_ckpt *c, void *x, int32_t dtype, int64_t ld, ufp4_stream_t stream) {
+    if (!valid_ckpt(c) || !valid_rows(x, dtype, c->rows, c->cols, ld)) return UFP4_ERR_INVALID;
+    if (!rows_within_limits(c->rows, c->cols, ld)) return UFP4_ERR_UNSUPPORTED;
+    if (c->rows == 0 || c->cols == 0) return UFP4_OK;
+    return from_cuda(launch_ckpt_load(ckpt_of(c), c->format, c->rows, c->cols, x, dtype, ld,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ufp4_status ufp4_swiglu(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int32_t in_dtype,
+                        int64_t rows, int64_t cols, void *h, int32_t h_dtype, int64_t ld_h,
+                        const ufp4_ckpt *keep_gate, const ufp4_ckpt *keep_up, ufp4_stream_t stream) {
+    if (!valid_rows(gate, in_dtype, rows, cols, ld_gate) || !valid_rows(up, in_dtype, rows, cols, ld_up) ||
+        !valid_rows(h, h_dtype, rows, cols, ld_h))
+        return UFP4_ERR_INVALID;
+    if (!keep_gate != !keep_up) return UFP4_ERR_INVALID;
+    for (const ufp4_ckpt *c : {keep_gate, keep_up})
+        if (c && (!valid_ckpt(c) || c->rows != rows || c->cols != cols)) return UFP4_ERR_INVALID;
+    if (keep_gate && keep_gate->format != keep_up->format) return UFP4_ERR_INVALID;
+    if (!rows_within_limits(rows, cols, std::max({ld_gate, ld_up, ld_h}))) return UFP4_ERR_UNSUPPORTED;
+    if (rows == 0 || cols == 0) return UFP4_OK;
+    return from_cuda(launch_swiglu(gate, ld_gate, up, ld_up, in_dtype, rows, cols, h, h_dtype, ld_h,
+                                   ckpt_of(keep_gate), ckpt_of(keep_up), keep_gate ? keep_gate->format : -1,
+                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ufp4_status ufp4_swiglu_bwd(const void *dh, int32_t dh_dtype, int64_t ld_dh, const ufp4_ckpt *gate,
+                            const ufp4_ckpt *up, void *dgate, int64_t ld_dgate, void *dup, int64_t ld_dup,
+                            int32_t out_dtype, ufp4_stream_t stream) {
+    if (!valid_ckpt(gate) || !valid_ckpt(up)) return UFP4_ERR_INVALID;
+    if (gate->rows != up->rows || gate->cols != up->cols || gate->format != up->format) return UFP4_ERR_INVALID;
+    const int64_t rows = gate->rows, cols = gate->cols;
+    if (!valid_rows(dh, dh_dtype, rows, cols, ld_dh) || !valid_rows(dgate, out_dtype, rows, cols, ld_dgate) ||
+        !valid_rows(dup, out_dtype, rows, cols, ld_dup))
+        return UFP4_ERR_INVALID;
+    if (!rows_within_limits(rows, cols, std::max({ld_dh, ld_dgate, ld_dup}))) return UFP4_ERR_UNSUPPORTED;
+    if (rows == 0 || cols == 0) return UFP4_OK;
+    return from_cuda(launch_swiglu_bwd(dh, dh_dtype, ld_dh, ckpt_of(gate), ckpt_of(up), gate->format, rows, cols,
+                                       dgate, ld_dgate, dup, ld_dup, out_dtype,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
 // ---------------------------------------------------------------------------
 // ufp4_quantize_noalloc: ufp4_quantize for callers that cannot allocate
 // device memory.  Some host programs may not call cudaMalloc at the point

@@ -129,6 +129,43 @@ cudaError_t launch_gemm(const uint8_t *a_codes, const uint8_t *a_eplane, const u
                         float *c, int64_t ldc, cudaStream_t s, float *c_amax = nullptr, int amax_rht = 0,
                         uint64_t amax_seed = 0);
 
+// The plan of a routed batch (ufp4_moe_plan, validated).
+struct MoePlan {
+    int32_t *pos, *src;
+    int64_t *counts, *offsets;
+    int64_t tokens;
+    int topk, n_experts;
+};
+
+// tokens * topk < 2^31; the others' sizes are positive and within the limits
+// of include/ufp4.h.  dtype arguments: 0 bf16, 1 fp32.
+cudaError_t launch_moe_sort(const void *ids, int id_bytes, const MoePlan &m, cudaStream_t s);
+cudaError_t launch_moe_dispatch(const void *x, int dtype, int64_t hidden, int64_t ld_x, const MoePlan &m, void *xs,
+                                int64_t ld_xs, cudaStream_t s);
+cudaError_t launch_moe_combine(const void *y, int y_dtype, int64_t hidden, int64_t ld_y, const MoePlan &m,
+                               const float *weights, void *out, int out_dtype, int64_t ld_out, cudaStream_t s);
+cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_dout, const void *y, int y_dtype,
+                                   int64_t ld_y, int64_t hidden, const MoePlan &m, const float *weights, void *dy,
+                                   int dy_dtype, int64_t ld_dy, float *dw, cudaStream_t s);
+
+// 8-bit checkpoints (ufp4_ckpt, validated): codes [rows][ckpt_ld(cols)],
+// scales [rows][ceil(cols / 32)]; fmt 0 INT8, 1 E4M3.
+inline int64_t ckpt_ld(int64_t cols) { return (cols + 15) / 16 * 16; }
+struct Ckpt {
+    uint8_t *codes, *scales;
+};
+cudaError_t launch_ckpt_save(const void *x, int dtype, int64_t ld, const Ckpt &c, int fmt, int64_t rows, int64_t cols,
+                             cudaStream_t s);
+cudaError_t launch_ckpt_load(const Ckpt &c, int fmt, int64_t rows, int64_t cols, void *x, int dtype, int64_t ld,
+                             cudaStream_t s);
+// fmt -1: no checkpoints.
+cudaError_t launch_swiglu(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int in_dtype,
+                          int64_t rows, int64_t cols, void *h, int h_dtype, int64_t ld_h, const Ckpt &cg,
+                          const Ckpt &cu, int fmt, cudaStream_t s);
+cudaError_t launch_swiglu_bwd(const void *dh, int dh_dtype, int64_t ld_dh, const Ckpt &cg, const Ckpt &cu, int fmt,
+                              int64_t rows, int64_t cols, void *dgate, int64_t ld_dgate, void *dup, int64_t ld_dup,
+                              int out_dtype, cudaStream_t s);
+
 // Reads and clears the sticky flag that a bounded device-side wait raises
 // when it gives up (synchronises s).
 cudaError_t read_timeout_flag(uint32_t *flag, cudaStream_t s);

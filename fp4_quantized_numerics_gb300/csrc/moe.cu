@@ -1,0 +1,280 @@
+// moe.cu -- tokens into expert order and back, for the grouped GEMMs of an
+// MoE layer ([HP] hotpaper.ai card, technical approach: MoE 7.9B and 124B
+// models; the pages give no kernels for this).  The contract is in
+// include/ufp4.h.
+//
+// Every kernel but the sort moves each row element once, so bytes bound them;
+// the sort moves 16 bytes a slot and is bound by its steps' latency.
+#include "common.cuh"
+#include "internal.h"
+#include "rowops.cuh"
+
+#include <algorithm>
+
+namespace ufp4 {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------- sort
+// Stable counting sort of n expert ids (bucket E = dropped) by one CTA.
+// Warp w owns a contiguous range of slots.  First pass: a histogram per warp
+// in shared memory.  Its exclusive sums over (expert, warp) are each warp's
+// first place for each expert.  Second pass: a warp takes 32 slots at a time;
+// lanes of one expert find each other by __match_any_sync, and a lane's place
+// is the warp's running place plus the number of such lanes before it.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+
+template <class Id>
+__device__ __forceinline__ uint32_t bucket_of(const Id *ids, uint32_t i, uint32_t E) {
+    const Id id = __ldg(ids + i);
+    return id >= 0 && id < (Id)E ? (uint32_t)id : E;
+}
+
+template <class Id>
+__global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32_t n, uint32_t E, int32_t *pos,
+                                                           int32_t *src, int64_t *counts, int64_t *offsets) {
+    extern __shared__ uint32_t hist[];   // [kSortWarps][E + 1]
+    __shared__ uint32_t warp_sum[kSortWarps];
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, B = E + 1;
+    const uint32_t per = ((n + kSortThreads - 1) / kSortThreads) * 32;   // slots of a warp
+    const uint32_t lo = min(n, warp * per), hi = min(n, lo + per);
+    uint32_t *mine = hist + warp * B;
+
+    for (uint32_t i = tid; i < kSortWarps * B; i += kSortThreads) hist[i] = 0;
+    __syncthreads();
+    for (uint32_t i = lo + lane; i < hi; i += 32) atomicAdd(mine + bucket_of(ids, i, E), 1u);
+    __syncthreads();
+
+    // thread e: sum of bucket e over the warps, then its exclusive sum over e
+    uint32_t total = 0;
+    if (tid < B)
+        for (uint32_t w = 0; w < kSortWarps; ++w) total += hist[w * B + tid];
+    uint32_t incl = total;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= (uint32_t)d) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    uint32_t first = incl - total;
+    for (uint32_t w = 0; w < warp; ++w) first += warp_sum[w];
+    if (tid < B) {
+        offsets[tid] = first;
+        if (tid < E) counts[tid] = total;
+        for (uint32_t w = 0; w < kSortWarps; ++w) {
+            const uint32_t c = hist[w * B + tid];
+            hist[w * B + tid] = first;
+            first += c;
+        }
+    }
+    __syncthreads();
+
+    for (uint32_t base = lo; base < hi; base += 32) {
+        const uint32_t i = base + lane;
+        const bool in = i < hi;
+        const uint32_t b = in ? bucket_of(ids, i, E) : 0xFFFFFFFFu;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, b);
+        const uint32_t before = __popc(same & ((1u << lane) - 1u));
+        uint32_t p = 0;
+        if (in) p = mine[b] + before;
+        __syncwarp();
+        if (in && before == 0) mine[b] = p + __popc(same);
+        __syncwarp();
+        if (in) {
+            pos[i] = (int32_t)p;
+            src[p] = (int32_t)i;
+        }
+    }
+}
+
+// --------------------------------------------------------------- dispatch
+// One thread per `Unit` (16 bytes, or one element where rows are not 16-byte
+// aligned) of a token's row: read once, written topk times.
+template <class Unit>
+__global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *x, int64_t ld_x, Unit *xs, int64_t ld_xs,
+                                                           const int32_t *pos, const int64_t *routed_at, int topk,
+                                                           RowDiv units, uint64_t work) {
+    const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= work) return;
+    const uint64_t t = row_of(i, units);
+    const uint32_t u = (uint32_t)(i - t * units.d);
+    const Unit v = x[t * ld_x + u];
+    const int32_t routed = (int32_t)__ldg(routed_at);
+    const int32_t *at = pos + t * topk;
+    for (int j = 0; j < topk; ++j) {
+        const int32_t p = __ldg(at + j);
+        xs[(int64_t)p * ld_xs + u] = p < routed ? v : Unit{};
+    }
+}
+
+// ---------------------------------------------------------------- combine
+// One thread per V elements of an output row; the topk rows are added in
+// ascending order of choice, in fp32.
+template <class Ty, class To, int V>
+__global__ void __launch_bounds__(kThreads) k_moe_combine(const Ty *y, int64_t ld_y, const int32_t *pos,
+                                                          const float *weights, const int64_t *routed_at, To *out,
+                                                          int64_t ld_out, int topk, RowDiv units, uint64_t work) {
+    const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= work) return;
+    const uint64_t t = row_of(i, units);
+    const uint32_t c = (uint32_t)(i - t * units.d) * V;
+    const int32_t routed = (int32_t)__ldg(routed_at);
+    float acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+    for (int j = 0; j < topk; ++j) {
+        const int32_t p = __ldg(pos + t * topk + j);
+        if (p >= routed) continue;
+        const float w = weights ? __ldg(weights + t * topk + j) : 1.0f;
+        float v[V];
+        load_f32<V>(y + (int64_t)p * ld_y + c, v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+    }
+    store_f32<V>(out + t * ld_out + c, acc);
+}
+
+// ------------------------------------------------------ combine's gradient
+// One warp per token: it reads dout's row once per kChoices choices, writes
+// the scaled copies and keeps the choices' dot products in registers.
+constexpr int kChoices = 8;
+
+template <class Td, class Ty, class To, int V>
+__global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(const Td *dout, int64_t ld_dout, const Ty *y,
+                                                              int64_t ld_y, const int32_t *pos, const float *weights,
+                                                              const int64_t *routed_at, To *dy, int64_t ld_dy,
+                                                              float *dw, int topk, uint32_t hidden, uint32_t tokens) {
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (t >= tokens) return;
+    const int32_t routed = (int32_t)__ldg(routed_at);
+    for (int j0 = 0; j0 < topk; j0 += kChoices) {
+        int32_t p[kChoices];
+        float w[kChoices], dot[kChoices];
+#pragma unroll
+        for (int j = 0; j < kChoices; ++j) {
+            const bool in = j0 + j < topk;
+            p[j] = in ? __ldg(pos + (int64_t)t * topk + j0 + j) : -1;
+            w[j] = in && p[j] < routed ? __ldg(weights + (int64_t)t * topk + j0 + j) : 0.0f;
+            dot[j] = 0.0f;
+        }
+        for (uint32_t c = lane * V; c < hidden; c += 32 * V) {
+            float d[V];
+            load_f32<V>(dout + (int64_t)t * ld_dout + c, d);
+#pragma unroll
+            for (int j = 0; j < kChoices; ++j) {
+                if (p[j] < 0) continue;
+                float o[V];
+                if (p[j] < routed) {
+                    float v[V];
+                    load_f32<V>(y + (int64_t)p[j] * ld_y + c, v);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        o[e] = w[j] * d[e];
+                        dot[j] = fmaf(d[e], v[e], dot[j]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o[e] = 0.0f;
+                }
+                store_f32<V>(dy + (int64_t)p[j] * ld_dy + c, o);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kChoices; ++j) {
+#pragma unroll
+            for (int m = 16; m; m >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], m);
+            if (lane == 0 && p[j] >= 0) dw[(int64_t)t * topk + j0 + j] = dot[j];
+        }
+    }
+}
+
+inline uint64_t ctas(uint64_t work) { return (work + kThreads - 1) / kThreads; }
+
+template <class Unit>
+void dispatch(const void *x, int64_t ldx, void *xs, int64_t ldxs, int64_t row_bytes, const MoePlan &m,
+              cudaStream_t s) {
+    const uint32_t units = (uint32_t)(row_bytes / sizeof(Unit));
+    const uint64_t work = (uint64_t)m.tokens * units;
+    k_moe_dispatch<Unit><<<(unsigned)ctas(work), kThreads, 0, s>>>(
+        static_cast<const Unit *>(x), ldx / (int64_t)sizeof(Unit), static_cast<Unit *>(xs),
+        ldxs / (int64_t)sizeof(Unit), m.pos, m.offsets + m.n_experts, m.topk, make_rowdiv(units), work);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_sort(const void *ids, int id_bytes, const MoePlan &m, cudaStream_t s) {
+    const uint32_t n = (uint32_t)(m.tokens * m.topk);
+    const size_t smem = (size_t)kSortWarps * (m.n_experts + 1) * sizeof(uint32_t);
+    if (id_bytes == 4)
+        k_moe_sort<int32_t><<<1, kSortThreads, smem, s>>>(static_cast<const int32_t *>(ids), n, m.n_experts, m.pos,
+                                                          m.src, m.counts, m.offsets);
+    else
+        k_moe_sort<int64_t><<<1, kSortThreads, smem, s>>>(static_cast<const int64_t *>(ids), n, m.n_experts, m.pos,
+                                                          m.src, m.counts, m.offsets);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_moe_dispatch(const void *x, int dtype, int64_t hidden, int64_t ld_x, const MoePlan &m, void *xs,
+                                int64_t ld_xs, cudaStream_t s) {
+    const int64_t esz = dtype == 0 ? 2 : 4, row = hidden * esz;
+    const uint64_t all = (uint64_t)(uintptr_t)x | (uint64_t)(uintptr_t)xs | (uint64_t)(ld_x * esz) |
+                         (uint64_t)(ld_xs * esz) | (uint64_t)row;
+    if (all % 16 == 0) dispatch<uint4>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
+    else if (esz == 4) dispatch<uint32_t>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
+    else dispatch<uint16_t>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_moe_combine(const void *y, int y_dtype, int64_t hidden, int64_t ld_y, const MoePlan &m,
+                               const float *weights, void *out, int out_dtype, int64_t ld_out, cudaStream_t s) {
+    const bool v8 = vec8(y, ld_y, hidden, y_dtype ? 4 : 2) && vec8(out, ld_out, hidden, out_dtype ? 4 : 2);
+    const uint32_t units = (uint32_t)(v8 ? hidden / 8 : hidden);
+    const uint64_t work = (uint64_t)m.tokens * units;
+    auto go = [&](auto *yp, auto *op, auto v) {
+        using Ty = std::remove_pointer_t<decltype(yp)>;
+        using To = std::remove_pointer_t<decltype(op)>;
+        k_moe_combine<Ty, To, decltype(v)::value><<<(unsigned)ctas(work), kThreads, 0, s>>>(
+            static_cast<const Ty *>(y), ld_y, m.pos, weights, m.offsets + m.n_experts, static_cast<To *>(out), ld_out,
+            m.topk, make_rowdiv(units), work);
+    };
+    by_type(y_dtype, [&](auto *yp) {
+        by_type(out_dtype, [&](auto *op) {
+            if (v8) go(yp, op, std::integral_constant<int, 8>());
+            else go(yp, op, std::integral_constant<int, 1>());
+        });
+    });
+    return cudaGetLastError();
+}
+
+cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_dout, const void *y, int y_dtype,
+                                   int64_t ld_y, int64_t hidden, const MoePlan &m, const float *weights, void *dy,
+                                   int dy_dtype, int64_t ld_dy, float *dw, cudaStream_t s) {
+    const bool v8 = vec8(dout, ld_dout, hidden, dout_dtype ? 4 : 2) && vec8(y, ld_y, hidden, y_dtype ? 4 : 2) &&
+                    vec8(dy, ld_dy, hidden, dy_dtype ? 4 : 2);
+    const unsigned grid = (unsigned)((m.tokens + kThreads / 32 - 1) / (kThreads / 32));
+    auto go = [&](auto *dp, auto *yp, auto *op, auto v) {
+        using Td = std::remove_pointer_t<decltype(dp)>;
+        using Ty = std::remove_pointer_t<decltype(yp)>;
+        using To = std::remove_pointer_t<decltype(op)>;
+        k_moe_combine_bwd<Td, Ty, To, decltype(v)::value><<<grid, kThreads, 0, s>>>(
+            static_cast<const Td *>(dout), ld_dout, static_cast<const Ty *>(y), ld_y, m.pos, weights,
+            m.offsets + m.n_experts, static_cast<To *>(dy), ld_dy, dw, m.topk, (uint32_t)hidden, (uint32_t)m.tokens);
+    };
+    by_type(dout_dtype, [&](auto *dp) {
+        by_type(y_dtype, [&](auto *yp) {
+            by_type(dy_dtype, [&](auto *op) {
+                if (v8) go(dp, yp, op, std::integral_constant<int, 8>());
+                else go(dp, yp, op, std::integral_constant<int, 1>());
+            });
+        });
+    });
+    return cudaGetLastError();
+}
+
+}  // namespace ufp4

@@ -11,6 +11,9 @@ The functions carry the C names:
   ufp4_gemm(a, b, ...)        -> fp32 tensor (C = A B^T)
   ufp4_stats(x, q, ...)       -> dict
   ufp4_check(...), ufp4_status_string(...)
+  ufp4_moe_sort(ids, n_experts) -> MoePlan;  ufp4_moe_dispatch / _combine / _combine_bwd
+  ufp4_ckpt_save(x, fmt) -> Ckpt;  ufp4_ckpt_load(c) -> tensor
+  ufp4_swiglu(gate, up, ...)  -> (h, Ckpt, Ckpt);  ufp4_swiglu_bwd(dh, ...) -> (dgate, dup)
 """
 import ctypes
 import os
@@ -24,6 +27,8 @@ UFP4_E2M1, UFP4_E1M2, UFP4_E2M1C, UFP4_MXFP4 = 0, 1, 2, 3
 UFP4_BLOCK, UFP4_MX_BLOCK = 16, 32
 UFP4_RTNE, UFP4_SR = 0, 1
 UFP4_BF16, UFP4_FP32 = 0, 1
+UFP4_CKPT_INT8, UFP4_CKPT_E4M3 = 0, 1
+UFP4_CKPT_BLOCK = 32
 UFP4_OK, UFP4_ERR_INVALID, UFP4_ERR_UNSUPPORTED, UFP4_ERR_NONFINITE, UFP4_ERR_CUDA, \
     UFP4_ERR_TIMEOUT = range(6)
 
@@ -31,7 +36,10 @@ EXPORTED = ["ufp4_kpad", "ufp4_codes_bytes", "ufp4_scales_bytes", "ufp4_workspac
             "ufp4_quantize", "ufp4_check", "ufp4_dequantize", "ufp4_gemm", "ufp4_stats",
             "ufp4_status_string", "ufp4_quantize_noalloc", "ufp4_grouped_rows",
             "ufp4_grouped_kpad", "ufp4_quantize_grouped", "ufp4_gemm_grouped", "ufp4_quantize_dual",
-            "ufp4_gemm_amax", "ufp4_quantize_stats", "ufp4_quantize_grouped_dual"]
+            "ufp4_gemm_amax", "ufp4_quantize_stats", "ufp4_quantize_grouped_dual", "ufp4_moe_sort",
+            "ufp4_moe_dispatch", "ufp4_moe_combine", "ufp4_moe_combine_bwd", "ufp4_ckpt_ld",
+            "ufp4_ckpt_codes_bytes", "ufp4_ckpt_scales_bytes", "ufp4_ckpt_save", "ufp4_ckpt_load",
+            "ufp4_swiglu", "ufp4_swiglu_bwd"]
 
 
 class QParamsC(ctypes.Structure):
@@ -59,6 +67,17 @@ class GemmGroupC(ctypes.Structure):
                 ("a_row", ctypes.c_int64), ("a_k", ctypes.c_int64), ("b_row", ctypes.c_int64),
                 ("b_k", ctypes.c_int64), ("a_seg", ctypes.c_int32), ("b_seg", ctypes.c_int32),
                 ("c", ctypes.c_void_p), ("ldc", ctypes.c_int64)]
+
+
+class MoePlanC(ctypes.Structure):
+    _fields_ = [("pos", ctypes.c_void_p), ("src", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("topk", ctypes.c_int32),
+                ("n_experts", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class CkptC(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("format", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class UFP4Error(RuntimeError):
@@ -128,6 +147,22 @@ def lib():
         L.ufp4_gemm_grouped.argtypes = [ctypes.POINTER(QTensorC), ctypes.POINTER(QTensorC),
                                         ctypes.POINTER(GemmGroupC), ctypes.c_int32, vp]
         L.ufp4_gemm_grouped.restype = ctypes.c_int
+        i32, plan, ck = ctypes.c_int32, ctypes.POINTER(MoePlanC), ctypes.POINTER(CkptC)
+        for name, args in (
+                ("ufp4_moe_sort", [vp, i32, plan, vp]),
+                ("ufp4_moe_dispatch", [vp, i32, i64, i64, plan, vp, i64, vp]),
+                ("ufp4_moe_combine", [vp, i32, i64, i64, plan, vp, vp, i32, i64, vp]),
+                ("ufp4_moe_combine_bwd", [vp, i32, i64, vp, i32, i64, i64, plan, vp, vp, i32, i64, vp, vp]),
+                ("ufp4_ckpt_save", [vp, i32, i64, ck, vp]),
+                ("ufp4_ckpt_load", [ck, vp, i32, i64, vp]),
+                ("ufp4_swiglu", [vp, i64, vp, i64, i32, i64, i64, vp, i32, i64, ck, ck, vp]),
+                ("ufp4_swiglu_bwd", [vp, i32, i64, ck, ck, vp, i64, vp, i64, i32, vp])):
+            f = getattr(L, name)
+            f.argtypes, f.restype = args, ctypes.c_int
+        for name, args in (("ufp4_ckpt_ld", [i64]), ("ufp4_ckpt_codes_bytes", [i64, i64]),
+                           ("ufp4_ckpt_scales_bytes", [i64, i64])):
+            f = getattr(L, name)
+            f.argtypes, f.restype = args, i64
         L.ufp4_status_string.argtypes = [ctypes.c_int]
         L.ufp4_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -447,3 +482,202 @@ def ufp4_gemm_grouped(a, b, groups, stream=None):
     ac, bc = a.c(), b.c()
     st = lib().ufp4_gemm_grouped(ctypes.byref(ac), ctypes.byref(bc), arr, len(groups), _stream(stream))
     _check(st, "ufp4_gemm_grouped")
+
+
+# ------------------------------------------- around the grouped GEMMs (MoE)
+class MoePlan:
+    """Expert order of a routed batch (layouts: include/ufp4.h): pos int32
+    [tokens, topk], src int32 [tokens * topk], counts int64 [n_experts],
+    offsets int64 [n_experts + 1].  counts.tolist() is the seg_rows of the
+    grouped calls; rows past offsets[-1] belong to dropped slots."""
+
+    def __init__(self, pos, src, counts, offsets):
+        for t, name, dtype, n in ((pos, "pos", torch.int32, pos.numel()), (src, "src", torch.int32, pos.numel()),
+                                  (counts, "counts", torch.int64, counts.numel()),
+                                  (offsets, "offsets", torch.int64, counts.numel() + 1)):
+            _cuda(t, name)
+            if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+                raise ValueError("%s must be contiguous, %s, of %d elements" % (name, dtype, n))
+        if pos.dim() != 2:
+            raise ValueError("pos must be [tokens, topk]")
+        self.pos, self.src, self.counts, self.offsets = pos, src, counts, offsets
+        self.tokens, self.topk = pos.shape
+        self.n_experts = counts.numel()
+        self._c = MoePlanC(pos.data_ptr(), src.data_ptr(), counts.data_ptr(), offsets.data_ptr(), self.tokens,
+                           self.topk, self.n_experts, 0)
+
+    @classmethod
+    def empty(cls, tokens, topk, n_experts, device="cuda"):
+        new = lambda n, dtype: torch.empty(n, dtype=dtype, device=device)  # noqa: E731
+        return cls(new((tokens, topk), torch.int32), new(tokens * topk, torch.int32), new(n_experts, torch.int64),
+                   new(n_experts + 1, torch.int64))
+
+    def c(self):
+        return ctypes.byref(self._c)
+
+
+def _rows2d(t, name, rows=None, cols=None):
+    """A 2-D CUDA tensor with unit stride in its last dim, of the given shape."""
+    _cuda(t, name)
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError("%s must be 2-D with unit stride in its last dim" % name)
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError("%s must be %s x %s, got %d x %d" % (name, rows, cols, *t.shape))
+    return t
+
+
+def _ld(t):
+    # the stride of a one-row tensor says nothing; the C call wants ld >= cols
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _result(out, name, rows, cols, dtype, device):
+    if out is None:
+        return torch.empty(rows, cols, dtype=dtype, device=device)
+    return _rows2d(out, name, rows, cols)
+
+
+def _plan_weights(weights, plan):
+    _cuda(weights, "weights")
+    if weights.dtype != torch.float32 or tuple(weights.shape) != (plan.tokens, plan.topk) or \
+            not weights.is_contiguous():
+        raise ValueError("weights must be contiguous fp32 [tokens, topk]")
+    return weights.data_ptr()
+
+
+def ufp4_moe_sort(ids, n_experts, out=None, stream=None):
+    """Stable sort of the slots of ids ([tokens, topk], int32 or int64) by
+    expert; ids outside [0, n_experts) are dropped.  Returns a MoePlan."""
+    _cuda(ids, "ids")
+    if ids.dim() != 2 or not ids.is_contiguous():
+        raise ValueError("ids must be contiguous [tokens, topk]")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
+    if out is None:
+        out = MoePlan.empty(ids.shape[0], ids.shape[1], n_experts, ids.device)
+    elif (out.tokens, out.topk, out.n_experts) != (*ids.shape, n_experts):
+        raise ValueError("out is a plan of another size")
+    st = lib().ufp4_moe_sort(ids.data_ptr(), ids.element_size(), out.c(), _stream(stream))
+    _check(st, "ufp4_moe_sort")
+    return out
+
+
+def ufp4_moe_dispatch(x, plan, out=None, stream=None):
+    """x ([tokens, hidden]) in expert order: [tokens * topk, hidden], dropped
+    slots' rows (the last ones) zero.  Gradient: ufp4_moe_combine(dxs, plan)."""
+    _rows2d(x, "x", plan.tokens)
+    out = _result(out, "out", plan.tokens * plan.topk, x.shape[1], x.dtype, x.device)
+    if out.dtype != x.dtype:
+        raise TypeError("out must have x's dtype")
+    st = lib().ufp4_moe_dispatch(x.data_ptr(), _dtype_code(x), x.shape[1], _ld(x), plan.c(), out.data_ptr(),
+                                 _ld(out), _stream(stream))
+    _check(st, "ufp4_moe_dispatch")
+    return out
+
+
+def ufp4_moe_combine(y, plan, weights=None, dtype=None, out=None, stream=None):
+    """y ([tokens * topk, hidden], expert order) back in token order: the sum
+    over each token's routed slots, times weights ([tokens, topk] fp32) if
+    given.  dtype: the result's (y's by default)."""
+    _rows2d(y, "y", plan.tokens * plan.topk)
+    w = None if weights is None else _plan_weights(weights, plan)
+    out = _result(out, "out", plan.tokens, y.shape[1], y.dtype if dtype is None else dtype, y.device)
+    st = lib().ufp4_moe_combine(y.data_ptr(), _dtype_code(y), y.shape[1], _ld(y), plan.c(), w, out.data_ptr(),
+                                _dtype_code(out), _ld(out), _stream(stream))
+    _check(st, "ufp4_moe_combine")
+    return out
+
+
+def ufp4_moe_combine_bwd(dout, y, plan, weights, dtype=None, dy=None, dw=None, stream=None):
+    """Gradients of ufp4_moe_combine(y, plan, weights): (dy, dw).  dtype: dy's
+    (dout's by default)."""
+    _rows2d(y, "y", plan.tokens * plan.topk)
+    _rows2d(dout, "dout", plan.tokens, y.shape[1])
+    w = _plan_weights(weights, plan)
+    dy = _result(dy, "dy", y.shape[0], y.shape[1], dout.dtype if dtype is None else dtype, y.device)
+    if dw is None:
+        dw = torch.empty(plan.tokens, plan.topk, dtype=torch.float32, device=y.device)
+    st = lib().ufp4_moe_combine_bwd(dout.data_ptr(), _dtype_code(dout), _ld(dout), y.data_ptr(), _dtype_code(y),
+                                    _ld(y), y.shape[1], plan.c(), w, dy.data_ptr(), _dtype_code(dy), _ld(dy),
+                                    _plan_weights(dw, plan), _stream(stream))
+    _check(st, "ufp4_moe_combine_bwd")
+    return dy, dw
+
+
+class Ckpt:
+    """An activation kept in 8 bits (layouts: include/ufp4.h): codes uint8
+    [rows, ufp4_ckpt_ld(cols)], scales uint8 [rows, ceil(cols / 32)]."""
+
+    def __init__(self, codes, scales, rows, cols, format):
+        self.codes, self.scales = codes, scales
+        self.rows, self.cols, self.format = int(rows), int(cols), int(format)
+        self._c = CkptC(codes.data_ptr(), scales.data_ptr(), self.rows, self.cols, self.format, 0)
+
+    @classmethod
+    def empty(cls, rows, cols, format, device="cuda"):
+        codes = torch.empty(rows, (cols + 15) // 16 * 16, dtype=torch.uint8, device=device)
+        scales = torch.empty(rows, (cols + UFP4_CKPT_BLOCK - 1) // UFP4_CKPT_BLOCK, dtype=torch.uint8, device=device)
+        return cls(codes, scales, rows, cols, format)
+
+    def c(self):
+        return ctypes.byref(self._c)
+
+
+def ufp4_ckpt_save(x, format=UFP4_CKPT_INT8, out=None, stream=None):
+    """x (2-D bf16 / fp32) in 8 bits with a power-of-two scale per 32
+    elements of a row.  Returns a Ckpt."""
+    _rows2d(x, "x")
+    if out is None:
+        out = Ckpt.empty(x.shape[0], x.shape[1], format, x.device)
+    elif (out.rows, out.cols, out.format) != (*x.shape, format):
+        raise ValueError("out is a checkpoint of another shape or format")
+    st = lib().ufp4_ckpt_save(x.data_ptr(), _dtype_code(x), _ld(x), out.c(), _stream(stream))
+    _check(st, "ufp4_ckpt_save")
+    return out
+
+
+def ufp4_ckpt_load(c, dtype=torch.bfloat16, out=None, stream=None):
+    """The values of a checkpoint (exact in bf16 and fp32)."""
+    _cuda(c.codes, "c.codes")
+    out = _result(out, "out", c.rows, c.cols, dtype, c.codes.device)
+    st = lib().ufp4_ckpt_load(c.c(), out.data_ptr(), _dtype_code(out), _ld(out), _stream(stream))
+    _check(st, "ufp4_ckpt_load")
+    return out
+
+
+def ufp4_swiglu(gate, up, ckpt=None, dtype=None, out=None, stream=None):
+    """h = silu(gate) * up, and gate's and up's 8-bit checkpoints for the
+    backward pass (ckpt: their format, or None to keep nothing).  Returns
+    (h, keep_gate, keep_up), the latter two None without ckpt.  dtype: h's
+    (gate's by default)."""
+    _rows2d(gate, "gate")
+    rows, cols = gate.shape
+    _rows2d(up, "up", rows, cols)
+    if up.dtype != gate.dtype:
+        raise TypeError("gate and up must have one dtype")
+    out = _result(out, "out", rows, cols, gate.dtype if dtype is None else dtype, gate.device)
+    kg = ku = None
+    if ckpt is not None:
+        kg, ku = Ckpt.empty(rows, cols, ckpt, gate.device), Ckpt.empty(rows, cols, ckpt, gate.device)
+    st = lib().ufp4_swiglu(gate.data_ptr(), _ld(gate), up.data_ptr(), _ld(up), _dtype_code(gate), rows, cols,
+                           out.data_ptr(), _dtype_code(out), _ld(out), None if kg is None else kg.c(),
+                           None if ku is None else ku.c(), _stream(stream))
+    _check(st, "ufp4_swiglu")
+    return out, kg, ku
+
+
+def ufp4_swiglu_bwd(dh, keep_gate, keep_up, dtype=None, dgate=None, dup=None, stream=None):
+    """Gradients of ufp4_swiglu from its checkpoints: (dgate, dup).  dtype:
+    the gradients' (dh's by default)."""
+    rows, cols = keep_gate.rows, keep_gate.cols
+    _rows2d(dh, "dh", rows, cols)
+    dtype = dh.dtype if dtype is None else dtype
+    dgate = _result(dgate, "dgate", rows, cols, dtype, dh.device)
+    dup = _result(dup, "dup", rows, cols, dgate.dtype, dh.device)
+    if dup.dtype != dgate.dtype:
+        raise TypeError("dgate and dup must have one dtype")
+    st = lib().ufp4_swiglu_bwd(dh.data_ptr(), _dtype_code(dh), _ld(dh), keep_gate.c(), keep_up.c(),
+                               dgate.data_ptr(), _ld(dgate), dup.data_ptr(), _ld(dup), _dtype_code(dgate),
+                               _stream(stream))
+    _check(st, "ufp4_swiglu_bwd")
+    return dgate, dup

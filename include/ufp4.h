@@ -399,6 +399,146 @@ UFP4_API ufp4_status ufp4_gemm_grouped(const ufp4_qtensor *a, const ufp4_qtensor
                                        const ufp4_gemm_group *groups, int32_t n,
                                        ufp4_stream_t stream);
 
+/* ---------------------------------------------------------------------
+ * Around the grouped GEMMs of an MoE layer: tokens into expert order, back to
+ * token order with the router's weights, the gated activation between the two
+ * products, and an 8-bit form of the activations the backward pass needs.
+ * The pages train MoE models ([HP] technical approach) and leave these steps
+ * to the training framework; the definitions here are this library's.
+ *
+ * Conventions of the calls in this section, beside those above:
+ *   - Tensors are BF16 or FP32 (`*_dtype`: UFP4_BF16, UFP4_FP32), row-major
+ *     with any row stride >= the row length, in elements, aligned to one
+ *     element.  Rows whose addresses and strides are multiples of 16 bytes
+ *     (and of 8 elements) take the fast path; results are the same.
+ *   - Arithmetic is fp32; each result element is rounded once, when written.
+ *   - Inputs and outputs must not overlap.
+ *   - hidden / cols <= UFP4_MAX_WIDTH, rows x width < 2^38, rows and
+ *     strides < 2^31; beyond that UFP4_ERR_UNSUPPORTED.
+ *   - Every output element is written; results do not depend on timing (no
+ *     floating-point atomics). */
+#define UFP4_MAX_WIDTH (1LL << 24)
+
+/* Which place of the expert order each routed token has.  A slot is one
+ * (token, choice) pair, slot = token * topk + choice; there are
+ * n = tokens * topk of them.
+ *   pos     : int32 [n], the slot's place in expert order;
+ *   src     : int32 [n], the slot at each place (the inverse of pos);
+ *   counts  : int64 [n_experts], slots of each expert (copied to the host it
+ *             is the seg_rows array of the grouped calls);
+ *   offsets : int64 [n_experts + 1], first place of each expert; the last
+ *             entry is the number of routed slots.
+ * Places offsets[n_experts] .. n-1 belong to dropped slots.  pos and src
+ * 4-byte, counts and offsets 8-byte aligned. */
+typedef struct {
+    int32_t *pos;
+    int32_t *src;
+    int64_t *counts;
+    int64_t *offsets;
+    int64_t tokens;
+    int32_t topk;
+    int32_t n_experts;         /* 1 .. UFP4_MAX_GROUPS */
+    int32_t reserved;          /* must be 0 */
+} ufp4_moe_plan;
+
+/* Sorts the slots by expert: stable (slots of one expert stay in slot order).
+ *   ids : device, [tokens][topk] expert ids, contiguous, int32 (id_bytes 4)
+ *         or int64 (id_bytes 8), aligned to one id.  A slot whose id is
+ *         outside [0, n_experts) is dropped (padding, a full expert): it is
+ *         placed behind all routed ones, also in slot order.
+ * tokens = 0 writes counts and offsets (zeros).  No workspace. */
+UFP4_API ufp4_status ufp4_moe_sort(const void *ids, int32_t id_bytes, const ufp4_moe_plan *plan,
+                                   ufp4_stream_t stream);
+
+/* Tokens into expert order: xs[pos[t * topk + j]] = x[t]; the rows of dropped
+ * slots are written as zeros.  x: tokens x hidden, xs: (tokens * topk) x
+ * hidden, both of `dtype`.  Its gradient, dx[t] = the sum over j of
+ * dxs[pos[t * topk + j]], is ufp4_moe_combine with weights = NULL. */
+UFP4_API ufp4_status ufp4_moe_dispatch(const void *x, int32_t dtype, int64_t hidden, int64_t ld_x,
+                                       const ufp4_moe_plan *plan, void *xs, int64_t ld_xs, ufp4_stream_t stream);
+
+/* Back to token order: out[t] = sum over j of w[t][j] * y[pos[t * topk + j]],
+ * j ascending, over the slots that are not dropped (a dropped slot's row and
+ * weight are not read; a token without routed slots gets zeros).
+ *   y       : (tokens * topk) x hidden of y_dtype;
+ *   weights : fp32 [tokens][topk], contiguous, or NULL for all ones;
+ *   out     : tokens x hidden of out_dtype. */
+UFP4_API ufp4_status ufp4_moe_combine(const void *y, int32_t y_dtype, int64_t hidden, int64_t ld_y,
+                                      const ufp4_moe_plan *plan, const float *weights, void *out,
+                                      int32_t out_dtype, int64_t ld_out, ufp4_stream_t stream);
+
+/* Gradients of ufp4_moe_combine:
+ *   dy[pos[t * topk + j]] = w[t][j] * dout[t], zeros for dropped slots;
+ *   dw[t][j] = sum over the row of dout[t] * y[pos[t * topk + j]], 0 for
+ *              dropped slots.
+ *   dout: tokens x hidden of dout_dtype; y as in the forward call; dy:
+ *   (tokens * topk) x hidden of dy_dtype; dw: fp32 [tokens][topk].  hidden = 0
+ *   writes dw (zeros). */
+UFP4_API ufp4_status ufp4_moe_combine_bwd(const void *dout, int32_t dout_dtype, int64_t ld_dout, const void *y,
+                                          int32_t y_dtype, int64_t ld_y, int64_t hidden,
+                                          const ufp4_moe_plan *plan, const float *weights, void *dy,
+                                          int32_t dy_dtype, int64_t ld_dy, float *dw, ufp4_stream_t stream);
+
+/* 8-bit element formats of a checkpointed activation. */
+typedef enum { UFP4_CKPT_INT8 = 0, UFP4_CKPT_E4M3 = 1 } ufp4_ckpt_format;
+#define UFP4_CKPT_BLOCK 32
+
+/* An activation kept in 8 bits for the backward pass: rows x cols codes, and
+ * one power-of-two scale byte b for every 32 elements of a row (the last
+ * block of a row may be shorter).  Value = code * 2^(b - 127).
+ *   b = max(e - emax, 0) with e the biased exponent of the block's largest
+ *       magnitude; emax = 6 (INT8) or 8 (E4M3), and E4M3 adds 1 to e where
+ *       that magnitude's significand is above 1.75, so that no element
+ *       saturates, but keeps b <= 246, so that every restored value is finite
+ *       in fp32.  An all-zero block has b = 0.
+ *   INT8: code = clamp(rint(x * 2^(127 - b)), -127, 127), ties to even: within
+ *         2^(b-128) of x, or 2^(b-127) where |x| is above 127.5 * 2^(b-127);
+ *   E4M3: code = E4M3 of x * 2^(127 - b), round to nearest even, saturating at
+ *         448 (which only magnitudes above 1.75 * 2^127 reach).
+ *   A block holding a NaN or an infinity has b = 255, codes 0, and is
+ *   restored as NaN throughout: a non-finite activation stays visible.
+ *   codes  : [rows][ufp4_ckpt_ld(cols)] bytes (rows padded to a multiple of
+ *            16; the padding is not written), 16-byte aligned;
+ *   scales : [rows][ceil(cols / 32)] bytes. */
+typedef struct {
+    uint8_t *codes;
+    uint8_t *scales;
+    int64_t rows;
+    int64_t cols;
+    int32_t format;            /* ufp4_ckpt_format */
+    int32_t reserved;          /* must be 0 */
+} ufp4_ckpt;
+
+UFP4_API int64_t ufp4_ckpt_ld(int64_t cols);
+UFP4_API int64_t ufp4_ckpt_codes_bytes(int64_t rows, int64_t cols);
+UFP4_API int64_t ufp4_ckpt_scales_bytes(int64_t rows, int64_t cols);
+
+/* x (out->rows x out->cols of `dtype`) into 8 bits, and back. */
+UFP4_API ufp4_status ufp4_ckpt_save(const void *x, int32_t dtype, int64_t ld, const ufp4_ckpt *out,
+                                    ufp4_stream_t stream);
+UFP4_API ufp4_status ufp4_ckpt_load(const ufp4_ckpt *c, void *x, int32_t dtype, int64_t ld, ufp4_stream_t stream);
+
+/* The gated activation between an expert's two products, h = silu(gate) * up
+ * with silu(g) = g / (1 + exp(-g)), and, from the same read, the 8-bit
+ * checkpoints that ufp4_swiglu_bwd takes.
+ *   gate, up : rows x cols of in_dtype (two halves of one product's output,
+ *              or two tensors; each with its own row stride);
+ *   h        : rows x cols of h_dtype, from the unrounded gate and up;
+ *   keep_gate, keep_up : checkpoints of gate and up (rows x cols, one
+ *              format), or both NULL (no backward pass will follow). */
+UFP4_API ufp4_status ufp4_swiglu(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up,
+                                 int32_t in_dtype, int64_t rows, int64_t cols, void *h, int32_t h_dtype,
+                                 int64_t ld_h, const ufp4_ckpt *keep_gate, const ufp4_ckpt *keep_up,
+                                 ufp4_stream_t stream);
+
+/* Gradients of ufp4_swiglu from the checkpoints: with g and u the restored
+ * gate and up and s = 1 / (1 + exp(-g)),
+ *   dgate = dh * u * s * (1 + g * (1 - s)),   dup = dh * g * s.
+ *   dh: rows x cols of dh_dtype; dgate, dup: rows x cols of out_dtype. */
+UFP4_API ufp4_status ufp4_swiglu_bwd(const void *dh, int32_t dh_dtype, int64_t ld_dh, const ufp4_ckpt *gate,
+                                     const ufp4_ckpt *up, void *dgate, int64_t ld_dgate, void *dup,
+                                     int64_t ld_dup, int32_t out_dtype, ufp4_stream_t stream);
+
 /* Quality of one quantization, in fp64 on the host ([ZC] "The cause",
  * "Compounding decay", "The RHT paradox").  A is the tensor that was
  * quantized (x, rotated when p->rht; transposed when p->colwise):
