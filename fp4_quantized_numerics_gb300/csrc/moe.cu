@@ -10,6 +10,7 @@
 #include "rowops.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace ufp4 {
 
@@ -18,14 +19,43 @@ namespace {
 constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------- sort
-// Stable counting sort of n expert ids (bucket E = dropped) by one CTA.
-// Warp w owns a contiguous range of slots.  First pass: a histogram per warp
-// in shared memory.  Its exclusive sums over (expert, warp) are each warp's
-// first place for each expert.  Second pass: a warp takes 32 slots at a time;
-// lanes of one expert find each other by __match_any_sync, and a lane's place
-// is the warp's running place plus the number of such lanes before it.
+// Stable counting sort of n expert ids (bucket E = dropped) by one cluster.
+// Every warp of the cluster owns a contiguous range of slots, in order.
+//   1. A histogram per warp in shared memory, summed over the CTA's warps.
+//   2. The CTAs read each other's sums over distributed shared memory: a
+//      bucket's first place in the order is the sum of all smaller buckets,
+//      a CTA's the sums of the CTAs before it, a warp's those of the warps
+//      before it.
+//   3. A warp takes 32 slots at a time; lanes of one expert find each other
+//      by one ballot per bit of the expert's number, and a lane's place is
+//      the warp's running place plus the number of such lanes before it.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxSortCtas = 16;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// *p of the cluster's CTA `rank`, p in this CTA's shared memory.
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t *p, uint32_t rank) {
+    uint32_t a, v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(a)
+        : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
 
 template <class Id>
 __device__ __forceinline__ uint32_t bucket_of(const Id *ids, uint32_t i, uint32_t E) {
@@ -33,25 +63,57 @@ __device__ __forceinline__ uint32_t bucket_of(const Id *ids, uint32_t i, uint32_
     return id >= 0 && id < (Id)E ? (uint32_t)id : E;
 }
 
+// The lanes of the warp whose b (of `bits` bits) equals this lane's, among
+// those of `in`.
+__device__ __forceinline__ uint32_t lanes_like(uint32_t b, int bits, bool in) {
+    uint32_t same = __ballot_sync(0xFFFFFFFFu, in);
+    for (int k = 0; k < bits; ++k) {
+        const bool set = (b >> k) & 1u;
+        const uint32_t v = __ballot_sync(0xFFFFFFFFu, set);
+        same &= set ? v : ~v;
+    }
+    return same;
+}
+
 template <class Id>
 __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32_t n, uint32_t E, int32_t *pos,
                                                            int32_t *src, int64_t *counts, int64_t *offsets) {
-    extern __shared__ uint32_t hist[];   // [kSortWarps][E + 1]
+    __shared__ uint32_t hist[kSortWarps * (kMaxGroups + 1)];   // [warp][bucket]
+    __shared__ uint32_t sums[kMaxGroups + 1];                  // this CTA's, read by the others
     __shared__ uint32_t warp_sum[kSortWarps];
-    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, B = E + 1;
-    const uint32_t per = ((n + kSortThreads - 1) / kSortThreads) * 32;   // slots of a warp
-    const uint32_t lo = min(n, warp * per), hi = min(n, lo + per);
+    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, B = E + 1, W = blockDim.x / 32;
+    const uint32_t rank = cluster_rank(), nctas = cluster_size();
+    const uint32_t warps = nctas * W;
+    const int bits = 32 - __clz((int)E);
+    const uint32_t per = (n / warps + 31u) / 32u * 32u + 32u;   // slots of a warp: warps * per >= n, a multiple of 32
+    const uint32_t lo = (uint32_t)min((uint64_t)n, (uint64_t)(rank * W + warp) * per), hi = min(n, lo + per);
     uint32_t *mine = hist + warp * B;
 
-    for (uint32_t i = tid; i < kSortWarps * B; i += kSortThreads) hist[i] = 0;
+    for (uint32_t i = tid; i < W * B; i += blockDim.x) hist[i] = 0;
     __syncthreads();
+#pragma unroll 4
     for (uint32_t i = lo + lane; i < hi; i += 32) atomicAdd(mine + bucket_of(ids, i, E), 1u);
     __syncthreads();
 
-    // thread e: sum of bucket e over the warps, then its exclusive sum over e
-    uint32_t total = 0;
-    if (tid < B)
-        for (uint32_t w = 0; w < kSortWarps; ++w) total += hist[w * B + tid];
+    if (tid < B) {
+        uint32_t t = 0;
+#pragma unroll 8
+        for (uint32_t w = 0; w < W; ++w) t += hist[w * B + tid];
+        sums[tid] = t;
+    }
+    cluster_arrive();
+    cluster_wait();
+    uint32_t total = 0, before_me = 0;
+    if (tid < B) {
+#pragma unroll 8
+        for (uint32_t r = 0; r < nctas; ++r) {
+            const uint32_t c = cluster_load(sums + tid, r);
+            total += c;
+            before_me += r < rank ? c : 0u;
+        }
+    }
+    cluster_arrive();   // this CTA has read the others' sums; waited for before it ends
+    // exclusive sum of the totals over the buckets
     uint32_t incl = total;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -60,12 +122,16 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    uint32_t first = incl - total;
-    for (uint32_t w = 0; w < warp; ++w) first += warp_sum[w];
     if (tid < B) {
-        offsets[tid] = first;
-        if (tid < E) counts[tid] = total;
-        for (uint32_t w = 0; w < kSortWarps; ++w) {
+        uint32_t first = incl - total;
+        for (uint32_t w = 0; w < warp; ++w) first += warp_sum[w];
+        if (rank == 0) {
+            offsets[tid] = first;
+            if (tid < E) counts[tid] = total;
+        }
+        first += before_me;
+#pragma unroll 8
+        for (uint32_t w = 0; w < W; ++w) {
             const uint32_t c = hist[w * B + tid];
             hist[w * B + tid] = first;
             first += c;
@@ -73,11 +139,12 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32
     }
     __syncthreads();
 
+    uint32_t next = lo + lane < hi ? bucket_of(ids, lo + lane, E) : 0u;
     for (uint32_t base = lo; base < hi; base += 32) {
-        const uint32_t i = base + lane;
+        const uint32_t i = base + lane, b = next;
         const bool in = i < hi;
-        const uint32_t b = in ? bucket_of(ids, i, E) : 0xFFFFFFFFu;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, b);
+        if (i + 32 < hi) next = bucket_of(ids, i + 32, E);
+        const uint32_t same = lanes_like(b, bits, in);
         const uint32_t before = __popc(same & ((1u << lane) - 1u));
         uint32_t p = 0;
         if (in) p = mine[b] + before;
@@ -89,6 +156,7 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32
             src[p] = (int32_t)i;
         }
     }
+    cluster_wait();
 }
 
 // --------------------------------------------------------------- dispatch
@@ -194,6 +262,12 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(const Td *dout, in
     }
 }
 
+// CTAs of the sort's cluster.  The steps between the passes cost about 3 us
+// in one CTA, 4 in several; the passes cost 0.8 us per 1024 slots of a CTA.
+// Measured (1 / 8 / 16 CTAs): 6 slots 3.0 / 3.8 / 3.8 us, 6144 slots
+// 9.0 / 5.8 / 6.0 us, 98304 slots 72 / 14 / 10 us.
+int sort_ctas(uint32_t n) { return n <= 1024 ? 1 : n <= 8192 ? 8 : kMaxSortCtas; }
+
 inline uint64_t ctas(uint64_t work) { return (work + kThreads - 1) / kThreads; }
 
 template <class Unit>
@@ -209,15 +283,29 @@ void dispatch(const void *x, int64_t ldx, void *xs, int64_t ldxs, int64_t row_by
 }  // namespace
 
 cudaError_t launch_moe_sort(const void *ids, int id_bytes, const MoePlan &m, cudaStream_t s) {
-    const uint32_t n = (uint32_t)(m.tokens * m.topk);
-    const size_t smem = (size_t)kSortWarps * (m.n_experts + 1) * sizeof(uint32_t);
-    if (id_bytes == 4)
-        k_moe_sort<int32_t><<<1, kSortThreads, smem, s>>>(static_cast<const int32_t *>(ids), n, m.n_experts, m.pos,
-                                                          m.src, m.counts, m.offsets);
-    else
-        k_moe_sort<int64_t><<<1, kSortThreads, smem, s>>>(static_cast<const int64_t *>(ids), n, m.n_experts, m.pos,
-                                                          m.src, m.counts, m.offsets);
-    return cudaGetLastError();
+    uint32_t n = (uint32_t)(m.tokens * m.topk), E = (uint32_t)m.n_experts;
+    int ctas = sort_ctas(n);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)ctas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(ctas > 1 ? kSortThreads : 32u * std::max((E + 32u) / 32u, std::min(32u, (n + 31u) / 32u)));
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    auto go = [&](auto *t) {
+        using Id = std::remove_pointer_t<decltype(t)>;
+        if (ctas > 8) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(k_moe_sort<Id>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+        }
+        return cudaLaunchKernelEx(&cfg, k_moe_sort<Id>, static_cast<const Id *>(ids), n, E, m.pos, m.src, m.counts,
+                                  m.offsets);
+    };
+    return id_bytes == 4 ? go(static_cast<int32_t *>(nullptr)) : go(static_cast<int64_t *>(nullptr));
 }
 
 cudaError_t launch_moe_dispatch(const void *x, int dtype, int64_t hidden, int64_t ld_x, const MoePlan &m, void *xs,
