@@ -7,14 +7,14 @@
 // 8 bytes an element pair in fp32.  At 8 bits and a scale byte per 32 they
 // cost 2.06 bytes, written by the pass that reads them anyway.
 //
-// Two layouts of the work, chosen by alignment:
-//  * quads: a thread owns 8 consecutive elements (16-byte accesses), four
-//    neighbouring lanes one 32-element block, whose maximum takes two shuffles;
-//  * lanes (rows that are not 16-byte aligned or not a multiple of 8 long): a
-//    warp owns a block, a lane one element.
+// In the whole layout (rowops.cuh) a thread owns 16 consecutive elements and
+// two neighbouring lanes one 32-element block; in the strided one a warp owns
+// eight blocks, a lane one element of each.
 #include "common.cuh"
 #include "internal.h"
 #include "rowops.cuh"
+
+#include <cuda_fp16.h>
 
 #include <type_traits>
 
@@ -46,28 +46,29 @@ __device__ __forceinline__ float scale_of(uint32_t b) {
 // The 8-bit code of x (already in units of the scale), in the low byte.
 template <int FMT>
 __device__ __forceinline__ uint32_t code_of(float x) {
-    if constexpr (FMT == kInt8)
-        // adding 1.5 * 2^23 rounds to an integer, ties to even, whose two's
-        // complement is then in the low mantissa bits (a NaN becomes -127;
-        // non-finite blocks are cleared by the caller)
-        return __float_as_uint(__fadd_rn(fminf(fmaxf(x, -127.0f), 127.0f), 12582912.0f)) & 0xFFu;
-    else
+    if constexpr (FMT == kInt8) {
+        // sign(x) min(|x|, 127); then adding 1.5 * 2^23 rounds to an integer,
+        // ties to even, whose two's complement is in the low mantissa bits
+        float c;
+        asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(c) : "f"(x), "f"(127.0f));
+        return __float_as_uint(__fadd_rn(c, 12582912.0f));
+    } else {
         return e4m3_from_f32(x);
-}
-
-// Codes of 8 elements, first element in the lowest byte.
-template <int FMT>
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], uint32_t b) {
-    const float inv = scale_inv(b);
-    uint32_t w[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = code_of<FMT>(x[4 * h + i] * inv);
-        w[h] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
     }
-    return b == 255u ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);
+}
+// Codes of 4 elements, the first in the lowest byte.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes4(const float *x, float inv) {
+    if constexpr (FMT == kInt8) {
+        const uint32_t lo = __byte_perm(code_of<FMT>(x[0] * inv), code_of<FMT>(x[1] * inv), 0x0040);
+        const uint32_t hi = __byte_perm(code_of<FMT>(x[2] * inv), code_of<FMT>(x[3] * inv), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
+    } else {
+        uint16_t lo, hi;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1] * inv), "f"(x[0] * inv));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3] * inv), "f"(x[2] * inv));
+        return (uint32_t)hi << 16 | lo;
+    }
 }
 
 template <int FMT>
@@ -75,11 +76,25 @@ __device__ __forceinline__ float value_of(uint32_t code, float scale) {
     if constexpr (FMT == kInt8) return (float)(int8_t)code * scale;
     else return e4m3_to_f32(code) * scale;
 }
-
+// Values of 4 codes.
 template <int FMT>
-__device__ __forceinline__ void values8(uint2 w, float scale, float (&x)[8]) {
+__device__ __forceinline__ void values4(uint32_t w, float scale, float *x) {
+    if constexpr (FMT == kInt8) {
+        // code + 128 in the low mantissa bits of 2^23, then 2^23 + 128 taken off
+        const uint32_t u = w ^ 0x80808080u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = value_of<FMT>(((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xFFu, scale);
+        for (int i = 0; i < 4; ++i)
+            x[i] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + i)) - 8388736.0f) * scale;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t h;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w >> (16 * i))));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            x[2 * i] = f.x * scale;
+            x[2 * i + 1] = f.y * scale;
+        }
+    }
 }
 
 // ------------------------------------------------------------- activation
@@ -98,163 +113,194 @@ __device__ __forceinline__ float silu(float g) {
 }
 
 // ------------------------------------------------------------------- work
-// A flat index over (row, block of 32, part): parts are 4 quad lanes or 32
-// lanes.  Every lane of a block is in or out together.
+// Elements of a thread, and the row and part it owns.  All lanes of a block
+// (whole: lane pair; strided: warp) are in or out together.
+template <bool WHOLE>
+constexpr int kElems = WHOLE ? 16 : 8;
+
+template <bool WHOLE>
 struct Place {
     int64_t row;
-    uint32_t blk, col;
+    Part<WHOLE, kElems<WHOLE>> part;
 };
-template <int V>
-__device__ __forceinline__ bool place(uint64_t blocks, RowDiv nb, Place &p) {
-    constexpr uint32_t kParts = 32 / V;
-    const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-    const uint64_t b = i / kParts;
-    if (b >= blocks) return false;
-    p.row = (int64_t)row_of(b, nb);
-    p.blk = (uint32_t)(b - (uint64_t)p.row * nb.d);
-    p.col = p.blk * 32 + (uint32_t)(i % kParts) * V;
+template <bool WHOLE>
+__device__ __forceinline__ bool place(uint64_t work, RowDiv units, uint32_t cols, Place<WHOLE> &p) {
+    uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (!WHOLE) i /= 32;
+    if (i >= work) return false;
+    p.row = (int64_t)row_of(i, units);
+    const uint32_t u = (uint32_t)(i - (uint64_t)p.row * units.d);
+    p.part.col = WHOLE ? u * 16 : u * 256 + (threadIdx.x & 31u);
+    p.part.cols = cols;
     return true;
 }
-// Maximum over the lanes of a block.
-template <int V>
-__device__ __forceinline__ uint32_t block_max(uint32_t m) {
-    if constexpr (V == 1) {
-        return __reduce_max_sync(0xFFFFFFFFu, m);
-    } else {
-        const uint32_t quad = 0xFu << (threadIdx.x & 28u);
-        m = max(m, __shfl_xor_sync(quad, m, 1));
-        return max(m, __shfl_xor_sync(quad, m, 2));
+
+// max(|a|, |b|, |c|), NaN if any is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// Bits of the block's largest magnitude over a lane pair; NaN above all.
+__device__ __forceinline__ uint32_t pair_max(const float (&x)[16]) {
+    float m[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        m[h] = max3_abs(x[8 * h], x[8 * h + 1], x[8 * h + 2]);
+        m[h] = max3_abs(m[h], x[8 * h + 3], x[8 * h + 4]);
+        m[h] = max3_abs(m[h], x[8 * h + 5], x[8 * h + 6]);
     }
+    const uint32_t a = __float_as_uint(max_nan(max3_abs(m[0], x[7], x[15]), m[1])) & 0x7FFFFFFFu;
+    return max(a, __shfl_xor_sync(3u << (threadIdx.x & 30u), a, 1));
 }
 
-// Writes the checkpoint of a block: x[] are this lane's elements (zeros where
-// it has none, `in` false).
-template <int FMT, int V>
-__device__ __forceinline__ void keep(const float (&x)[V], bool in, const Place &p, uint32_t nb, int64_t ld,
-                                     const Ckpt &c) {
-    uint32_t m = 0;
+// Writes the checkpoint of this thread's elements (0 where it has none).
+template <int FMT, bool WHOLE>
+__device__ __forceinline__ void keep(const float (&x)[kElems<WHOLE>], const Place<WHOLE> &p, const Ckpt &c,
+                                     int64_t ld, uint32_t nb) {
+    uint8_t *codes = c.codes + p.row * ld + p.part.col, *scales = c.scales + p.row * nb;
+    if constexpr (WHOLE) {
+        const uint32_t b = scale_byte<FMT>(pair_max(x));
+        const float inv = scale_inv(b);
+        if ((p.part.col & 16u) == 0) scales[p.part.col / 32] = (uint8_t)b;
+        if (!p.part.has(0)) return;
+        uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = max(m, abs_bits(x[i]));
-    const uint32_t b = scale_byte<FMT>(block_max<V>(m));
-    if ((p.col & 31u) == 0) c.scales[p.row * nb + p.blk] = (uint8_t)b;
-    if (!in) return;
-    uint8_t *at = c.codes + p.row * ld + p.col;
-    if constexpr (V == 8) *reinterpret_cast<uint2 *>(at) = codes8<FMT>(x, b);
-    else *at = b == 255u ? 0 : (uint8_t)code_of<FMT>(x[0] * scale_inv(b));
+        for (int i = 0; i < 4; ++i) w[i] = b == 255u ? 0u : codes4<FMT>(x + 4 * i, inv);
+        store_words(codes, w);
+    } else {
+        const uint32_t lane = threadIdx.x & 31u, first = p.part.col - lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (first + 32 * i >= p.part.cols) break;
+            const uint32_t b = scale_byte<FMT>(__reduce_max_sync(0xFFFFFFFFu, abs_bits(x[i])));
+            if (lane == 0) scales[first / 32 + i] = (uint8_t)b;
+            if (p.part.has(i)) codes[32 * i] = b == 255u ? 0 : (uint8_t)code_of<FMT>(x[i] * scale_inv(b));
+        }
+    }
 }
-template <int FMT, int V>
-__device__ __forceinline__ void restore(const Ckpt &c, const Place &p, uint32_t nb, int64_t ld, float (&x)[V]) {
-    const float s = scale_of(__ldg(c.scales + p.row * nb + p.blk));
-    const uint8_t *at = c.codes + p.row * ld + p.col;
-    if constexpr (V == 8) values8<FMT>(__ldg(reinterpret_cast<const uint2 *>(at)), s, x);
-    else x[0] = value_of<FMT>(__ldg(at), s);
+template <int FMT, bool WHOLE>
+__device__ __forceinline__ void restore(const Ckpt &c, const Place<WHOLE> &p, int64_t ld, uint32_t nb,
+                                        float (&x)[kElems<WHOLE>]) {
+    const uint8_t *codes = c.codes + p.row * ld + p.part.col, *scales = c.scales + p.row * nb + p.part.col / 32;
+    if constexpr (WHOLE) {
+        uint32_t w[4];
+        load_words(codes, w);
+        const float s = scale_of(__ldg(scales));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) values4<FMT>(w[i], s, x + 4 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = p.part.has(i) ? value_of<FMT>(__ldg(codes + 32 * i), scale_of(__ldg(scales + i))) : 0.0f;
+    }
 }
 
 // ---------------------------------------------------------------- kernels
-template <class T, int FMT, int V>
-__global__ void __launch_bounds__(kThreads) k_ckpt_save(const T *x, int64_t ld, Ckpt c, int64_t ldc, uint32_t cols,
-                                                        RowDiv nb, uint64_t blocks) {
-    Place p;
-    if (!place<V>(blocks, nb, p)) return;
-    const bool in = p.col < cols;
-    float v[V] = {};
-    if (in) load_f32<V>(x + p.row * ld + p.col, v);
-    keep<FMT, V>(v, in, p, nb.d, ldc, c);
+template <class T, int FMT, bool WHOLE>
+__global__ void __launch_bounds__(kThreads) k_ckpt_save(const T *__restrict__ x, int64_t ld, Ckpt c, int64_t ldc,
+                                                        uint32_t cols, uint32_t nb, RowDiv units, uint64_t work) {
+    Place<WHOLE> p;
+    if (!place(work, units, cols, p)) return;
+    float v[kElems<WHOLE>] = {};
+    if (!WHOLE || p.part.has(0)) p.part.load(x + p.row * ld, v);
+    keep<FMT, WHOLE>(v, p, c, ldc, nb);
 }
 
-template <class T, int FMT, int V>
-__global__ void __launch_bounds__(kThreads) k_ckpt_load(Ckpt c, int64_t ldc, T *x, int64_t ld, uint32_t cols,
-                                                        RowDiv nb, uint64_t blocks) {
-    Place p;
-    if (!place<V>(blocks, nb, p) || p.col >= cols) return;
-    float v[V];
-    restore<FMT, V>(c, p, nb.d, ldc, v);
-    store_f32<V>(x + p.row * ld + p.col, v);
+template <class T, int FMT, bool WHOLE>
+__global__ void __launch_bounds__(kThreads) k_ckpt_load(Ckpt c, int64_t ldc, T *__restrict__ x, int64_t ld,
+                                                        uint32_t cols, uint32_t nb, RowDiv units, uint64_t work) {
+    Place<WHOLE> p;
+    if (!place(work, units, cols, p) || !p.part.has(0)) return;
+    float v[kElems<WHOLE>];
+    restore<FMT, WHOLE>(c, p, ldc, nb, v);
+    p.part.store(x + p.row * ld, v);
 }
 
-template <class Ti, class To, int FMT, int V>
-__global__ void __launch_bounds__(kThreads) k_swiglu(const Ti *gate, int64_t ld_gate, const Ti *up, int64_t ld_up,
-                                                     To *h, int64_t ld_h, Ckpt cg, Ckpt cu, int64_t ldc,
-                                                     uint32_t cols, RowDiv nb, uint64_t blocks) {
+template <class Ti, class To, int FMT, bool WHOLE>
+__global__ void __launch_bounds__(kThreads) k_swiglu(const Ti *__restrict__ gate, int64_t ld_gate,
+                                                     const Ti *__restrict__ up, int64_t ld_up, To *__restrict__ h,
+                                                     int64_t ld_h, Ckpt cg, Ckpt cu, int64_t ldc, uint32_t cols,
+                                                     uint32_t nb, RowDiv units, uint64_t work) {
     constexpr bool kExact = std::is_same<To, float>::value;
-    Place p;
-    if (!place<V>(blocks, nb, p)) return;
-    const bool in = p.col < cols;
-    float g[V] = {}, u[V] = {};
-    if (in) {
-        load_f32<V>(gate + p.row * ld_gate + p.col, g);
-        load_f32<V>(up + p.row * ld_up + p.col, u);
-        float o[V];
+    constexpr int N = kElems<WHOLE>;
+    Place<WHOLE> p;
+    if (!place(work, units, cols, p)) return;
+    float g[N] = {}, u[N] = {};
+    if (!WHOLE || p.part.has(0)) {
+        p.part.load(gate + p.row * ld_gate, g);
+        p.part.load(up + p.row * ld_up, u);
+        float o[N];
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = silu<kExact>(g[i]) * u[i];
-        store_f32<V>(h + p.row * ld_h + p.col, o);
+        for (int i = 0; i < N; ++i) o[i] = silu<kExact>(g[i]) * u[i];
+        p.part.store(h + p.row * ld_h, o);
     }
     if constexpr (FMT != kNone) {
-        keep<FMT, V>(g, in, p, nb.d, ldc, cg);
-        keep<FMT, V>(u, in, p, nb.d, ldc, cu);
+        keep<FMT, WHOLE>(g, p, cg, ldc, nb);
+        keep<FMT, WHOLE>(u, p, cu, ldc, nb);
     }
 }
 
-template <class Td, class To, int FMT, int V>
-__global__ void __launch_bounds__(kThreads) k_swiglu_bwd(const Td *dh, int64_t ld_dh, Ckpt cg, Ckpt cu, int64_t ldc,
-                                                         To *dgate, int64_t ld_dgate, To *dup, int64_t ld_dup,
-                                                         uint32_t cols, RowDiv nb, uint64_t blocks) {
+template <class Td, class To, int FMT, bool WHOLE>
+__global__ void __launch_bounds__(kThreads) k_swiglu_bwd(const Td *__restrict__ dh, int64_t ld_dh, Ckpt cg, Ckpt cu,
+                                                         int64_t ldc, To *__restrict__ dgate, int64_t ld_dgate,
+                                                         To *__restrict__ dup, int64_t ld_dup, uint32_t cols,
+                                                         uint32_t nb, RowDiv units, uint64_t work) {
     constexpr bool kExact = std::is_same<To, float>::value;
-    Place p;
-    if (!place<V>(blocks, nb, p) || p.col >= cols) return;
-    float d[V], g[V], u[V];
-    load_f32<V>(dh + p.row * ld_dh + p.col, d);
-    restore<FMT, V>(cg, p, nb.d, ldc, g);
-    restore<FMT, V>(cu, p, nb.d, ldc, u);
+    constexpr int N = kElems<WHOLE>;
+    Place<WHOLE> p;
+    if (!place(work, units, cols, p) || !p.part.has(0)) return;
+    float d[N], g[N], u[N];
+    p.part.load(dh + p.row * ld_dh, d);
+    restore<FMT, WHOLE>(cg, p, ldc, nb, g);
+    restore<FMT, WHOLE>(cu, p, ldc, nb, u);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < N; ++i) {
         const float s = sigmoid<kExact>(g[i]), gs = g[i] * s;
         u[i] = d[i] * u[i] * fmaf(gs, 1.0f - s, s);
         g[i] = d[i] * gs;
     }
-    store_f32<V>(dgate + p.row * ld_dgate + p.col, u);
-    store_f32<V>(dup + p.row * ld_dup + p.col, g);
+    p.part.store(dgate + p.row * ld_dgate, u);
+    p.part.store(dup + p.row * ld_dup, g);
 }
 
 // -------------------------------------------------------------- launching
+// The work over rows x cols in one of the layouts.
 struct Grid {
-    RowDiv nb;
-    uint64_t blocks;
+    bool whole;
+    uint32_t nb;       // blocks of a row
+    RowDiv units;
+    uint64_t work;
     unsigned ctas;
 };
-Grid grid_of(int64_t rows, int64_t cols, bool v8) {
-    const uint32_t nb = (uint32_t)((cols + 31) / 32);
-    const uint64_t blocks = (uint64_t)rows * nb, lanes = blocks * (v8 ? 4 : 32);
-    return Grid{make_rowdiv(nb), blocks, (unsigned)((lanes + kThreads - 1) / kThreads)};
-}
-template <int N>
-using Int = std::integral_constant<int, N>;
-template <class F>
-void by_width(bool v8, F f) {
-    if (v8) f(Int<8>());
-    else f(Int<1>());
+Grid grid_of(int64_t rows, int64_t cols, bool aligned) {
+    Grid g;
+    g.whole = aligned && cols % 16 == 0;
+    g.nb = (uint32_t)((cols + 31) / 32);
+    // a lane pair per block, so that both lanes of a last half block are there
+    const uint32_t units = g.whole ? 2 * g.nb : units_of(false, kElems<false>, cols);
+    g.units = make_rowdiv(units);
+    g.work = (uint64_t)rows * units;
+    g.ctas = (unsigned)(((g.whole ? g.work : g.work * 32) + kThreads - 1) / kThreads);
+    return g;
 }
 template <class F>
 void by_format(int fmt, F f) {
-    if (fmt == kInt8) f(Int<kInt8>());
-    else f(Int<kE4M3>());
+    if (fmt == kInt8) f(std::integral_constant<int, kInt8>());
+    else f(std::integral_constant<int, kE4M3>());
 }
-template <class P>
-using Elem = std::remove_pointer_t<P>;
-inline size_t size_of(int dtype) { return dtype == 0 ? 2 : 4; }
 
 }  // namespace
 
 cudaError_t launch_ckpt_save(const void *x, int dtype, int64_t ld, const Ckpt &c, int fmt, int64_t rows, int64_t cols,
                              cudaStream_t s) {
-    const bool v8 = vec8(x, ld, cols, size_of(dtype));
-    const Grid g = grid_of(rows, cols, v8);
+    const Grid g = grid_of(rows, cols, whole_rows(x, ld, type_size(dtype), kElems<true>));
     by_type(dtype, [&](auto *t) {
         using T = Elem<decltype(t)>;
         by_format(fmt, [&](auto f) {
-            by_width(v8, [&](auto v) {
-                k_ckpt_save<T, decltype(f)::value, decltype(v)::value><<<g.ctas, kThreads, 0, s>>>(
-                    static_cast<const T *>(x), ld, c, ckpt_ld(cols), (uint32_t)cols, g.nb, g.blocks);
+            by_bool(g.whole, [&](auto w) {
+                k_ckpt_save<T, decltype(f)::value, decltype(w)::value><<<g.ctas, kThreads, 0, s>>>(
+                    static_cast<const T *>(x), ld, c, ckpt_ld(cols), (uint32_t)cols, g.nb, g.units, g.work);
             });
         });
     });
@@ -263,14 +309,13 @@ cudaError_t launch_ckpt_save(const void *x, int dtype, int64_t ld, const Ckpt &c
 
 cudaError_t launch_ckpt_load(const Ckpt &c, int fmt, int64_t rows, int64_t cols, void *x, int dtype, int64_t ld,
                              cudaStream_t s) {
-    const bool v8 = vec8(x, ld, cols, size_of(dtype));
-    const Grid g = grid_of(rows, cols, v8);
+    const Grid g = grid_of(rows, cols, whole_rows(x, ld, type_size(dtype), kElems<true>));
     by_type(dtype, [&](auto *t) {
         using T = Elem<decltype(t)>;
         by_format(fmt, [&](auto f) {
-            by_width(v8, [&](auto v) {
-                k_ckpt_load<T, decltype(f)::value, decltype(v)::value><<<g.ctas, kThreads, 0, s>>>(
-                    c, ckpt_ld(cols), static_cast<T *>(x), ld, (uint32_t)cols, g.nb, g.blocks);
+            by_bool(g.whole, [&](auto w) {
+                k_ckpt_load<T, decltype(f)::value, decltype(w)::value><<<g.ctas, kThreads, 0, s>>>(
+                    c, ckpt_ld(cols), static_cast<T *>(x), ld, (uint32_t)cols, g.nb, g.units, g.work);
             });
         });
     });
@@ -280,20 +325,20 @@ cudaError_t launch_ckpt_load(const Ckpt &c, int fmt, int64_t rows, int64_t cols,
 cudaError_t launch_swiglu(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int in_dtype,
                           int64_t rows, int64_t cols, void *h, int h_dtype, int64_t ld_h, const Ckpt &cg,
                           const Ckpt &cu, int fmt, cudaStream_t s) {
-    const bool v8 = vec8(gate, ld_gate, cols, size_of(in_dtype)) && vec8(up, ld_up, cols, size_of(in_dtype)) &&
-                    vec8(h, ld_h, cols, size_of(h_dtype));
-    const Grid gr = grid_of(rows, cols, v8);
+    const Grid gr = grid_of(rows, cols, whole_rows(gate, ld_gate, type_size(in_dtype), kElems<true>) &&
+                                            whole_rows(up, ld_up, type_size(in_dtype), kElems<true>) &&
+                                            whole_rows(h, ld_h, type_size(h_dtype), kElems<true>));
     by_type(in_dtype, [&](auto *ti) {
         using Ti = Elem<decltype(ti)>;
         by_type(h_dtype, [&](auto *to) {
             using To = Elem<decltype(to)>;
-            by_width(v8, [&](auto v) {
+            by_bool(gr.whole, [&](auto w) {
                 auto go = [&](auto f) {
-                    k_swiglu<Ti, To, decltype(f)::value, decltype(v)::value><<<gr.ctas, kThreads, 0, s>>>(
+                    k_swiglu<Ti, To, decltype(f)::value, decltype(w)::value><<<gr.ctas, kThreads, 0, s>>>(
                         static_cast<const Ti *>(gate), ld_gate, static_cast<const Ti *>(up), ld_up,
-                        static_cast<To *>(h), ld_h, cg, cu, ckpt_ld(cols), (uint32_t)cols, gr.nb, gr.blocks);
+                        static_cast<To *>(h), ld_h, cg, cu, ckpt_ld(cols), (uint32_t)cols, gr.nb, gr.units, gr.work);
                 };
-                if (fmt == kNone) go(Int<kNone>());
+                if (fmt == kNone) go(std::integral_constant<int, kNone>());
                 else by_format(fmt, go);
             });
         });
@@ -304,18 +349,18 @@ cudaError_t launch_swiglu(const void *gate, int64_t ld_gate, const void *up, int
 cudaError_t launch_swiglu_bwd(const void *dh, int dh_dtype, int64_t ld_dh, const Ckpt &cg, const Ckpt &cu, int fmt,
                               int64_t rows, int64_t cols, void *dgate, int64_t ld_dgate, void *dup, int64_t ld_dup,
                               int out_dtype, cudaStream_t s) {
-    const bool v8 = vec8(dh, ld_dh, cols, size_of(dh_dtype)) && vec8(dgate, ld_dgate, cols, size_of(out_dtype)) &&
-                    vec8(dup, ld_dup, cols, size_of(out_dtype));
-    const Grid g = grid_of(rows, cols, v8);
+    const Grid g = grid_of(rows, cols, whole_rows(dh, ld_dh, type_size(dh_dtype), kElems<true>) &&
+                                           whole_rows(dgate, ld_dgate, type_size(out_dtype), kElems<true>) &&
+                                           whole_rows(dup, ld_dup, type_size(out_dtype), kElems<true>));
     by_type(dh_dtype, [&](auto *td) {
         using Td = Elem<decltype(td)>;
         by_type(out_dtype, [&](auto *to) {
             using To = Elem<decltype(to)>;
             by_format(fmt, [&](auto f) {
-                by_width(v8, [&](auto v) {
-                    k_swiglu_bwd<Td, To, decltype(f)::value, decltype(v)::value><<<g.ctas, kThreads, 0, s>>>(
+                by_bool(g.whole, [&](auto w) {
+                    k_swiglu_bwd<Td, To, decltype(f)::value, decltype(w)::value><<<g.ctas, kThreads, 0, s>>>(
                         static_cast<const Td *>(dh), ld_dh, cg, cu, ckpt_ld(cols), static_cast<To *>(dgate), ld_dgate,
-                        static_cast<To *>(dup), ld_dup, (uint32_t)cols, g.nb, g.blocks);
+                        static_cast<To *>(dup), ld_dup, (uint32_t)cols, g.nb, g.units, g.work);
                 });
             });
         });

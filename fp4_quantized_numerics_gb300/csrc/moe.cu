@@ -160,104 +160,143 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32
 }
 
 // --------------------------------------------------------------- dispatch
-// One thread per `Unit` (16 bytes, or one element where rows are not 16-byte
-// aligned) of a token's row: read once, written topk times.
-template <class Unit>
-__global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *x, int64_t ld_x, Unit *xs, int64_t ld_xs,
-                                                           const int32_t *pos, const int64_t *routed_at, int topk,
-                                                           RowDiv units, uint64_t work) {
-    const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+// A thread reads its part of a token's row once and writes it topk times:
+// one 16-byte unit where all rows are 16-byte aligned, else eight elements a
+// warp's width apart.
+template <class Unit, int N>
+__global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *__restrict__ x, int64_t ld_x,
+                                                           Unit *__restrict__ xs, int64_t ld_xs,
+                                                           const int32_t *__restrict__ pos,
+                                                           const int64_t *__restrict__ routed_at, int topk,
+                                                           uint32_t width, RowDiv units, uint64_t work) {
+    uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+    if constexpr (N > 1) i /= 32;
     if (i >= work) return;
     const uint64_t t = row_of(i, units);
     const uint32_t u = (uint32_t)(i - t * units.d);
-    const Unit v = x[t * ld_x + u];
+    const uint32_t c = N > 1 ? u * (32 * N) + (threadIdx.x & 31u) : u;
+    Unit v[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = c + 32 * e < width ? x[t * ld_x + c + 32 * e] : Unit{};
     const int32_t routed = (int32_t)__ldg(routed_at);
     const int32_t *at = pos + t * topk;
     for (int j = 0; j < topk; ++j) {
         const int32_t p = __ldg(at + j);
-        xs[(int64_t)p * ld_xs + u] = p < routed ? v : Unit{};
+        Unit *to = xs + (int64_t)p * ld_xs + c;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (c + 32 * e < width) to[32 * e] = p < routed ? v[e] : Unit{};
     }
 }
 
 // ---------------------------------------------------------------- combine
-// One thread per V elements of an output row; the topk rows are added in
+// A thread owns 8 elements of an output row; the topk rows are added in
 // ascending order of choice, in fp32.
-template <class Ty, class To, int V>
-__global__ void __launch_bounds__(kThreads) k_moe_combine(const Ty *y, int64_t ld_y, const int32_t *pos,
-                                                          const float *weights, const int64_t *routed_at, To *out,
-                                                          int64_t ld_out, int topk, RowDiv units, uint64_t work) {
-    const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+template <class Ty, class To, bool WHOLE>
+__global__ void __launch_bounds__(kThreads) k_moe_combine(const Ty *__restrict__ y, int64_t ld_y,
+                                                          const int32_t *__restrict__ pos,
+                                                          const float *__restrict__ weights,
+                                                          const int64_t *__restrict__ routed_at, To *__restrict__ out,
+                                                          int64_t ld_out, int topk, uint32_t hidden, RowDiv units,
+                                                          uint64_t work) {
+    uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+    if constexpr (!WHOLE) i /= 32;
     if (i >= work) return;
     const uint64_t t = row_of(i, units);
-    const uint32_t c = (uint32_t)(i - t * units.d) * V;
+    const uint32_t u = (uint32_t)(i - t * units.d);
+    const Part<WHOLE, 8> part{WHOLE ? u * 8 : u * 256 + (threadIdx.x & 31u), hidden};
     const int32_t routed = (int32_t)__ldg(routed_at);
-    float acc[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+    float acc[8] = {};
 #pragma unroll 4
     for (int j = 0; j < topk; ++j) {
         const int32_t p = __ldg(pos + t * topk + j);
         if (p >= routed) continue;
         const float w = weights ? __ldg(weights + t * topk + j) : 1.0f;
-        float v[V];
-        load_f32<V>(y + (int64_t)p * ld_y + c, v);
+        float v[8];
+        part.load(y + (int64_t)p * ld_y, v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, v[e], acc[e]);
     }
-    store_f32<V>(out + t * ld_out + c, acc);
+    part.store(out + t * ld_out, acc);
 }
 
 // ------------------------------------------------------ combine's gradient
-// One warp per token: it reads dout's row once per kChoices choices, writes
-// the scaled copies and keeps the choices' dot products in registers.
-constexpr int kChoices = 8;
+// G threads per token (32, 64 or 128): they read dout's row once per kBatch
+// choices, write the scaled copies and keep the choices' dot products in
+// registers; a butterfly over the warp that halves the number of sums at each
+// step, then one addition per warp in shared memory, joins them in an order
+// that depends on nothing but the sizes.
+constexpr int kBatch = 4;
 
-template <class Td, class Ty, class To, int V>
-__global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(const Td *dout, int64_t ld_dout, const Ty *y,
-                                                              int64_t ld_y, const int32_t *pos, const float *weights,
-                                                              const int64_t *routed_at, To *dy, int64_t ld_dy,
-                                                              float *dw, int topk, uint32_t hidden, uint32_t tokens) {
-    const uint32_t lane = threadIdx.x & 31u;
-    const uint32_t t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (t >= tokens) return;
+template <class Td, class Ty, class To, bool WHOLE, int G>
+__global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(
+    const Td *__restrict__ dout, int64_t ld_dout, const Ty *__restrict__ y, int64_t ld_y,
+    const int32_t *__restrict__ pos, const float *__restrict__ weights, const int64_t *__restrict__ routed_at,
+    To *__restrict__ dy, int64_t ld_dy, float *__restrict__ dw, int topk, uint32_t hidden, uint32_t tokens) {
+    constexpr int kWarps = G / 32;
+    __shared__ float sums[kThreads / 32][kBatch];
+    const uint32_t lane = threadIdx.x & 31u, in_group = threadIdx.x % G, group = threadIdx.x / G;
+    const uint32_t t = blockIdx.x * (kThreads / G) + group;
+    const bool live = t < tokens;
     const int32_t routed = (int32_t)__ldg(routed_at);
-    for (int j0 = 0; j0 < topk; j0 += kChoices) {
-        int32_t p[kChoices];
-        float w[kChoices], dot[kChoices];
+    for (int j0 = 0; j0 < topk; j0 += kBatch) {
+        int32_t p[kBatch];
+        float w[kBatch], dot[kBatch];
 #pragma unroll
-        for (int j = 0; j < kChoices; ++j) {
-            const bool in = j0 + j < topk;
+        for (int j = 0; j < kBatch; ++j) {
+            const bool in = live && j0 + j < topk;
             p[j] = in ? __ldg(pos + (int64_t)t * topk + j0 + j) : -1;
             w[j] = in && p[j] < routed ? __ldg(weights + (int64_t)t * topk + j0 + j) : 0.0f;
             dot[j] = 0.0f;
         }
-        for (uint32_t c = lane * V; c < hidden; c += 32 * V) {
-            float d[V];
-            load_f32<V>(dout + (int64_t)t * ld_dout + c, d);
+        // the part's first element; the warp's segments are 256 elements
+        uint32_t c = WHOLE ? in_group * 8 : in_group / 32 * 256 + lane;
+        for (; live && c < (WHOLE ? hidden : (hidden + 255) / 256 * 256); c += G * 8) {
+            const Part<WHOLE, 8> part{c, hidden};
+            float d[8], v[kBatch][8];
+            part.load(dout + (int64_t)t * ld_dout, d);
 #pragma unroll
-            for (int j = 0; j < kChoices; ++j) {
+            for (int j = 0; j < kBatch; ++j)
+                if (p[j] >= 0 && p[j] < routed) part.load(y + (int64_t)p[j] * ld_y, v[j]);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
                 if (p[j] < 0) continue;
-                float o[V];
+                float o[8] = {};
                 if (p[j] < routed) {
-                    float v[V];
-                    load_f32<V>(y + (int64_t)p[j] * ld_y + c, v);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         o[e] = w[j] * d[e];
-                        dot[j] = fmaf(d[e], v[e], dot[j]);
+                        dot[j] = fmaf(d[e], v[j][e], dot[j]);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) o[e] = 0.0f;
                 }
-                store_f32<V>(dy + (int64_t)p[j] * ld_dy + c, o);
+                part.store(dy + (int64_t)p[j] * ld_dy, o);
             }
         }
+        // kBatch = 4 sums over 32 lanes: two steps that halve their number,
+        // three that add; lanes 0, 8, 16, 24 hold sums 0, 1, 2, 3
+        float s = 0.0f;
+        {
+            const bool h16 = lane & 16u, h8 = lane & 8u;
+            const float a = (h16 ? dot[2] : dot[0]) + __shfl_xor_sync(0xFFFFFFFFu, h16 ? dot[0] : dot[2], 16);
+            const float b = (h16 ? dot[3] : dot[1]) + __shfl_xor_sync(0xFFFFFFFFu, h16 ? dot[1] : dot[3], 16);
+            s = (h8 ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, h8 ? a : b, 8);
 #pragma unroll
-        for (int j = 0; j < kChoices; ++j) {
+            for (int m = 4; m; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
+        }
+        const int mine = (int)(lane >> 3);
+        const bool has = live && (lane & 7u) == 0 && j0 + mine < topk;
+        if constexpr (kWarps == 1) {
+            if (has) dw[(int64_t)t * topk + j0 + mine] = s;
+        } else {
+            if ((lane & 7u) == 0) sums[threadIdx.x / 32][mine] = s;
+            __syncthreads();
+            if (has && in_group < 32) {
+                float all = 0.0f;
 #pragma unroll
-            for (int m = 16; m; m >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], m);
-            if (lane == 0 && p[j] >= 0) dw[(int64_t)t * topk + j0 + j] = dot[j];
+                for (int k = 0; k < kWarps; ++k) all += sums[group * kWarps + k][mine];
+                dw[(int64_t)t * topk + j0 + mine] = all;
+            }
+            __syncthreads();
         }
     }
 }
@@ -268,16 +307,23 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(const Td *dout, in
 // 9.0 / 5.8 / 6.0 us, 98304 slots 72 / 14 / 10 us.
 int sort_ctas(uint32_t n) { return n <= 1024 ? 1 : n <= 8192 ? 8 : kMaxSortCtas; }
 
+// Threads per token of combine's gradient: as many as have 8 elements each,
+// at most 128.  Measured (32 / 64 / 128 / 256): 16384 tokens x 6 of 2048
+// 195 / 189 / 190 / 214 us, 128 tokens 9.4 / 6.2 / 4.3 / 3.8 us, 8192 x 2 of
+// 8192 129 / 120 / 120 / 129 us.
+int bwd_group(int64_t hidden) { return hidden <= 256 ? 32 : hidden <= 512 ? 64 : 128; }
+
 inline uint64_t ctas(uint64_t work) { return (work + kThreads - 1) / kThreads; }
 
-template <class Unit>
+template <class Unit, int N>
 void dispatch(const void *x, int64_t ldx, void *xs, int64_t ldxs, int64_t row_bytes, const MoePlan &m,
               cudaStream_t s) {
-    const uint32_t units = (uint32_t)(row_bytes / sizeof(Unit));
+    const int64_t size = sizeof(Unit);
+    const uint32_t width = (uint32_t)(row_bytes / size), units = N > 1 ? units_of(false, N, width) : width;
     const uint64_t work = (uint64_t)m.tokens * units;
-    k_moe_dispatch<Unit><<<(unsigned)ctas(work), kThreads, 0, s>>>(
-        static_cast<const Unit *>(x), ldx / (int64_t)sizeof(Unit), static_cast<Unit *>(xs),
-        ldxs / (int64_t)sizeof(Unit), m.pos, m.offsets + m.n_experts, m.topk, make_rowdiv(units), work);
+    k_moe_dispatch<Unit, N><<<(unsigned)ctas(work * (N > 1 ? 32 : 1)), kThreads, 0, s>>>(
+        static_cast<const Unit *>(x), ldx / size, static_cast<Unit *>(xs), ldxs / size, m.pos,
+        m.offsets + m.n_experts, m.topk, width, make_rowdiv(units), work);
 }
 
 }  // namespace
@@ -313,28 +359,28 @@ cudaError_t launch_moe_dispatch(const void *x, int dtype, int64_t hidden, int64_
     const int64_t esz = dtype == 0 ? 2 : 4, row = hidden * esz;
     const uint64_t all = (uint64_t)(uintptr_t)x | (uint64_t)(uintptr_t)xs | (uint64_t)(ld_x * esz) |
                          (uint64_t)(ld_xs * esz) | (uint64_t)row;
-    if (all % 16 == 0) dispatch<uint4>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
-    else if (esz == 4) dispatch<uint32_t>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
-    else dispatch<uint16_t>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
+    if (all % 16 == 0) dispatch<uint4, 1>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
+    else if (esz == 4) dispatch<uint32_t, 8>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
+    else dispatch<uint16_t, 8>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
     return cudaGetLastError();
 }
 
 cudaError_t launch_moe_combine(const void *y, int y_dtype, int64_t hidden, int64_t ld_y, const MoePlan &m,
                                const float *weights, void *out, int out_dtype, int64_t ld_out, cudaStream_t s) {
-    const bool v8 = vec8(y, ld_y, hidden, y_dtype ? 4 : 2) && vec8(out, ld_out, hidden, out_dtype ? 4 : 2);
-    const uint32_t units = (uint32_t)(v8 ? hidden / 8 : hidden);
+    const bool whole = hidden % 8 == 0 && whole_rows(y, ld_y, type_size(y_dtype), 8) &&
+                       whole_rows(out, ld_out, type_size(out_dtype), 8);
+    const uint32_t units = units_of(whole, 8, hidden);
     const uint64_t work = (uint64_t)m.tokens * units;
-    auto go = [&](auto *yp, auto *op, auto v) {
-        using Ty = std::remove_pointer_t<decltype(yp)>;
-        using To = std::remove_pointer_t<decltype(op)>;
-        k_moe_combine<Ty, To, decltype(v)::value><<<(unsigned)ctas(work), kThreads, 0, s>>>(
-            static_cast<const Ty *>(y), ld_y, m.pos, weights, m.offsets + m.n_experts, static_cast<To *>(out), ld_out,
-            m.topk, make_rowdiv(units), work);
-    };
     by_type(y_dtype, [&](auto *yp) {
+        using Ty = Elem<decltype(yp)>;
         by_type(out_dtype, [&](auto *op) {
-            if (v8) go(yp, op, std::integral_constant<int, 8>());
-            else go(yp, op, std::integral_constant<int, 1>());
+            using To = Elem<decltype(op)>;
+            by_bool(whole, [&](auto w) {
+                k_moe_combine<Ty, To, decltype(w)::value>
+                    <<<(unsigned)ctas(whole ? work : work * 32), kThreads, 0, s>>>(
+                        static_cast<const Ty *>(y), ld_y, m.pos, weights, m.offsets + m.n_experts,
+                        static_cast<To *>(out), ld_out, m.topk, (uint32_t)hidden, make_rowdiv(units), work);
+            });
         });
     });
     return cudaGetLastError();
@@ -343,22 +389,28 @@ cudaError_t launch_moe_combine(const void *y, int y_dtype, int64_t hidden, int64
 cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_dout, const void *y, int y_dtype,
                                    int64_t ld_y, int64_t hidden, const MoePlan &m, const float *weights, void *dy,
                                    int dy_dtype, int64_t ld_dy, float *dw, cudaStream_t s) {
-    const bool v8 = vec8(dout, ld_dout, hidden, dout_dtype ? 4 : 2) && vec8(y, ld_y, hidden, y_dtype ? 4 : 2) &&
-                    vec8(dy, ld_dy, hidden, dy_dtype ? 4 : 2);
-    const unsigned grid = (unsigned)((m.tokens + kThreads / 32 - 1) / (kThreads / 32));
-    auto go = [&](auto *dp, auto *yp, auto *op, auto v) {
-        using Td = std::remove_pointer_t<decltype(dp)>;
-        using Ty = std::remove_pointer_t<decltype(yp)>;
-        using To = std::remove_pointer_t<decltype(op)>;
-        k_moe_combine_bwd<Td, Ty, To, decltype(v)::value><<<grid, kThreads, 0, s>>>(
-            static_cast<const Td *>(dout), ld_dout, static_cast<const Ty *>(y), ld_y, m.pos, weights,
-            m.offsets + m.n_experts, static_cast<To *>(dy), ld_dy, dw, m.topk, (uint32_t)hidden, (uint32_t)m.tokens);
-    };
+    const bool whole = hidden % 8 == 0 && whole_rows(dout, ld_dout, type_size(dout_dtype), 8) &&
+                       whole_rows(y, ld_y, type_size(y_dtype), 8) && whole_rows(dy, ld_dy, type_size(dy_dtype), 8);
+    const int G = bwd_group(hidden);
     by_type(dout_dtype, [&](auto *dp) {
+        using Td = Elem<decltype(dp)>;
         by_type(y_dtype, [&](auto *yp) {
+            using Ty = Elem<decltype(yp)>;
             by_type(dy_dtype, [&](auto *op) {
-                if (v8) go(dp, yp, op, std::integral_constant<int, 8>());
-                else go(dp, yp, op, std::integral_constant<int, 1>());
+                using To = Elem<decltype(op)>;
+                by_bool(whole, [&](auto w) {
+                    auto go = [&](auto g) {
+                        constexpr int kG = decltype(g)::value;
+                        const unsigned grid = (unsigned)((m.tokens + kThreads / kG - 1) / (kThreads / kG));
+                        k_moe_combine_bwd<Td, Ty, To, decltype(w)::value, kG><<<grid, kThreads, 0, s>>>(
+                            static_cast<const Td *>(dout), ld_dout, static_cast<const Ty *>(y), ld_y, m.pos, weights,
+                            m.offsets + m.n_experts, static_cast<To *>(dy), ld_dy, dw, m.topk, (uint32_t)hidden,
+                            (uint32_t)m.tokens);
+                    };
+                    if (G == 32) go(std::integral_constant<int, 32>());
+                    else if (G == 64) go(std::integral_constant<int, 64>());
+                    else go(std::integral_constant<int, 128>());
+                });
             });
         });
     });

@@ -1,6 +1,14 @@
 // rowops.cuh -- pieces shared by the row-wise operators around the grouped
-// GEMMs (moe.cu, activation.cu): vectors of row elements as fp32, and the
-// division that turns a flat work index into (row, place in the row).
+// GEMMs (moe.cu, activation.cu): how a thread finds and reads its part of a
+// row, and the division that turns a flat work index into (row, part).
+//
+// Two layouts, chosen by alignment (`whole`):
+//  * whole: a thread owns N consecutive elements, in accesses of 16 or 32
+//    bytes on such boundaries; rows are multiples of N long.
+//  * strided (anything else): a warp owns 32 N consecutive elements of a row,
+//    lane l the elements l, l + 32, ...: every access of the warp is one run
+//    of neighbouring elements, whatever the row's alignment, and the work of
+//    finding the place is shared by N elements.
 #pragma once
 
 #include <cstdint>
@@ -21,71 +29,129 @@ struct RowDiv {
 inline RowDiv make_rowdiv(uint32_t d) { return RowDiv{d == 1 ? 0 : ~0ull / d + 1, d}; }
 __device__ __forceinline__ uint64_t row_of(uint64_t n, RowDiv f) { return f.m ? __umul64hi(n, f.m) : n; }
 
-// V consecutive elements to and from fp32 registers: V = 8 in 16-byte
-// accesses (the pointer 16-byte aligned), V = 1 by element.
-template <int V>
-__device__ __forceinline__ void load_f32(const __nv_bfloat16 *p, float (&f)[V]) {
-    static_assert(V == 8 || V == 1, "vector of 8 or single element");
-    if constexpr (V == 8) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(u[i] << 16);
-            f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        }
-    } else {
-        f[0] = __bfloat162float(*p);
-    }
+// ------------------------------------------------------- 16 and 32 bytes
+__device__ __forceinline__ void load_words(const void *p, uint32_t (&w)[4]) {
+    const uint4 v = __ldg(static_cast<const uint4 *>(p));
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
 }
-template <int V>
-__device__ __forceinline__ void load_f32(const float *p, float (&f)[V]) {
-    if constexpr (V == 8) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    } else {
-        f[0] = __ldg(p);
-    }
+__device__ __forceinline__ void load_words(const void *p, uint32_t (&w)[8]) {
+    asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+        : "l"(p));
+}
+__device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[4]) {
+    *static_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(p)
+                 : "memory");
 }
 
+// ------------------------------------------- N consecutive elements as fp32
+template <int N>
+__device__ __forceinline__ void load_whole(const __nv_bfloat16 *p, float (&f)[N]) {
+    uint32_t w[N / 2];
+    load_words(p, w);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+template <int N>
+__device__ __forceinline__ void load_whole(const float *p, float (&f)[N]) {
+#pragma unroll
+    for (int h = 0; h < N / 8; ++h) {
+        uint32_t w[8];
+        load_words(p + 8 * h, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[8 * h + i] = __uint_as_float(w[i]);
+    }
+}
 // Rounds to nearest even, once, on the way out.
-template <int V>
-__device__ __forceinline__ void store_f32(__nv_bfloat16 *p, const float (&f)[V]) {
-    if constexpr (V == 8) {
-        uint32_t u[4];
+template <int N>
+__device__ __forceinline__ void store_whole(__nv_bfloat16 *p, const float (&f)[N]) {
+    uint32_t w[N / 2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-    } else {
-        *p = __float2bfloat16_rn(f[0]);
+    for (int i = 0; i < N / 2; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
+    store_words(p, w);
 }
-template <int V>
-__device__ __forceinline__ void store_f32(float *p, const float (&f)[V]) {
-    if constexpr (V == 8) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-        *p = f[0];
+template <int N>
+__device__ __forceinline__ void store_whole(float *p, const float (&f)[N]) {
+#pragma unroll
+    for (int h = 0; h < N / 8; ++h) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[8 * h + i]);
+        store_words(p + 8 * h, w);
     }
 }
 
-// Whether a tensor of `cols` elements of esz bytes a row (stride ld elements)
-// can be taken in vectors of 8.
-inline bool vec8(const void *p, int64_t ld, int64_t cols, size_t esz) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * (int64_t)esz) % 16 == 0 && cols % 8 == 0;
+__device__ __forceinline__ float load_one(const __nv_bfloat16 *p) {
+    return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p)) << 16);
+}
+__device__ __forceinline__ float load_one(const float *p) { return __ldg(p); }
+__device__ __forceinline__ void store_one(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
+
+// ---------------------------------------------------------- a thread's part
+// Elements col, col + kStep, ... of a row of `cols` (those below cols; in the
+// whole layout all N or none).
+template <bool WHOLE, int N>
+struct Part {
+    static constexpr uint32_t kStep = WHOLE ? 1 : 32;
+    uint32_t col, cols;
+
+    __device__ __forceinline__ bool has(int i) const { return col + i * kStep < cols; }
+    template <class T>
+    __device__ __forceinline__ void load(const T *row, float (&f)[N]) const {
+        if constexpr (WHOLE) {
+            load_whole<N>(row + col, f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = has(i) ? load_one(row + col + i * kStep) : 0.0f;
+        }
+    }
+    template <class T>
+    __device__ __forceinline__ void store(T *row, const float (&f)[N]) const {
+        if constexpr (WHOLE) {
+            store_whole<N>(row + col, f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (has(i)) store_one(row + col + i * kStep, f[i]);
+        }
+    }
+};
+
+// Units of work in a row: threads' parts (whole) or warps' segments.
+inline uint32_t units_of(bool whole, int n, int64_t cols) {
+    const int64_t per = whole ? n : 32 * n;
+    return (uint32_t)((cols + per - 1) / per);
+}
+
+// Whether a tensor (row stride ld elements of esz bytes) allows whole parts of
+// n elements: its accesses are n * esz bytes, at most 32.
+inline bool whole_rows(const void *p, int64_t ld, size_t esz, int n) {
+    const size_t a = n * esz < 32 ? n * esz : 32;
+    return reinterpret_cast<uintptr_t>(p) % a == 0 && (size_t)ld * esz % a == 0;
 }
 
 // Calls f with a null pointer of the element type of `dtype` (0 BF16, 1 FP32).
 template <class F>
-void by_type(int dtype, F f) {
-    if (dtype == 0) f(static_cast<__nv_bfloat16 *>(nullptr));
-    else f(static_cast<float *>(nullptr));
+auto by_type(int dtype, F f) {
+    return dtype == 0 ? f(static_cast<__nv_bfloat16 *>(nullptr)) : f(static_cast<float *>(nullptr));
+}
+inline size_t type_size(int dtype) { return dtype == 0 ? 2 : 4; }
+template <class P>
+using Elem = std::remove_pointer_t<P>;
+template <class F>
+auto by_bool(bool b, F f) {
+    return b ? f(std::true_type()) : f(std::false_type());
 }
 
 }  // namespace ufp4
