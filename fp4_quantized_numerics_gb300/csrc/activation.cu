@@ -8,14 +8,15 @@
 // cost 2.06 bytes, written by the pass that reads them anyway.
 //
 // In the whole layout (rowops.cuh) a thread owns 16 consecutive elements and
-// two neighbouring lanes one 32-element block; in the strided one a warp owns
-// eight blocks, a lane one element of each.
+// two neighbouring lanes one 32-element block; in pairs a half warp owns each
+// block, in singles the warp.
 #include "common.cuh"
 #include "internal.h"
 #include "rowops.cuh"
 
 #include <cuda_fp16.h>
 
+#include <initializer_list>
 #include <type_traits>
 
 namespace ufp4 {
@@ -55,6 +56,11 @@ __device__ __forceinline__ uint32_t code_of(float x) {
     } else {
         return e4m3_from_f32(x);
     }
+}
+// The code of x under the factor scale_inv gave its block.
+template <int FMT>
+__device__ __forceinline__ uint32_t block_code(float x, float inv) {
+    return inv == 0.0f ? 0u : code_of<FMT>(x * inv) & 0xFFu;
 }
 // Codes of 4 elements, the first in the lowest byte.
 template <int FMT>
@@ -113,26 +119,23 @@ __device__ __forceinline__ float silu(float g) {
 }
 
 // ------------------------------------------------------------------- work
-// Elements of a thread, and the row and part it owns.  All lanes of a block
-// (whole: lane pair; strided: warp) are in or out together.
-template <bool WHOLE>
-constexpr int kElems = WHOLE ? 16 : 8;
+template <int L>
+constexpr int kElems = L == kWhole ? 16 : 8;
 
-template <bool WHOLE>
+// The row and part a thread owns; false past the last.  All lanes of a block
+// are in or out together.
+template <int L>
 struct Place {
     int64_t row;
-    Part<WHOLE, kElems<WHOLE>> part;
+    Part<L, kElems<L>> part;
+
+    __device__ __forceinline__ Place(RowDiv parts, uint32_t cols, uint64_t i)
+        : row((int64_t)row_of(i, parts)), part((uint32_t)(i - (uint64_t)row * parts.d), cols) {}
 };
-template <bool WHOLE>
-__device__ __forceinline__ bool place(uint64_t work, RowDiv units, uint32_t cols, Place<WHOLE> &p) {
-    uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (!WHOLE) i /= 32;
-    if (i >= work) return false;
-    p.row = (int64_t)row_of(i, units);
-    const uint32_t u = (uint32_t)(i - (uint64_t)p.row * units.d);
-    p.part.col = WHOLE ? u * 16 : u * 256 + (threadIdx.x & 31u);
-    p.part.cols = cols;
-    return true;
+template <int L>
+__device__ __forceinline__ uint64_t part_index() {
+    const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+    return L == kWhole ? i : i / 32;
 }
 
 // max(|a|, |b|, |c|), NaN if any is.
@@ -155,152 +158,215 @@ __device__ __forceinline__ uint32_t pair_max(const float (&x)[16]) {
 }
 
 // Writes the checkpoint of this thread's elements (0 where it has none).
-template <int FMT, bool WHOLE>
-__device__ __forceinline__ void keep(const float (&x)[kElems<WHOLE>], const Place<WHOLE> &p, const Ckpt &c,
-                                     int64_t ld, uint32_t nb) {
-    uint8_t *codes = c.codes + p.row * ld + p.part.col, *scales = c.scales + p.row * nb;
-    if constexpr (WHOLE) {
+template <int FMT, int L>
+__device__ __forceinline__ void keep(const float (&x)[kElems<L>], const Place<L> &p, const Ckpt &c, int64_t ld,
+                                     uint32_t nb) {
+    const uint32_t col = p.part.col;
+    uint8_t *codes = c.codes + p.row * ld + col, *scales = c.scales + p.row * nb + col / 32;
+    if constexpr (L == kWhole) {
         const uint32_t b = scale_byte<FMT>(pair_max(x));
         const float inv = scale_inv(b);
-        if ((p.part.col & 16u) == 0) scales[p.part.col / 32] = (uint8_t)b;
+        if ((col & 16u) == 0) *scales = (uint8_t)b;
         if (!p.part.has(0)) return;
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = b == 255u ? 0u : codes4<FMT>(x + 4 * i, inv);
         store_words(codes, w);
     } else {
-        const uint32_t lane = threadIdx.x & 31u, first = p.part.col - lane;
+        // the blocks' maxima reach all their lanes; lane k of a block's lanes
+        // turns the k-th maximum into a scale and writes it, and the others
+        // take the factor from there
+        constexpr int kStep = L == kPairs ? 2 : 1, kLanes = 32 / kStep;
+        const uint32_t lane = threadIdx.x & 31u, k = lane % kLanes, first = lane - k;
+        const uint32_t lanes = kLanes == 32 ? 0xFFFFFFFFu : 0xFFFFu << first;
+        uint32_t mine = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (first + 32 * i >= p.part.cols) break;
-            const uint32_t b = scale_byte<FMT>(__reduce_max_sync(0xFFFFFFFFu, abs_bits(x[i])));
-            if (lane == 0) scales[first / 32 + i] = (uint8_t)b;
-            if (p.part.has(i)) codes[32 * i] = b == 255u ? 0 : (uint8_t)code_of<FMT>(x[i] * scale_inv(b));
+        for (int i = 0; i < 8; i += kStep) {
+            uint32_t m = abs_bits(x[i]);
+            if (kStep == 2) m = max(m, abs_bits(x[i + 1]));
+            m = __reduce_max_sync(lanes, m);
+            if (k == (uint32_t)(i / kStep)) mine = m;
+        }
+        const uint32_t b = scale_byte<FMT>(mine);
+        if (k < 8 / kStep && (col - kStep * k) + p.part.at((int)k * kStep) < p.part.cols)
+            scales[k * kStep] = (uint8_t)b;
+        const float inv = scale_inv(b);
+#pragma unroll
+        for (int i = 0; i < 8; i += kStep) {
+            const float f = __shfl_sync(lanes, inv, first + i / kStep);
+            if (!p.part.has(i)) continue;
+            const uint32_t c0 = block_code<FMT>(x[i], f);
+            if constexpr (kStep == 2)
+                *reinterpret_cast<uint16_t *>(codes + p.part.at(i)) =
+                    (uint16_t)(block_code<FMT>(x[i + 1], f) << 8 | c0);
+            else
+                codes[p.part.at(i)] = (uint8_t)c0;
         }
     }
 }
-template <int FMT, bool WHOLE>
-__device__ __forceinline__ void restore(const Ckpt &c, const Place<WHOLE> &p, int64_t ld, uint32_t nb,
-                                        float (&x)[kElems<WHOLE>]) {
-    const uint8_t *codes = c.codes + p.row * ld + p.part.col, *scales = c.scales + p.row * nb + p.part.col / 32;
-    if constexpr (WHOLE) {
+template <int FMT, int L>
+__device__ __forceinline__ void restore(const Ckpt &c, const Place<L> &p, int64_t ld, uint32_t nb,
+                                        float (&x)[kElems<L>]) {
+    const uint32_t col = p.part.col;
+    const uint8_t *codes = c.codes + p.row * ld + col, *scales = c.scales + p.row * nb + col / 32;
+    if constexpr (L == kWhole) {
         uint32_t w[4];
         load_words(codes, w);
         const float s = scale_of(__ldg(scales));
 #pragma unroll
         for (int i = 0; i < 4; ++i) values4<FMT>(w[i], s, x + 4 * i);
     } else {
+        constexpr int kStep = L == kPairs ? 2 : 1, kLanes = 32 / kStep;
+        const uint32_t lane = threadIdx.x & 31u, k = lane % kLanes, first = lane - k;
+        const uint32_t lanes = kLanes == 32 ? 0xFFFFFFFFu : 0xFFFFu << first;
+        float mine = 0.0f;   // lane k: the scale of the k-th block
+        if (k < 8 / kStep && (col - kStep * k) + p.part.at((int)k * kStep) < p.part.cols)
+            mine = scale_of(__ldg(scales + k * kStep));
+        uint32_t w[8 / kStep];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = p.part.has(i) ? value_of<FMT>(__ldg(codes + 32 * i), scale_of(__ldg(scales + i))) : 0.0f;
+        for (int i = 0; i < 8; i += kStep) {
+            if constexpr (kStep == 2)
+                w[i / 2] = p.part.has(i) ? __ldg(reinterpret_cast<const uint16_t *>(codes + p.part.at(i))) : 0u;
+            else
+                w[i] = p.part.has(i) ? __ldg(codes + p.part.at(i)) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += kStep) {
+            const float s = __shfl_sync(lanes, mine, first + i / kStep);
+            x[i] = value_of<FMT>(w[i / kStep] & 0xFFu, s);
+            if constexpr (kStep == 2) x[i + 1] = value_of<FMT>(w[i / 2] >> 8, s);
+        }
     }
 }
 
 // ---------------------------------------------------------------- kernels
-template <class T, int FMT, bool WHOLE>
+template <class T, int FMT, int L>
 __global__ void __launch_bounds__(kThreads) k_ckpt_save(const T *__restrict__ x, int64_t ld, Ckpt c, int64_t ldc,
-                                                        uint32_t cols, uint32_t nb, RowDiv units, uint64_t work) {
-    Place<WHOLE> p;
-    if (!place(work, units, cols, p)) return;
-    float v[kElems<WHOLE>] = {};
-    if (!WHOLE || p.part.has(0)) p.part.load(x + p.row * ld, v);
-    keep<FMT, WHOLE>(v, p, c, ldc, nb);
+                                                        uint32_t cols, uint32_t nb, RowDiv parts, uint64_t work) {
+    const uint64_t i = part_index<L>();
+    if (i >= work) return;
+    const Place<L> p(parts, cols, i);
+    float v[kElems<L>] = {};
+    if (L != kWhole || p.part.has(0)) p.part.load(x + p.row * ld, v);
+    keep<FMT, L>(v, p, c, ldc, nb);
 }
 
-template <class T, int FMT, bool WHOLE>
+template <class T, int FMT, int L>
 __global__ void __launch_bounds__(kThreads) k_ckpt_load(Ckpt c, int64_t ldc, T *__restrict__ x, int64_t ld,
-                                                        uint32_t cols, uint32_t nb, RowDiv units, uint64_t work) {
-    Place<WHOLE> p;
-    if (!place(work, units, cols, p) || !p.part.has(0)) return;
-    float v[kElems<WHOLE>];
-    restore<FMT, WHOLE>(c, p, ldc, nb, v);
+                                                        uint32_t cols, uint32_t nb, RowDiv parts, uint64_t work) {
+    const uint64_t i = part_index<L>();
+    if (i >= work) return;
+    const Place<L> p(parts, cols, i);
+    if (L == kWhole && !p.part.has(0)) return;
+    float v[kElems<L>];
+    restore<FMT, L>(c, p, ldc, nb, v);
     p.part.store(x + p.row * ld, v);
 }
 
-template <class Ti, class To, int FMT, bool WHOLE>
+template <class Ti, class To, int FMT, int L>
 __global__ void __launch_bounds__(kThreads) k_swiglu(const Ti *__restrict__ gate, int64_t ld_gate,
                                                      const Ti *__restrict__ up, int64_t ld_up, To *__restrict__ h,
                                                      int64_t ld_h, Ckpt cg, Ckpt cu, int64_t ldc, uint32_t cols,
-                                                     uint32_t nb, RowDiv units, uint64_t work) {
+                                                     uint32_t nb, RowDiv parts, uint64_t work) {
     constexpr bool kExact = std::is_same<To, float>::value;
-    constexpr int N = kElems<WHOLE>;
-    Place<WHOLE> p;
-    if (!place(work, units, cols, p)) return;
+    constexpr int N = kElems<L>;
+    const uint64_t i = part_index<L>();
+    if (i >= work) return;
+    const Place<L> p(parts, cols, i);
     float g[N] = {}, u[N] = {};
-    if (!WHOLE || p.part.has(0)) {
+    if (L != kWhole || p.part.has(0)) {
         p.part.load(gate + p.row * ld_gate, g);
         p.part.load(up + p.row * ld_up, u);
         float o[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = silu<kExact>(g[i]) * u[i];
+        for (int e = 0; e < N; ++e) o[e] = silu<kExact>(g[e]) * u[e];
         p.part.store(h + p.row * ld_h, o);
     }
     if constexpr (FMT != kNone) {
-        keep<FMT, WHOLE>(g, p, cg, ldc, nb);
-        keep<FMT, WHOLE>(u, p, cu, ldc, nb);
+        keep<FMT, L>(g, p, cg, ldc, nb);
+        keep<FMT, L>(u, p, cu, ldc, nb);
     }
 }
 
-template <class Td, class To, int FMT, bool WHOLE>
+template <class Td, class To, int FMT, int L>
 __global__ void __launch_bounds__(kThreads) k_swiglu_bwd(const Td *__restrict__ dh, int64_t ld_dh, Ckpt cg, Ckpt cu,
                                                          int64_t ldc, To *__restrict__ dgate, int64_t ld_dgate,
                                                          To *__restrict__ dup, int64_t ld_dup, uint32_t cols,
-                                                         uint32_t nb, RowDiv units, uint64_t work) {
+                                                         uint32_t nb, RowDiv parts, uint64_t work) {
     constexpr bool kExact = std::is_same<To, float>::value;
-    constexpr int N = kElems<WHOLE>;
-    Place<WHOLE> p;
-    if (!place(work, units, cols, p) || !p.part.has(0)) return;
+    constexpr int N = kElems<L>;
+    const uint64_t i = part_index<L>();
+    if (i >= work) return;
+    const Place<L> p(parts, cols, i);
+    if (L == kWhole && !p.part.has(0)) return;
     float d[N], g[N], u[N];
     p.part.load(dh + p.row * ld_dh, d);
-    restore<FMT, WHOLE>(cg, p, ldc, nb, g);
-    restore<FMT, WHOLE>(cu, p, ldc, nb, u);
+    restore<FMT, L>(cg, p, ldc, nb, g);
+    restore<FMT, L>(cu, p, ldc, nb, u);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float s = sigmoid<kExact>(g[i]), gs = g[i] * s;
-        u[i] = d[i] * u[i] * fmaf(gs, 1.0f - s, s);
-        g[i] = d[i] * gs;
+    for (int e = 0; e < N; ++e) {
+        const float s = sigmoid<kExact>(g[e]), gs = g[e] * s;
+        u[e] = d[e] * u[e] * fmaf(gs, 1.0f - s, s);
+        g[e] = d[e] * gs;
     }
     p.part.store(dgate + p.row * ld_dgate, u);
     p.part.store(dup + p.row * ld_dup, g);
 }
 
 // -------------------------------------------------------------- launching
-// The work over rows x cols in one of the layouts.
+// The work over rows x cols in one of the layouts: the widest that all of
+// `tensors` allow.
+struct Tensor {
+    const void *p;
+    int64_t ld;
+    int dtype;
+};
 struct Grid {
-    bool whole;
+    int layout;
     uint32_t nb;       // blocks of a row
-    RowDiv units;
+    RowDiv parts;
     uint64_t work;
     unsigned ctas;
 };
-Grid grid_of(int64_t rows, int64_t cols, bool aligned) {
+Grid grid_of(int64_t rows, int64_t cols, std::initializer_list<Tensor> tensors) {
+    const auto by = [&](int n) {
+        for (const Tensor &t : tensors)
+            if (!rows_by(t.p, t.ld, type_size(t.dtype), n)) return false;
+        return cols % n == 0;
+    };
     Grid g;
-    g.whole = aligned && cols % 16 == 0;
+    g.layout = by(kElems<kWhole>) ? kWhole : by(2) ? kPairs : kSingles;
     g.nb = (uint32_t)((cols + 31) / 32);
     // a lane pair per block, so that both lanes of a last half block are there
-    const uint32_t units = g.whole ? 2 * g.nb : units_of(false, kElems<false>, cols);
-    g.units = make_rowdiv(units);
-    g.work = (uint64_t)rows * units;
-    g.ctas = (unsigned)(((g.whole ? g.work : g.work * 32) + kThreads - 1) / kThreads);
+    const uint32_t parts = g.layout == kWhole ? 2 * g.nb : parts_of(g.layout, kElems<kSingles>, cols);
+    g.parts = make_rowdiv(parts);
+    g.work = (uint64_t)rows * parts;
+    g.ctas = (unsigned)((threads_of(g.layout, g.work) + kThreads - 1) / kThreads);
     return g;
 }
 template <class F>
+void by_layout(int layout, F f) {
+    if (layout == kWhole) f(Int<kWhole>());
+    else if (layout == kPairs) f(Int<kPairs>());
+    else f(Int<kSingles>());
+}
+template <class F>
 void by_format(int fmt, F f) {
-    if (fmt == kInt8) f(std::integral_constant<int, kInt8>());
-    else f(std::integral_constant<int, kE4M3>());
+    if (fmt == kInt8) f(Int<kInt8>());
+    else f(Int<kE4M3>());
 }
 
 }  // namespace
 
 cudaError_t launch_ckpt_save(const void *x, int dtype, int64_t ld, const Ckpt &c, int fmt, int64_t rows, int64_t cols,
                              cudaStream_t s) {
-    const Grid g = grid_of(rows, cols, whole_rows(x, ld, type_size(dtype), kElems<true>));
+    const Grid g = grid_of(rows, cols, {{x, ld, dtype}});
     by_type(dtype, [&](auto *t) {
         using T = Elem<decltype(t)>;
         by_format(fmt, [&](auto f) {
-            by_bool(g.whole, [&](auto w) {
+            by_layout(g.layout, [&](auto w) {
                 k_ckpt_save<T, decltype(f)::value, decltype(w)::value><<<g.ctas, kThreads, 0, s>>>(
-                    static_cast<const T *>(x), ld, c, ckpt_ld(cols), (uint32_t)cols, g.nb, g.units, g.work);
+                    static_cast<const T *>(x), ld, c, ckpt_ld(cols), (uint32_t)cols, g.nb, g.parts, g.work);
             });
         });
     });
@@ -309,13 +375,13 @@ cudaError_t launch_ckpt_save(const void *x, int dtype, int64_t ld, const Ckpt &c
 
 cudaError_t launch_ckpt_load(const Ckpt &c, int fmt, int64_t rows, int64_t cols, void *x, int dtype, int64_t ld,
                              cudaStream_t s) {
-    const Grid g = grid_of(rows, cols, whole_rows(x, ld, type_size(dtype), kElems<true>));
+    const Grid g = grid_of(rows, cols, {{x, ld, dtype}});
     by_type(dtype, [&](auto *t) {
         using T = Elem<decltype(t)>;
         by_format(fmt, [&](auto f) {
-            by_bool(g.whole, [&](auto w) {
+            by_layout(g.layout, [&](auto w) {
                 k_ckpt_load<T, decltype(f)::value, decltype(w)::value><<<g.ctas, kThreads, 0, s>>>(
-                    c, ckpt_ld(cols), static_cast<T *>(x), ld, (uint32_t)cols, g.nb, g.units, g.work);
+                    c, ckpt_ld(cols), static_cast<T *>(x), ld, (uint32_t)cols, g.nb, g.parts, g.work);
             });
         });
     });
@@ -325,20 +391,18 @@ cudaError_t launch_ckpt_load(const Ckpt &c, int fmt, int64_t rows, int64_t cols,
 cudaError_t launch_swiglu(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int in_dtype,
                           int64_t rows, int64_t cols, void *h, int h_dtype, int64_t ld_h, const Ckpt &cg,
                           const Ckpt &cu, int fmt, cudaStream_t s) {
-    const Grid gr = grid_of(rows, cols, whole_rows(gate, ld_gate, type_size(in_dtype), kElems<true>) &&
-                                            whole_rows(up, ld_up, type_size(in_dtype), kElems<true>) &&
-                                            whole_rows(h, ld_h, type_size(h_dtype), kElems<true>));
+    const Grid gr = grid_of(rows, cols, {{gate, ld_gate, in_dtype}, {up, ld_up, in_dtype}, {h, ld_h, h_dtype}});
     by_type(in_dtype, [&](auto *ti) {
         using Ti = Elem<decltype(ti)>;
         by_type(h_dtype, [&](auto *to) {
             using To = Elem<decltype(to)>;
-            by_bool(gr.whole, [&](auto w) {
+            by_layout(gr.layout, [&](auto w) {
                 auto go = [&](auto f) {
                     k_swiglu<Ti, To, decltype(f)::value, decltype(w)::value><<<gr.ctas, kThreads, 0, s>>>(
                         static_cast<const Ti *>(gate), ld_gate, static_cast<const Ti *>(up), ld_up,
-                        static_cast<To *>(h), ld_h, cg, cu, ckpt_ld(cols), (uint32_t)cols, gr.nb, gr.units, gr.work);
+                        static_cast<To *>(h), ld_h, cg, cu, ckpt_ld(cols), (uint32_t)cols, gr.nb, gr.parts, gr.work);
                 };
-                if (fmt == kNone) go(std::integral_constant<int, kNone>());
+                if (fmt == kNone) go(Int<kNone>());
                 else by_format(fmt, go);
             });
         });
@@ -349,18 +413,16 @@ cudaError_t launch_swiglu(const void *gate, int64_t ld_gate, const void *up, int
 cudaError_t launch_swiglu_bwd(const void *dh, int dh_dtype, int64_t ld_dh, const Ckpt &cg, const Ckpt &cu, int fmt,
                               int64_t rows, int64_t cols, void *dgate, int64_t ld_dgate, void *dup, int64_t ld_dup,
                               int out_dtype, cudaStream_t s) {
-    const Grid g = grid_of(rows, cols, whole_rows(dh, ld_dh, type_size(dh_dtype), kElems<true>) &&
-                                           whole_rows(dgate, ld_dgate, type_size(out_dtype), kElems<true>) &&
-                                           whole_rows(dup, ld_dup, type_size(out_dtype), kElems<true>));
+    const Grid g = grid_of(rows, cols, {{dh, ld_dh, dh_dtype}, {dgate, ld_dgate, out_dtype}, {dup, ld_dup, out_dtype}});
     by_type(dh_dtype, [&](auto *td) {
         using Td = Elem<decltype(td)>;
         by_type(out_dtype, [&](auto *to) {
             using To = Elem<decltype(to)>;
             by_format(fmt, [&](auto f) {
-                by_bool(g.whole, [&](auto w) {
+                by_layout(g.layout, [&](auto w) {
                     k_swiglu_bwd<Td, To, decltype(f)::value, decltype(w)::value><<<g.ctas, kThreads, 0, s>>>(
                         static_cast<const Td *>(dh), ld_dh, cg, cu, ckpt_ld(cols), static_cast<To *>(dgate), ld_dgate,
-                        static_cast<To *>(dup), ld_dup, (uint32_t)cols, g.nb, g.units, g.work);
+                        static_cast<To *>(dup), ld_dup, (uint32_t)cols, g.nb, g.parts, g.work);
                 });
             });
         });

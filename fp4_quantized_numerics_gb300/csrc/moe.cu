@@ -190,53 +190,68 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *__restric
 }
 
 // ---------------------------------------------------------------- combine
-// A thread owns 8 elements of an output row; the topk rows are added in
+// A thread owns N elements of an output row; the topk rows are added in
 // ascending order of choice, in fp32.
-template <class Ty, class To, bool WHOLE>
+template <class Ty, class To, int L, int N>
 __global__ void __launch_bounds__(kThreads) k_moe_combine(const Ty *__restrict__ y, int64_t ld_y,
                                                           const int32_t *__restrict__ pos,
                                                           const float *__restrict__ weights,
                                                           const int64_t *__restrict__ routed_at, To *__restrict__ out,
-                                                          int64_t ld_out, int topk, uint32_t hidden, RowDiv units,
+                                                          int64_t ld_out, int topk, uint32_t hidden, RowDiv parts,
                                                           uint64_t work) {
     uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-    if constexpr (!WHOLE) i /= 32;
+    if (L != kWhole) i /= 32;
     if (i >= work) return;
-    const uint64_t t = row_of(i, units);
-    const uint32_t u = (uint32_t)(i - t * units.d);
-    const Part<WHOLE, 8> part{WHOLE ? u * 8 : u * 256 + (threadIdx.x & 31u), hidden};
+    const uint64_t t = row_of(i, parts);
+    const Part<L, N> part((uint32_t)(i - t * parts.d), hidden);
     const int32_t routed = (int32_t)__ldg(routed_at);
-    float acc[8] = {};
-#pragma unroll 4
+    float acc[N] = {};
+#pragma unroll(L == kWhole ? 4 : 1)
     for (int j = 0; j < topk; ++j) {
         const int32_t p = __ldg(pos + t * topk + j);
         if (p >= routed) continue;
         const float w = weights ? __ldg(weights + t * topk + j) : 1.0f;
-        float v[8];
+        float v[N];
         part.load(y + (int64_t)p * ld_y, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+        for (int e = 0; e < N; ++e) acc[e] = fmaf(w, v[e], acc[e]);
     }
     part.store(out + t * ld_out, acc);
 }
 
 // ------------------------------------------------------ combine's gradient
-// G threads per token (32, 64 or 128): they read dout's row once per kBatch
-// choices, write the scaled copies and keep the choices' dot products in
-// registers; a butterfly over the warp that halves the number of sums at each
-// step, then one addition per warp in shared memory, joins them in an order
-// that depends on nothing but the sizes.
+// G threads per token: they read dout's row once per
+// kBatch choices, write the scaled copies and keep the choices' dot products
+// in registers; a butterfly over the warp that halves the number of sums at
+// each step, then one addition per warp in shared memory, joins them in an
+// order that depends on nothing but the sizes and the layout.
 constexpr int kBatch = 4;
 
-template <class Td, class Ty, class To, bool WHOLE, int G>
+// Elements of a thread: 32 bytes of y in the whole layout.
+template <class Ty, int L>
+constexpr int kBwdElems = L == kWhole && sizeof(Ty) == 2 ? 16 : 8;
+
+// y's elements of one part: raw in the whole layout, else as fp32.
+template <class Ty, int L, int N>
+struct Held {
+    std::conditional_t<L == kWhole, Raw<Ty, N>, float[N]> v;
+    __device__ __forceinline__ void load(const Part<L, N> &part, const Ty *row) {
+        if constexpr (L == kWhole) v.load(row + part.col);
+        else part.load(row, v);
+    }
+};
+
+template <class Td, class Ty, class To, int L, uint32_t G>
 __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(
     const Td *__restrict__ dout, int64_t ld_dout, const Ty *__restrict__ y, int64_t ld_y,
     const int32_t *__restrict__ pos, const float *__restrict__ weights, const int64_t *__restrict__ routed_at,
-    To *__restrict__ dy, int64_t ld_dy, float *__restrict__ dw, int topk, uint32_t hidden, uint32_t tokens) {
-    constexpr int kWarps = G / 32;
+    To *__restrict__ dy, int64_t ld_dy, float *__restrict__ dw, int topk, uint32_t hidden, uint32_t parts,
+    uint32_t tokens) {
+    constexpr int N = kBwdElems<Ty, L>;
     __shared__ float sums[kThreads / 32][kBatch];
-    const uint32_t lane = threadIdx.x & 31u, in_group = threadIdx.x % G, group = threadIdx.x / G;
-    const uint32_t t = blockIdx.x * (kThreads / G) + group;
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x / 32;
+    const uint32_t mine = threadIdx.x / G, in_group = threadIdx.x % G;
+    const uint32_t t = blockIdx.x * (kThreads / G) + mine;
     const bool live = t < tokens;
     const int32_t routed = (int32_t)__ldg(routed_at);
     for (int j0 = 0; j0 < topk; j0 += kBatch) {
@@ -249,55 +264,49 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(
             w[j] = in && p[j] < routed ? __ldg(weights + (int64_t)t * topk + j0 + j) : 0.0f;
             dot[j] = 0.0f;
         }
-        // the part's first element; the warp's segments are 256 elements
-        uint32_t c = WHOLE ? in_group * 8 : in_group / 32 * 256 + lane;
-        for (; live && c < (WHOLE ? hidden : (hidden + 255) / 256 * 256); c += G * 8) {
-            const Part<WHOLE, 8> part{c, hidden};
-            float d[8], v[kBatch][8];
-            part.load(dout + (int64_t)t * ld_dout, d);
+        if (live)
+            for (uint32_t u = L == kWhole ? in_group : in_group / 32; u < parts;
+                 u += L == kWhole ? G : G / 32) {
+                const Part<L, N> part(u, hidden);
+                Held<Td, L, N> d;
+                Held<Ty, L, N> v[kBatch];
+                d.load(part, dout + (int64_t)t * ld_dout);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-                if (p[j] >= 0 && p[j] < routed) part.load(y + (int64_t)p[j] * ld_y, v[j]);
+                for (int j = 0; j < kBatch; ++j)
+                    if (p[j] >= 0 && p[j] < routed) v[j].load(part, y + (int64_t)p[j] * ld_y);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                if (p[j] < 0) continue;
-                float o[8] = {};
-                if (p[j] < routed) {
+                for (int j = 0; j < kBatch; ++j) {
+                    if (p[j] < 0) continue;
+                    float o[N] = {};
+                    if (p[j] < routed) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        o[e] = w[j] * d[e];
-                        dot[j] = fmaf(d[e], v[j][e], dot[j]);
+                        for (int e = 0; e < N; ++e) {
+                            o[e] = w[j] * d.v[e];
+                            dot[j] = fmaf(d.v[e], v[j].v[e], dot[j]);
+                        }
                     }
+                    part.store(dy + (int64_t)p[j] * ld_dy, o);
                 }
-                part.store(dy + (int64_t)p[j] * ld_dy, o);
             }
-        }
         // kBatch = 4 sums over 32 lanes: two steps that halve their number,
         // three that add; lanes 0, 8, 16, 24 hold sums 0, 1, 2, 3
-        float s = 0.0f;
-        {
-            const bool h16 = lane & 16u, h8 = lane & 8u;
-            const float a = (h16 ? dot[2] : dot[0]) + __shfl_xor_sync(0xFFFFFFFFu, h16 ? dot[0] : dot[2], 16);
-            const float b = (h16 ? dot[3] : dot[1]) + __shfl_xor_sync(0xFFFFFFFFu, h16 ? dot[1] : dot[3], 16);
-            s = (h8 ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, h8 ? a : b, 8);
+        const bool h16 = lane & 16u, h8 = lane & 8u;
+        const float a = (h16 ? dot[2] : dot[0]) + __shfl_xor_sync(0xFFFFFFFFu, h16 ? dot[0] : dot[2], 16);
+        const float b = (h16 ? dot[3] : dot[1]) + __shfl_xor_sync(0xFFFFFFFFu, h16 ? dot[1] : dot[3], 16);
+        float s = (h8 ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, h8 ? a : b, 8);
 #pragma unroll
-            for (int m = 4; m; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
-        }
-        const int mine = (int)(lane >> 3);
-        const bool has = live && (lane & 7u) == 0 && j0 + mine < topk;
-        if constexpr (kWarps == 1) {
-            if (has) dw[(int64_t)t * topk + j0 + mine] = s;
-        } else {
-            if ((lane & 7u) == 0) sums[threadIdx.x / 32][mine] = s;
-            __syncthreads();
-            if (has && in_group < 32) {
-                float all = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) all += sums[group * kWarps + k][mine];
-                dw[(int64_t)t * topk + j0 + mine] = all;
-            }
+        for (int m = 4; m; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
+        const int k = (int)(lane >> 3);
+        if (G > 32) {
+            if ((lane & 7u) == 0) sums[warp][k] = s;
             __syncthreads();
         }
+        if (live && in_group < 32 && (lane & 7u) == 0 && j0 + k < topk) {
+#pragma unroll
+            for (uint32_t o = 1; o < G / 32; ++o) s += sums[warp + o][k];
+            dw[(int64_t)t * topk + j0 + k] = s;
+        }
+        if (G > 32) __syncthreads();
     }
 }
 
@@ -307,19 +316,13 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(
 // 9.0 / 5.8 / 6.0 us, 98304 slots 72 / 14 / 10 us.
 int sort_ctas(uint32_t n) { return n <= 1024 ? 1 : n <= 8192 ? 8 : kMaxSortCtas; }
 
-// Threads per token of combine's gradient: as many as have 8 elements each,
-// at most 128.  Measured (32 / 64 / 128 / 256): 16384 tokens x 6 of 2048
-// 195 / 189 / 190 / 214 us, 128 tokens 9.4 / 6.2 / 4.3 / 3.8 us, 8192 x 2 of
-// 8192 129 / 120 / 120 / 129 us.
-int bwd_group(int64_t hidden) { return hidden <= 256 ? 32 : hidden <= 512 ? 64 : 128; }
-
 inline uint64_t ctas(uint64_t work) { return (work + kThreads - 1) / kThreads; }
 
 template <class Unit, int N>
 void dispatch(const void *x, int64_t ldx, void *xs, int64_t ldxs, int64_t row_bytes, const MoePlan &m,
               cudaStream_t s) {
     const int64_t size = sizeof(Unit);
-    const uint32_t width = (uint32_t)(row_bytes / size), units = N > 1 ? units_of(false, N, width) : width;
+    const uint32_t width = (uint32_t)(row_bytes / size), units = N > 1 ? parts_of(kSingles, N, width) : width;
     const uint64_t work = (uint64_t)m.tokens * units;
     k_moe_dispatch<Unit, N><<<(unsigned)ctas(work * (N > 1 ? 32 : 1)), kThreads, 0, s>>>(
         static_cast<const Unit *>(x), ldx / size, static_cast<Unit *>(xs), ldxs / size, m.pos,
@@ -367,20 +370,27 @@ cudaError_t launch_moe_dispatch(const void *x, int dtype, int64_t hidden, int64_
 
 cudaError_t launch_moe_combine(const void *y, int y_dtype, int64_t hidden, int64_t ld_y, const MoePlan &m,
                                const float *weights, void *out, int out_dtype, int64_t ld_out, cudaStream_t s) {
-    const bool whole = hidden % 8 == 0 && whole_rows(y, ld_y, type_size(y_dtype), 8) &&
-                       whole_rows(out, ld_out, type_size(out_dtype), 8);
-    const uint32_t units = units_of(whole, 8, hidden);
-    const uint64_t work = (uint64_t)m.tokens * units;
-    by_type(y_dtype, [&](auto *yp) {
+    auto go = [&](auto *yp, auto *op, auto layout, auto elems) {
+        constexpr int L = decltype(layout)::value, N = decltype(elems)::value;
+        const uint32_t parts = parts_of(L, N, hidden);
+        const uint64_t work = (uint64_t)m.tokens * parts;
         using Ty = Elem<decltype(yp)>;
+        using To = Elem<decltype(op)>;
+        k_moe_combine<Ty, To, L, N><<<(unsigned)ctas(threads_of(L, work)), kThreads, 0, s>>>(
+            static_cast<const Ty *>(y), ld_y, m.pos, weights, m.offsets + m.n_experts, static_cast<To *>(out), ld_out,
+            m.topk, (uint32_t)hidden, make_rowdiv(parts), work);
+    };
+    const auto by = [&](int n) {
+        return hidden % n == 0 && rows_by(y, ld_y, type_size(y_dtype), n) &&
+               rows_by(out, ld_out, type_size(out_dtype), n);
+    };
+    by_type(y_dtype, [&](auto *yp) {
         by_type(out_dtype, [&](auto *op) {
-            using To = Elem<decltype(op)>;
-            by_bool(whole, [&](auto w) {
-                k_moe_combine<Ty, To, decltype(w)::value>
-                    <<<(unsigned)ctas(whole ? work : work * 32), kThreads, 0, s>>>(
-                        static_cast<const Ty *>(y), ld_y, m.pos, weights, m.offsets + m.n_experts,
-                        static_cast<To *>(out), ld_out, m.topk, (uint32_t)hidden, make_rowdiv(units), work);
-            });
+            // 32 bytes of y a thread
+            if (y_dtype == 0 && by(16)) go(yp, op, Int<kWhole>(), Int<16>());
+            else if (by(8)) go(yp, op, Int<kWhole>(), Int<8>());
+            else if (by(2)) go(yp, op, Int<kPairs>(), Int<8>());
+            else go(yp, op, Int<kSingles>(), Int<8>());
         });
     });
     return cudaGetLastError();
@@ -389,28 +399,38 @@ cudaError_t launch_moe_combine(const void *y, int y_dtype, int64_t hidden, int64
 cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_dout, const void *y, int y_dtype,
                                    int64_t ld_y, int64_t hidden, const MoePlan &m, const float *weights, void *dy,
                                    int dy_dtype, int64_t ld_dy, float *dw, cudaStream_t s) {
-    const bool whole = hidden % 8 == 0 && whole_rows(dout, ld_dout, type_size(dout_dtype), 8) &&
-                       whole_rows(y, ld_y, type_size(y_dtype), 8) && whole_rows(dy, ld_dy, type_size(dy_dtype), 8);
-    const int G = bwd_group(hidden);
+    const auto by = [&](int n) {
+        return hidden % n == 0 && rows_by(dout, ld_dout, type_size(dout_dtype), n) &&
+               rows_by(y, ld_y, type_size(y_dtype), n) && rows_by(dy, ld_dy, type_size(dy_dtype), n);
+    };
     by_type(dout_dtype, [&](auto *dp) {
         using Td = Elem<decltype(dp)>;
         by_type(y_dtype, [&](auto *yp) {
             using Ty = Elem<decltype(yp)>;
             by_type(dy_dtype, [&](auto *op) {
                 using To = Elem<decltype(op)>;
-                by_bool(whole, [&](auto w) {
-                    auto go = [&](auto g) {
-                        constexpr int kG = decltype(g)::value;
-                        const unsigned grid = (unsigned)((m.tokens + kThreads / kG - 1) / (kThreads / kG));
-                        k_moe_combine_bwd<Td, Ty, To, decltype(w)::value, kG><<<grid, kThreads, 0, s>>>(
+                auto go = [&](auto layout) {
+                    constexpr int L = decltype(layout)::value, N = kBwdElems<Ty, L>;
+                    const uint32_t parts = parts_of(L, N, hidden);
+                    auto with = [&](auto group) {
+                        constexpr uint32_t G = decltype(group)::value;
+                        k_moe_combine_bwd<Td, Ty, To, L, G><<<(unsigned)ctas((uint64_t)m.tokens * G), kThreads, 0, s>>>(
                             static_cast<const Td *>(dout), ld_dout, static_cast<const Ty *>(y), ld_y, m.pos, weights,
                             m.offsets + m.n_experts, static_cast<To *>(dy), ld_dy, dw, m.topk, (uint32_t)hidden,
-                            (uint32_t)m.tokens);
+                            parts, (uint32_t)m.tokens);
                     };
-                    if (G == 32) go(std::integral_constant<int, 32>());
-                    else if (G == 64) go(std::integral_constant<int, 64>());
-                    else go(std::integral_constant<int, 128>());
-                });
+                    // 128 threads a token unless most would idle.  Measured
+                    // (32 / 64 / 128 / 256, rows of 2048): 16384 tokens x 6
+                    // 195 / 189 / 190 / 214 us, 128 tokens 9.4 / 6.2 / 4.3 /
+                    // 3.8 us; the count is a constant of the kernel, which
+                    // lets its loop over the row be unrolled (8192 x 2 of
+                    // 8192 BF16: 115 us with a variable, 103 us so).
+                    if (threads_of(L, parts) <= 64) with(Int<32>());
+                    else with(Int<128>());
+                };
+                if (by(kBwdElems<Ty, kWhole>)) go(Int<kWhole>());
+                else if (by(2)) go(Int<kPairs>());
+                else go(Int<kSingles>());
             });
         });
     });

@@ -2,13 +2,13 @@
 // GEMMs (moe.cu, activation.cu): how a thread finds and reads its part of a
 // row, and the division that turns a flat work index into (row, part).
 //
-// Two layouts, chosen by alignment (`whole`):
-//  * whole: a thread owns N consecutive elements, in accesses of 16 or 32
+// Three layouts, chosen by alignment:
+//  * kWhole: a thread owns N consecutive elements, in accesses of 16 or 32
 //    bytes on such boundaries; rows are multiples of N long.
-//  * strided (anything else): a warp owns 32 N consecutive elements of a row,
-//    lane l the elements l, l + 32, ...: every access of the warp is one run
-//    of neighbouring elements, whatever the row's alignment, and the work of
-//    finding the place is shared by N elements.
+//  * kPairs (rows on two-element boundaries, of even length) and kSingles
+//    (anything): a warp owns 32 N consecutive elements of a row, a lane two
+//    neighbours (or one) of every 64 (32): every access of the warp is one run
+//    of neighbouring elements, and finding the place is shared by N elements.
 #pragma once
 
 #include <cstdint>
@@ -49,25 +49,37 @@ __device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[8]) {
 }
 
 // ------------------------------------------- N consecutive elements as fp32
-template <int N>
-__device__ __forceinline__ void load_whole(const __nv_bfloat16 *p, float (&f)[N]) {
-    uint32_t w[N / 2];
-    load_words(p, w);
+// As they lie in memory (N of 16 bits, or 8 of 32 bits a half): what a thread
+// holds while a load is under way.
+template <class T, int N>
+struct Raw {
+    uint32_t w[N * sizeof(T) / 4];
+    __device__ __forceinline__ void load(const T *p) {
+        constexpr int kWords = N * sizeof(T) / 4;
+        if constexpr (kWords <= 8) {
+            load_words(p, w);
+        } else {
+            uint32_t a[8], b[8];
+            load_words(p, a);
+            load_words(p + 8, b);
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            for (int i = 0; i < 8; ++i) {
+                w[i] = a[i];
+                w[8 + i] = b[i];
+            }
+        }
     }
-}
-template <int N>
-__device__ __forceinline__ void load_whole(const float *p, float (&f)[N]) {
-#pragma unroll
-    for (int h = 0; h < N / 8; ++h) {
-        uint32_t w[8];
-        load_words(p + 8 * h, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[8 * h + i] = __uint_as_float(w[i]);
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
     }
+};
+template <int N, class T>
+__device__ __forceinline__ void load_whole(const T *p, float (&f)[N]) {
+    Raw<T, N> r;
+    r.load(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = r[i];
 }
 // Rounds to nearest even, once, on the way out.
 template <int N>
@@ -95,48 +107,83 @@ __device__ __forceinline__ float load_one(const __nv_bfloat16 *p) {
     return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p)) << 16);
 }
 __device__ __forceinline__ float load_one(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float2 load_two(const __nv_bfloat16 *p) {
+    const uint32_t w = __ldg(reinterpret_cast<const unsigned int *>(p));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 load_two(const float *p) { return __ldg(reinterpret_cast<const float2 *>(p)); }
 __device__ __forceinline__ void store_one(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_two(__nv_bfloat16 *p, float a, float b) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(a, b);
+}
+__device__ __forceinline__ void store_two(float *p, float a, float b) {
+    *reinterpret_cast<float2 *>(p) = make_float2(a, b);
+}
 
 // ---------------------------------------------------------- a thread's part
-// Elements col, col + kStep, ... of a row of `cols` (those below cols; in the
-// whole layout all N or none).
-template <bool WHOLE, int N>
+constexpr int kWhole = 0, kPairs = 1, kSingles = 2;
+
+// N elements of a row of `cols`, from `col`: those for which has(i).
+template <int L, int N>
 struct Part {
-    static constexpr uint32_t kStep = WHOLE ? 1 : 32;
     uint32_t col, cols;
 
-    __device__ __forceinline__ bool has(int i) const { return col + i * kStep < cols; }
+    // Part u of a row (kWhole: this thread's; else this warp's).
+    __device__ __forceinline__ Part(uint32_t u, uint32_t cols_) : cols(cols_) {
+        const uint32_t lane = threadIdx.x & 31u;
+        col = L == kWhole ? u * N : u * (32 * N) + (L == kPairs ? 2 * lane : lane);
+    }
+    // Offset of element i from col.
+    static __device__ __forceinline__ constexpr uint32_t at(int i) {
+        return L == kWhole ? i : L == kPairs ? i / 2 * 64 + i % 2 : i * 32;
+    }
+    __device__ __forceinline__ bool has(int i) const { return col + at(i) < cols; }
     template <class T>
     __device__ __forceinline__ void load(const T *row, float (&f)[N]) const {
-        if constexpr (WHOLE) {
-            load_whole<N>(row + col, f);
+        const T *p = row + col;
+        if constexpr (L == kWhole) {
+            load_whole<N>(p, f);
+        } else if constexpr (L == kPairs) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float2 v = has(i) ? load_two(p + at(i)) : make_float2(0.0f, 0.0f);
+                f[i] = v.x;
+                f[i + 1] = v.y;
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = has(i) ? load_one(row + col + i * kStep) : 0.0f;
+            for (int i = 0; i < N; ++i) f[i] = has(i) ? load_one(p + at(i)) : 0.0f;
         }
     }
     template <class T>
     __device__ __forceinline__ void store(T *row, const float (&f)[N]) const {
-        if constexpr (WHOLE) {
-            store_whole<N>(row + col, f);
+        T *p = row + col;
+        if constexpr (L == kWhole) {
+            store_whole<N>(p, f);
+        } else if constexpr (L == kPairs) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2)
+                if (has(i)) store_two(p + at(i), f[i], f[i + 1]);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i)
-                if (has(i)) store_one(row + col + i * kStep, f[i]);
+                if (has(i)) store_one(p + at(i), f[i]);
         }
     }
 };
 
-// Units of work in a row: threads' parts (whole) or warps' segments.
-inline uint32_t units_of(bool whole, int n, int64_t cols) {
-    const int64_t per = whole ? n : 32 * n;
+// Parts of a row.
+inline uint32_t parts_of(int layout, int n, int64_t cols) {
+    const int64_t per = layout == kWhole ? n : 32 * n;
     return (uint32_t)((cols + per - 1) / per);
 }
+// Threads of `parts` parts.
+inline uint64_t threads_of(int layout, uint64_t parts) { return layout == kWhole ? parts : parts * 32; }
 
-// Whether a tensor (row stride ld elements of esz bytes) allows whole parts of
-// n elements: its accesses are n * esz bytes, at most 32.
-inline bool whole_rows(const void *p, int64_t ld, size_t esz, int n) {
+// Whether a tensor (row stride ld elements of esz bytes) can be accessed n
+// elements at a time, in at most 32 bytes.
+inline bool rows_by(const void *p, int64_t ld, size_t esz, int n) {
     const size_t a = n * esz < 32 ? n * esz : 32;
     return reinterpret_cast<uintptr_t>(p) % a == 0 && (size_t)ld * esz % a == 0;
 }
@@ -149,9 +196,7 @@ auto by_type(int dtype, F f) {
 inline size_t type_size(int dtype) { return dtype == 0 ? 2 : 4; }
 template <class P>
 using Elem = std::remove_pointer_t<P>;
-template <class F>
-auto by_bool(bool b, F f) {
-    return b ? f(std::true_type()) : f(std::false_type());
-}
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 }  // namespace ufp4

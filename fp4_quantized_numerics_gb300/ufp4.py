@@ -485,6 +485,15 @@ def ufp4_gemm_grouped(a, b, groups, stream=None):
 
 
 # ------------------------------------------- around the grouped GEMMs (MoE)
+# These calls are also made a token at a time, where the binding's own time
+# counts: one stream query without a Stream object, no second check of
+# buffers made here.
+def _raw_stream(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
+
+
 class MoePlan:
     """Expert order of a routed batch (layouts: include/ufp4.h): pos int32
     [tokens, topk], src int32 [tokens * topk], counts int64 [n_experts],
@@ -500,48 +509,60 @@ class MoePlan:
                 raise ValueError("%s must be contiguous, %s, of %d elements" % (name, dtype, n))
         if pos.dim() != 2:
             raise ValueError("pos must be [tokens, topk]")
+        self._set(pos, src, counts, offsets, pos.shape[0], pos.shape[1], counts.numel())
+
+    def _set(self, pos, src, counts, offsets, tokens, topk, n_experts):
         self.pos, self.src, self.counts, self.offsets = pos, src, counts, offsets
-        self.tokens, self.topk = pos.shape
-        self.n_experts = counts.numel()
-        self._c = MoePlanC(pos.data_ptr(), src.data_ptr(), counts.data_ptr(), offsets.data_ptr(), self.tokens,
-                           self.topk, self.n_experts, 0)
+        self.tokens, self.topk, self.n_experts = tokens, topk, n_experts
+        self._c = ctypes.byref(MoePlanC(pos.data_ptr(), src.data_ptr(), counts.data_ptr(), offsets.data_ptr(),
+                                        tokens, topk, n_experts, 0))
 
     @classmethod
     def empty(cls, tokens, topk, n_experts, device="cuda"):
-        new = lambda n, dtype: torch.empty(n, dtype=dtype, device=device)  # noqa: E731
-        return cls(new((tokens, topk), torch.int32), new(tokens * topk, torch.int32), new(n_experts, torch.int64),
-                   new(n_experts + 1, torch.int64))
+        plan = cls.__new__(cls)
+        plan._set(torch.empty((tokens, topk), dtype=torch.int32, device=device),
+                  torch.empty(tokens * topk, dtype=torch.int32, device=device),
+                  torch.empty(n_experts, dtype=torch.int64, device=device),
+                  torch.empty(n_experts + 1, dtype=torch.int64, device=device), tokens, topk, n_experts)
+        return plan
 
     def c(self):
-        return ctypes.byref(self._c)
+        return self._c
 
 
 def _rows2d(t, name, rows=None, cols=None):
-    """A 2-D CUDA tensor with unit stride in its last dim, of the given shape."""
-    _cuda(t, name)
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError("%s must be 2-D with unit stride in its last dim" % name)
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError("%s must be %s x %s, got %d x %d" % (name, rows, cols, *t.shape))
-    return t
-
-
-def _ld(t):
-    # the stride of a one-row tensor says nothing; the C call wants ld >= cols
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    """Checks a 2-D CUDA tensor with unit stride in its last dim, of the given
+    shape.  Returns its pointer, dtype code, row stride, rows and cols."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        _cuda(t, name)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s must be 2-D" % name)
+    r, c = shape
+    ld, unit = t.stride()
+    if unit != 1 and c > 1:
+        raise ValueError("%s must have unit stride in its last dim" % name)
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError("%s must be %s x %s, got %d x %d" % (name, rows, cols, r, c))
+    if r <= 1 and ld < c:   # the stride of a single row says nothing
+        ld = c
+    return t.data_ptr(), _dtype_code(t), ld, r, c
 
 
 def _result(out, name, rows, cols, dtype, device):
+    """A fresh rows x cols result, or the caller's, checked: the tensor, its
+    pointer, dtype code and row stride."""
     if out is None:
-        return torch.empty(rows, cols, dtype=dtype, device=device)
-    return _rows2d(out, name, rows, cols)
+        out = torch.empty((rows, cols), dtype=dtype, device=device)
+        return out, out.data_ptr(), _dtype_code(out), cols
+    p, dt, ld, _, _ = _rows2d(out, name, rows, cols)
+    return out, p, dt, ld
 
 
-def _plan_weights(weights, plan):
-    _cuda(weights, "weights")
-    if weights.dtype != torch.float32 or tuple(weights.shape) != (plan.tokens, plan.topk) or \
-            not weights.is_contiguous():
-        raise ValueError("weights must be contiguous fp32 [tokens, topk]")
+def _plan_weights(weights, plan, name="weights"):
+    _cuda(weights, name)
+    if weights.dtype != torch.float32 or weights.shape != plan.pos.shape or not weights.is_contiguous():
+        raise ValueError("%s must be contiguous fp32 [tokens, topk]" % name)
     return weights.data_ptr()
 
 
@@ -551,13 +572,15 @@ def ufp4_moe_sort(ids, n_experts, out=None, stream=None):
     _cuda(ids, "ids")
     if ids.dim() != 2 or not ids.is_contiguous():
         raise ValueError("ids must be contiguous [tokens, topk]")
-    if ids.dtype not in (torch.int32, torch.int64):
+    size = 8 if ids.dtype == torch.int64 else 4 if ids.dtype == torch.int32 else 0
+    if not size:
         raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
+    tokens, topk = ids.shape
     if out is None:
-        out = MoePlan.empty(ids.shape[0], ids.shape[1], n_experts, ids.device)
-    elif (out.tokens, out.topk, out.n_experts) != (*ids.shape, n_experts):
+        out = MoePlan.empty(tokens, topk, n_experts, ids.device)
+    elif (out.tokens, out.topk, out.n_experts) != (tokens, topk, n_experts):
         raise ValueError("out is a plan of another size")
-    st = lib().ufp4_moe_sort(ids.data_ptr(), ids.element_size(), out.c(), _stream(stream))
+    st = lib().ufp4_moe_sort(ids.data_ptr(), size, out._c, _raw_stream(stream))
     _check(st, "ufp4_moe_sort")
     return out
 
@@ -565,12 +588,11 @@ def ufp4_moe_sort(ids, n_experts, out=None, stream=None):
 def ufp4_moe_dispatch(x, plan, out=None, stream=None):
     """x ([tokens, hidden]) in expert order: [tokens * topk, hidden], dropped
     slots' rows (the last ones) zero.  Gradient: ufp4_moe_combine(dxs, plan)."""
-    _rows2d(x, "x", plan.tokens)
-    out = _result(out, "out", plan.tokens * plan.topk, x.shape[1], x.dtype, x.device)
-    if out.dtype != x.dtype:
+    xp, dt, ld, _, hidden = _rows2d(x, "x", plan.tokens)
+    out, op, odt, old = _result(out, "out", plan.tokens * plan.topk, hidden, x.dtype, x.device)
+    if odt != dt:
         raise TypeError("out must have x's dtype")
-    st = lib().ufp4_moe_dispatch(x.data_ptr(), _dtype_code(x), x.shape[1], _ld(x), plan.c(), out.data_ptr(),
-                                 _ld(out), _stream(stream))
+    st = lib().ufp4_moe_dispatch(xp, dt, hidden, ld, plan._c, op, old, _raw_stream(stream))
     _check(st, "ufp4_moe_dispatch")
     return out
 
@@ -579,11 +601,10 @@ def ufp4_moe_combine(y, plan, weights=None, dtype=None, out=None, stream=None):
     """y ([tokens * topk, hidden], expert order) back in token order: the sum
     over each token's routed slots, times weights ([tokens, topk] fp32) if
     given.  dtype: the result's (y's by default)."""
-    _rows2d(y, "y", plan.tokens * plan.topk)
+    yp, dt, ld, _, hidden = _rows2d(y, "y", plan.tokens * plan.topk)
     w = None if weights is None else _plan_weights(weights, plan)
-    out = _result(out, "out", plan.tokens, y.shape[1], y.dtype if dtype is None else dtype, y.device)
-    st = lib().ufp4_moe_combine(y.data_ptr(), _dtype_code(y), y.shape[1], _ld(y), plan.c(), w, out.data_ptr(),
-                                _dtype_code(out), _ld(out), _stream(stream))
+    out, op, odt, old = _result(out, "out", plan.tokens, hidden, dtype or y.dtype, y.device)
+    st = lib().ufp4_moe_combine(yp, dt, hidden, ld, plan._c, w, op, odt, old, _raw_stream(stream))
     _check(st, "ufp4_moe_combine")
     return out
 
@@ -591,15 +612,14 @@ def ufp4_moe_combine(y, plan, weights=None, dtype=None, out=None, stream=None):
 def ufp4_moe_combine_bwd(dout, y, plan, weights, dtype=None, dy=None, dw=None, stream=None):
     """Gradients of ufp4_moe_combine(y, plan, weights): (dy, dw).  dtype: dy's
     (dout's by default)."""
-    _rows2d(y, "y", plan.tokens * plan.topk)
-    _rows2d(dout, "dout", plan.tokens, y.shape[1])
+    yp, ydt, yld, rows, hidden = _rows2d(y, "y", plan.tokens * plan.topk)
+    dp, ddt, dld, _, _ = _rows2d(dout, "dout", plan.tokens, hidden)
     w = _plan_weights(weights, plan)
-    dy = _result(dy, "dy", y.shape[0], y.shape[1], dout.dtype if dtype is None else dtype, y.device)
+    dy, gp, gdt, gld = _result(dy, "dy", rows, hidden, dtype or dout.dtype, y.device)
     if dw is None:
-        dw = torch.empty(plan.tokens, plan.topk, dtype=torch.float32, device=y.device)
-    st = lib().ufp4_moe_combine_bwd(dout.data_ptr(), _dtype_code(dout), _ld(dout), y.data_ptr(), _dtype_code(y),
-                                    _ld(y), y.shape[1], plan.c(), w, dy.data_ptr(), _dtype_code(dy), _ld(dy),
-                                    _plan_weights(dw, plan), _stream(stream))
+        dw = torch.empty((plan.tokens, plan.topk), dtype=torch.float32, device=y.device)
+    st = lib().ufp4_moe_combine_bwd(dp, ddt, dld, yp, ydt, yld, hidden, plan._c, w, gp, gdt, gld,
+                                    _plan_weights(dw, plan, "dw"), _raw_stream(stream))
     _check(st, "ufp4_moe_combine_bwd")
     return dy, dw
 
@@ -609,38 +629,70 @@ class Ckpt:
     [rows, ufp4_ckpt_ld(cols)], scales uint8 [rows, ceil(cols / 32)]."""
 
     def __init__(self, codes, scales, rows, cols, format):
-        self.codes, self.scales = codes, scales
-        self.rows, self.cols, self.format = int(rows), int(cols), int(format)
-        self._c = CkptC(codes.data_ptr(), scales.data_ptr(), self.rows, self.cols, self.format, 0)
+        for t, name, width in ((codes, "codes", self._ld(cols)), (scales, "scales", self._blocks(cols))):
+            _cuda(t, name)
+            if t.dtype != torch.uint8 or tuple(t.shape) != (rows, width) or not t.is_contiguous():
+                raise ValueError("%s must be contiguous uint8 [%d, %d]" % (name, rows, width))
+        self._codes, self._scales, self.device = codes, scales, codes.device
+        self._set(codes.data_ptr(), scales.data_ptr(), rows, cols, format)
+
+    def _set(self, codes, scales, rows, cols, format):
+        self.rows, self.cols, self.format = rows, cols, int(format)
+        self._c = ctypes.byref(CkptC(codes, scales, rows, cols, self.format, 0))
+
+    @staticmethod
+    def _ld(cols):
+        return (cols + 15) // 16 * 16
+
+    @staticmethod
+    def _blocks(cols):
+        return (cols + UFP4_CKPT_BLOCK - 1) // UFP4_CKPT_BLOCK
 
     @classmethod
     def empty(cls, rows, cols, format, device="cuda"):
-        codes = torch.empty(rows, (cols + 15) // 16 * 16, dtype=torch.uint8, device=device)
-        scales = torch.empty(rows, (cols + UFP4_CKPT_BLOCK - 1) // UFP4_CKPT_BLOCK, dtype=torch.uint8, device=device)
-        return cls(codes, scales, rows, cols, format)
+        """One buffer for codes and scales; the two views are made when asked for."""
+        c = cls.__new__(cls)
+        n = rows * cls._ld(cols)
+        c._buf = torch.empty(n + rows * cls._blocks(cols), dtype=torch.uint8, device=device)
+        c._codes = c._scales = None
+        c.device = c._buf.device
+        at = c._buf.data_ptr()
+        c._set(at, at + n, rows, cols, format)
+        return c
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._codes = self._buf[:self.rows * self._ld(self.cols)].view(self.rows, self._ld(self.cols))
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._buf[self.rows * self._ld(self.cols):].view(self.rows, self._blocks(self.cols))
+        return self._scales
 
     def c(self):
-        return ctypes.byref(self._c)
+        return self._c
 
 
 def ufp4_ckpt_save(x, format=UFP4_CKPT_INT8, out=None, stream=None):
     """x (2-D bf16 / fp32) in 8 bits with a power-of-two scale per 32
     elements of a row.  Returns a Ckpt."""
-    _rows2d(x, "x")
+    xp, dt, ld, rows, cols = _rows2d(x, "x")
     if out is None:
-        out = Ckpt.empty(x.shape[0], x.shape[1], format, x.device)
-    elif (out.rows, out.cols, out.format) != (*x.shape, format):
+        out = Ckpt.empty(rows, cols, format, x.device)
+    elif (out.rows, out.cols, out.format) != (rows, cols, format):
         raise ValueError("out is a checkpoint of another shape or format")
-    st = lib().ufp4_ckpt_save(x.data_ptr(), _dtype_code(x), _ld(x), out.c(), _stream(stream))
+    st = lib().ufp4_ckpt_save(xp, dt, ld, out._c, _raw_stream(stream))
     _check(st, "ufp4_ckpt_save")
     return out
 
 
 def ufp4_ckpt_load(c, dtype=torch.bfloat16, out=None, stream=None):
     """The values of a checkpoint (exact in bf16 and fp32)."""
-    _cuda(c.codes, "c.codes")
-    out = _result(out, "out", c.rows, c.cols, dtype, c.codes.device)
-    st = lib().ufp4_ckpt_load(c.c(), out.data_ptr(), _dtype_code(out), _ld(out), _stream(stream))
+    out, op, odt, old = _result(out, "out", c.rows, c.cols, dtype, c.device)
+    st = lib().ufp4_ckpt_load(c._c, op, odt, old, _raw_stream(stream))
     _check(st, "ufp4_ckpt_load")
     return out
 
@@ -650,18 +702,17 @@ def ufp4_swiglu(gate, up, ckpt=None, dtype=None, out=None, stream=None):
     backward pass (ckpt: their format, or None to keep nothing).  Returns
     (h, keep_gate, keep_up), the latter two None without ckpt.  dtype: h's
     (gate's by default)."""
-    _rows2d(gate, "gate")
-    rows, cols = gate.shape
-    _rows2d(up, "up", rows, cols)
-    if up.dtype != gate.dtype:
+    gp, dt, gld, rows, cols = _rows2d(gate, "gate")
+    up_p, udt, uld, _, _ = _rows2d(up, "up", rows, cols)
+    if udt != dt:
         raise TypeError("gate and up must have one dtype")
-    out = _result(out, "out", rows, cols, gate.dtype if dtype is None else dtype, gate.device)
+    device = gate.device
+    out, hp, hdt, hld = _result(out, "out", rows, cols, dtype or gate.dtype, device)
     kg = ku = None
     if ckpt is not None:
-        kg, ku = Ckpt.empty(rows, cols, ckpt, gate.device), Ckpt.empty(rows, cols, ckpt, gate.device)
-    st = lib().ufp4_swiglu(gate.data_ptr(), _ld(gate), up.data_ptr(), _ld(up), _dtype_code(gate), rows, cols,
-                           out.data_ptr(), _dtype_code(out), _ld(out), None if kg is None else kg.c(),
-                           None if ku is None else ku.c(), _stream(stream))
+        kg, ku = Ckpt.empty(rows, cols, ckpt, device), Ckpt.empty(rows, cols, ckpt, device)
+    st = lib().ufp4_swiglu(gp, gld, up_p, uld, dt, rows, cols, hp, hdt, hld, kg and kg._c, ku and ku._c,
+                           _raw_stream(stream))
     _check(st, "ufp4_swiglu")
     return out, kg, ku
 
@@ -670,14 +721,12 @@ def ufp4_swiglu_bwd(dh, keep_gate, keep_up, dtype=None, dgate=None, dup=None, st
     """Gradients of ufp4_swiglu from its checkpoints: (dgate, dup).  dtype:
     the gradients' (dh's by default)."""
     rows, cols = keep_gate.rows, keep_gate.cols
-    _rows2d(dh, "dh", rows, cols)
-    dtype = dh.dtype if dtype is None else dtype
-    dgate = _result(dgate, "dgate", rows, cols, dtype, dh.device)
-    dup = _result(dup, "dup", rows, cols, dgate.dtype, dh.device)
-    if dup.dtype != dgate.dtype:
+    dp, ddt, dld, _, _ = _rows2d(dh, "dh", rows, cols)
+    device = dh.device
+    dgate, gp, gdt, gld = _result(dgate, "dgate", rows, cols, dtype or dh.dtype, device)
+    dup, up, udt, uld = _result(dup, "dup", rows, cols, dgate.dtype, device)
+    if udt != gdt:
         raise TypeError("dgate and dup must have one dtype")
-    st = lib().ufp4_swiglu_bwd(dh.data_ptr(), _dtype_code(dh), _ld(dh), keep_gate.c(), keep_up.c(),
-                               dgate.data_ptr(), _ld(dgate), dup.data_ptr(), _ld(dup), _dtype_code(dgate),
-                               _stream(stream))
+    st = lib().ufp4_swiglu_bwd(dp, ddt, dld, keep_gate._c, keep_up._c, gp, gld, up, uld, gdt, _raw_stream(stream))
     _check(st, "ufp4_swiglu_bwd")
     return dgate, dup

@@ -43,7 +43,8 @@ def _values(g, rows, cols):
 
 # (rows, cols, pad, shift): blocks that end inside a row, rows off 16 bytes, one element, one block
 SHAPES = [(1, 1, 0, 0), (1, 32, 0, 0), (3, 8, 0, 0), (5, 40, 0, 0), (5, 40, 8, 0), (5, 40, 3, 0), (7, 64, 0, 1),
-          (9, 33, 0, 0), (2, 1001, 0, 0), (4, 1408, 0, 0), (65, 72, 0, 0)]
+          (9, 33, 0, 0), (2, 1001, 0, 0), (4, 1408, 0, 0), (65, 72, 0, 0),
+          (6, 34, 0, 0), (3, 1002, 0, 0), (5, 96, 2, 2), (5, 48, 0, 0)]
 
 
 @pytest.mark.parametrize("rows,cols,pad,shift", SHAPES)
@@ -61,7 +62,7 @@ def test_ckpt(U, rows, cols, pad, shift, dtype, fmt):
     np.testing.assert_array_equal(_f64(out), back)
 
 
-@pytest.mark.parametrize("cols", [32, 31])   # both layouts of the work
+@pytest.mark.parametrize("cols", [32, 31, 30])   # the layouts of the work
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_ckpt_edges(U, fmt, cols):
     """Powers of two and their neighbours at the top of a block (the scale's
@@ -85,7 +86,7 @@ def test_ckpt_edges(U, fmt, cols):
     np.testing.assert_array_equal(_f64(U.ufp4_ckpt_load(c, dtype=FP)), back)
 
 
-@pytest.mark.parametrize("cols", [96, 95])
+@pytest.mark.parametrize("cols", [96, 95, 94])
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_ckpt_keeps_non_finite_blocks_visible(U, fmt, bad, cols):
