@@ -641,8 +641,8 @@ def run_kernel(args):
     orientation or both (quant_dual_*; the SR variant quantizes dY, T x F),
     after `warmup` launches, the tensor amax given (quant_resident_e1m2: W,
     F x H, both ways with its maxima, the on-chip single pass; quant_grouped_dual_e1m2:
-    the MoE-7.9B X both ways, its amax pass included).  --shape dense: T, H,
-    F = 8192, 2048, 5632; moe124b: 65536, 8192, 2048.  Prints the mean event
+    the MoE-7.9B X both ways, its amax pass included; moe_*, ckpt_*, swiglu*:
+    the calls around that layer's grouped GEMMs).  --shape dense: T, H, F = 8192, 2048, 5632; moe124b: 65536, 8192, 2048.  Prints the mean event
     time."""
     import torch
     from fp4_quantized_numerics_gb300 import build, inputs, ufp4 as U
@@ -662,6 +662,9 @@ def run_kernel(args):
         work = 2 * x.numel() * Q_BYTES_PER_ELEM
         unit = "GB/s"
         return _run_kernel_timing(args, kind, fn, work, unit, dev)
+    if kind.startswith(("moe_", "ckpt_", "swiglu")):
+        calls = moe_calls(U, torch, dev, kinds=(kind.split("_")[0],))
+        return _run_kernel_timing(args, kind, *calls[kind], "GB/s", dev)
     wl = WORKLOAD if args.shape == "moe124b" else DENSE
     T, H, F = wl["tokens"], wl["hidden"], wl["ffn"]
     x = inputs.device_normal((T, H), 1.0, 21, dev)
@@ -713,6 +716,51 @@ def run_kernel(args):
         work = x.numel() * Q_BYTES_PER_ELEM
         unit = "GB/s"
     return _run_kernel_timing(args, kind, fn, work, unit, dev)
+
+
+def moe_calls(U, torch, dev, kinds=("moe", "ckpt", "swiglu")):
+    """The calls around the grouped GEMMs on the MoE-7.9B layer (64 experts,
+    16384 tokens x top-6, 2048 -> 1408; fp32 products, BF16 stream): name ->
+    (call, algorithmic bytes)."""
+    from fp4_quantized_numerics_gb300 import inputs
+    T, K, E, H, F = 16384, 6, 64, 2048, 1408
+    N = T * K
+    bf, f32 = torch.bfloat16, torch.float32
+    new = lambda *shape, dtype=bf: torch.empty(shape, dtype=dtype, device=dev)
+    k8 = 33 / 32                             # bytes of a checkpointed element
+    calls = {}
+    if "moe" in kinds:
+        ids = inputs.device_normal((T, E), 1.0, 41, dev, f32) + inputs.device_normal((E,), 1.0, 42, dev, f32)
+        ids = torch.topk(ids, K, dim=1).indices
+        w = torch.softmax(inputs.device_normal((T, K), 1.0, 43, dev, f32), dim=1)
+        x, dout = inputs.device_normal((T, H), 1.0, 44, dev), inputs.device_normal((T, H), 1e-3, 45, dev)
+        y = inputs.device_normal((N, H), 1.0, 46, dev, f32)
+        plan, xs, out, dy, dw = U.ufp4_moe_sort(ids, E), new(N, H), new(T, H), new(N, H), new(T, K, dtype=f32)
+        calls.update({
+            "moe_sort": (lambda: U.ufp4_moe_sort(ids, E, out=plan), 16 * N),
+            "moe_dispatch": (lambda: U.ufp4_moe_dispatch(x, plan, out=xs), 2 * (T + N) * H),
+            "moe_combine": (lambda: U.ufp4_moe_combine(y, plan, w, out=out), 4 * N * H + 2 * T * H),
+            "moe_combine_bwd": (lambda: U.ufp4_moe_combine_bwd(dout, y, plan, w, dy=dy, dw=dw),
+                                6 * N * H + 2 * T * H),
+        })
+    if "ckpt" in kinds:
+        a = inputs.device_normal((N, H), 1.0, 49, dev)
+        kept, back = U.ufp4_ckpt_save(a), new(N, H)
+        calls.update({
+            "ckpt_save": (lambda: U.ufp4_ckpt_save(a, out=kept), (2 + k8) * N * H),
+            "ckpt_load": (lambda: U.ufp4_ckpt_load(kept, out=back), (2 + k8) * N * H),
+        })
+    if "swiglu" in kinds:
+        gu = inputs.device_normal((N, 2 * F), 1.0, 47, dev, f32)
+        dh = inputs.device_normal((N, F), 1e-3, 48, dev, f32)
+        h, dgu, fmt = new(N, F), new(N, 2 * F), U.UFP4_CKPT_INT8
+        _, kg, ku = U.ufp4_swiglu(gu[:, :F], gu[:, F:], ckpt=fmt, out=h)
+        calls.update({
+            "swiglu": (lambda: U.ufp4_swiglu(gu[:, :F], gu[:, F:], ckpt=fmt, out=h), (10 + 2 * k8) * N * F),
+            "swiglu_bwd": (lambda: U.ufp4_swiglu_bwd(dh, kg, ku, dgate=dgu[:, :F], dup=dgu[:, F:]),
+                           (8 + 2 * k8) * N * F),
+        })
+    return calls
 
 
 def _run_kernel_timing(args, kind, fn, work, unit, dev):
@@ -803,6 +851,7 @@ def run_all_kernels(args):
         ("grouped GEMM E1M2 fwd_y (MoE-7.9B)", lambda: U.ufp4_gemm_grouped(gr, gw, groups),
          2.0 * sum(counts) * 1408 * H, "F"),
     ]
+    calls += [(name + " (MoE-7.9B)", fn, work, "B") for name, (fn, work) in moe_calls(U, torch, dev).items()]
     out = []
     for name, fn, work, kind in calls:
         ms = _timeit(torch, fn, flush, max(args.steps, 1))
@@ -1116,7 +1165,8 @@ def build_parser():
                              "quant_row_e1m2", "quant_col_e1m2", "quant_dual_e1m2",
                              "quant_dual_sr_e1m2", "amax_dual_e1m2",
                              "quant_row_e2m1", "quant_col_e2m1", "quant_grouped_dual_e1m2", "quant_resident_e1m2",
-                             "all"],
+                             "moe_sort", "moe_dispatch", "moe_combine", "moe_combine_bwd", "ckpt_save", "ckpt_load",
+                             "swiglu", "swiglu_bwd", "all"],
                     help="time one kernel of the step in isolation (profiling); all: every public call once")
     return ap
 
