@@ -5,11 +5,26 @@
 // The dual quantizer already leaves the GEMM operands of the backward pass in
 // 4 bits; what the gated activation's own gradient needs is gate and up,
 // 8 bytes an element pair in fp32.  At 8 bits and a scale byte per 32 they
-// cost 2.06 bytes, written by the pass that reads them anyway.
+// cost 2.06 bytes, written by the pass that reads them anyway.  Scales are
+// powers of two, so that dividing by them and multiplying back are exact and
+// the restored values are exact in bf16 as well.
+//
+// Bound by memory: at most 3 instructions a byte moved.  One GB300, "of
+// measured" is of the 6676 GB/s of a plain copy:
+//   98304 x 1408, fp32 in, BF16 out, INT8 kept:
+//     k_swiglu 232 us, 7.2 TB/s (108 %; reads run faster than a copy), without
+//     checkpoints 190 us; k_swiglu_bwd 197 us (105 %);
+//   65536 x 8192 BF16: k_ckpt_save 249 us (98 %; INT8), k_ckpt_load 230 us
+//     (106 %).
+// With 8 elements a thread and 16-byte accesses these were 232, 241, 462 and
+// 372 us: too few bytes in flight, and the scale's arithmetic shared by half
+// as many elements.
 //
 // In the whole layout (rowops.cuh) a thread owns 16 consecutive elements and
 // two neighbouring lanes one 32-element block; in pairs a half warp owns each
-// block, in singles the warp.
+// block, in singles the warp.  Those two are bound by instructions (72 % of
+// the issue slots in k_ckpt_save): 65536 x 1002 and 1001 BF16 73 and 67 us
+// saved (41 and 44 % of measured), 52 and 56 us restored.
 #include "common.cuh"
 #include "internal.h"
 #include "rowops.cuh"
