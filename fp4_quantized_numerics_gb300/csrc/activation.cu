@@ -20,11 +20,13 @@
 // 372 us: too few bytes in flight, and the scale's arithmetic shared by half
 // as many elements.
 //
-// In the whole layout (rowops.cuh) a thread owns 16 consecutive elements and
-// two neighbouring lanes one 32-element block; in pairs a half warp owns each
+// In the whole layout (rowops.cuh) a thread owns 16 consecutive elements (8
+// where rows allow no more) and two (four) neighbouring lanes one 32-element
+// block; in pairs a half warp owns each
 // block, in singles the warp.  Those two are bound by instructions (72 % of
 // the issue slots in k_ckpt_save): 65536 x 1002 and 1001 BF16 73 and 67 us
-// saved (41 and 44 % of measured), 52 and 56 us restored.
+// saved (41 and 44 % of measured), 52 and 56 us restored; x 1000 (whole, by
+// eights) 57 and 39 us, in fp32 52 and 51 us (95 and 97 %).
 #include "common.cuh"
 #include "internal.h"
 #include "rowops.cuh"
@@ -134,15 +136,11 @@ __device__ __forceinline__ float silu(float g) {
 }
 
 // ------------------------------------------------------------------- work
-template <int L>
-constexpr int kElems = L == kWhole ? 16 : 8;
-
-// The row and part a thread owns; false past the last.  All lanes of a block
-// are in or out together.
-template <int L>
+// The row and part a thread owns.  All lanes of a block are in or out together.
+template <int L, int N>
 struct Place {
     int64_t row;
-    Part<L, kElems<L>> part;
+    Part<L, N> part;
 
     __device__ __forceinline__ Place(RowDiv parts, uint32_t cols, uint64_t i)
         : row((int64_t)row_of(i, parts)), part((uint32_t)(i - (uint64_t)row * parts.d), cols) {}
@@ -159,33 +157,36 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
     asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-// Bits of the block's largest magnitude over a lane pair; NaN above all.
-__device__ __forceinline__ uint32_t pair_max(const float (&x)[16]) {
-    float m[2];
+// Bits of the block's largest magnitude, over the 32 / N lanes that hold it;
+// NaN above all.
+template <int N>
+__device__ __forceinline__ uint32_t lanes_max(const float (&x)[N]) {
+    float m = x[0];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        m[h] = max3_abs(x[8 * h], x[8 * h + 1], x[8 * h + 2]);
-        m[h] = max3_abs(m[h], x[8 * h + 3], x[8 * h + 4]);
-        m[h] = max3_abs(m[h], x[8 * h + 5], x[8 * h + 6]);
-    }
-    const uint32_t a = __float_as_uint(max_nan(max3_abs(m[0], x[7], x[15]), m[1])) & 0x7FFFFFFFu;
-    return max(a, __shfl_xor_sync(3u << (threadIdx.x & 30u), a, 1));
+    for (int i = 1; i + 1 < N; i += 2) m = max3_abs(m, x[i], x[i + 1]);
+    m = max3_abs(m, x[N - 1], 0.0f);
+    uint32_t a = __float_as_uint(m) & 0x7FFFFFFFu;
+    constexpr uint32_t kLanes = 32 / N, kOne = (1u << kLanes) - 1u;
+    const uint32_t lanes = kOne << (threadIdx.x & (32u - kLanes));
+#pragma unroll
+    for (uint32_t d = 1; d < kLanes; d <<= 1) a = max(a, __shfl_xor_sync(lanes, a, d));
+    return a;
 }
 
 // Writes the checkpoint of this thread's elements (0 where it has none).
-template <int FMT, int L>
-__device__ __forceinline__ void keep(const float (&x)[kElems<L>], const Place<L> &p, const Ckpt &c, int64_t ld,
+template <int FMT, int L, int N>
+__device__ __forceinline__ void keep(const float (&x)[N], const Place<L, N> &p, const Ckpt &c, int64_t ld,
                                      uint32_t nb) {
     const uint32_t col = p.part.col;
     uint8_t *codes = c.codes + p.row * ld + col, *scales = c.scales + p.row * nb + col / 32;
     if constexpr (L == kWhole) {
-        const uint32_t b = scale_byte<FMT>(pair_max(x));
+        const uint32_t b = scale_byte<FMT>(lanes_max(x));
         const float inv = scale_inv(b);
-        if ((col & 16u) == 0) *scales = (uint8_t)b;
+        if (col % 32 == 0) *scales = (uint8_t)b;
         if (!p.part.has(0)) return;
-        uint32_t w[4];
+        uint32_t w[N / 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = b == 255u ? 0u : codes4<FMT>(x + 4 * i, inv);
+        for (int i = 0; i < N / 4; ++i) w[i] = b == 255u ? 0u : codes4<FMT>(x + 4 * i, inv);
         store_words(codes, w);
     } else {
         // the blocks' maxima reach all their lanes; lane k of a block's lanes
@@ -219,17 +220,17 @@ __device__ __forceinline__ void keep(const float (&x)[kElems<L>], const Place<L>
         }
     }
 }
-template <int FMT, int L>
-__device__ __forceinline__ void restore(const Ckpt &c, const Place<L> &p, int64_t ld, uint32_t nb,
-                                        float (&x)[kElems<L>]) {
+template <int FMT, int L, int N>
+__device__ __forceinline__ void restore(const Ckpt &c, const Place<L, N> &p, int64_t ld, uint32_t nb,
+                                        float (&x)[N]) {
     const uint32_t col = p.part.col;
     const uint8_t *codes = c.codes + p.row * ld + col, *scales = c.scales + p.row * nb + col / 32;
     if constexpr (L == kWhole) {
-        uint32_t w[4];
+        uint32_t w[N / 4];
         load_words(codes, w);
         const float s = scale_of(__ldg(scales));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) values4<FMT>(w[i], s, x + 4 * i);
+        for (int i = 0; i < N / 4; ++i) values4<FMT>(w[i], s, x + 4 * i);
     } else {
         constexpr int kStep = L == kPairs ? 2 : 1, kLanes = 32 / kStep;
         const uint32_t lane = threadIdx.x & 31u, k = lane % kLanes, first = lane - k;
@@ -255,39 +256,38 @@ __device__ __forceinline__ void restore(const Ckpt &c, const Place<L> &p, int64_
 }
 
 // ---------------------------------------------------------------- kernels
-template <class T, int FMT, int L>
+template <class T, int FMT, int L, int N>
 __global__ void __launch_bounds__(kThreads) k_ckpt_save(const T *__restrict__ x, int64_t ld, Ckpt c, int64_t ldc,
                                                         uint32_t cols, uint32_t nb, RowDiv parts, uint64_t work) {
     const uint64_t i = part_index<L>();
     if (i >= work) return;
-    const Place<L> p(parts, cols, i);
-    float v[kElems<L>] = {};
+    const Place<L, N> p(parts, cols, i);
+    float v[N] = {};
     if (L != kWhole || p.part.has(0)) p.part.load(x + p.row * ld, v);
-    keep<FMT, L>(v, p, c, ldc, nb);
+    keep<FMT>(v, p, c, ldc, nb);
 }
 
-template <class T, int FMT, int L>
+template <class T, int FMT, int L, int N>
 __global__ void __launch_bounds__(kThreads) k_ckpt_load(Ckpt c, int64_t ldc, T *__restrict__ x, int64_t ld,
                                                         uint32_t cols, uint32_t nb, RowDiv parts, uint64_t work) {
     const uint64_t i = part_index<L>();
     if (i >= work) return;
-    const Place<L> p(parts, cols, i);
+    const Place<L, N> p(parts, cols, i);
     if (L == kWhole && !p.part.has(0)) return;
-    float v[kElems<L>];
-    restore<FMT, L>(c, p, ldc, nb, v);
+    float v[N];
+    restore<FMT>(c, p, ldc, nb, v);
     p.part.store(x + p.row * ld, v);
 }
 
-template <class Ti, class To, int FMT, int L>
+template <class Ti, class To, int FMT, int L, int N>
 __global__ void __launch_bounds__(kThreads) k_swiglu(const Ti *__restrict__ gate, int64_t ld_gate,
                                                      const Ti *__restrict__ up, int64_t ld_up, To *__restrict__ h,
                                                      int64_t ld_h, Ckpt cg, Ckpt cu, int64_t ldc, uint32_t cols,
                                                      uint32_t nb, RowDiv parts, uint64_t work) {
     constexpr bool kExact = std::is_same<To, float>::value;
-    constexpr int N = kElems<L>;
     const uint64_t i = part_index<L>();
     if (i >= work) return;
-    const Place<L> p(parts, cols, i);
+    const Place<L, N> p(parts, cols, i);
     float g[N] = {}, u[N] = {};
     if (L != kWhole || p.part.has(0)) {
         p.part.load(gate + p.row * ld_gate, g);
@@ -298,26 +298,25 @@ __global__ void __launch_bounds__(kThreads) k_swiglu(const Ti *__restrict__ gate
         p.part.store(h + p.row * ld_h, o);
     }
     if constexpr (FMT != kNone) {
-        keep<FMT, L>(g, p, cg, ldc, nb);
-        keep<FMT, L>(u, p, cu, ldc, nb);
+        keep<FMT>(g, p, cg, ldc, nb);
+        keep<FMT>(u, p, cu, ldc, nb);
     }
 }
 
-template <class Td, class To, int FMT, int L>
+template <class Td, class To, int FMT, int L, int N>
 __global__ void __launch_bounds__(kThreads) k_swiglu_bwd(const Td *__restrict__ dh, int64_t ld_dh, Ckpt cg, Ckpt cu,
                                                          int64_t ldc, To *__restrict__ dgate, int64_t ld_dgate,
                                                          To *__restrict__ dup, int64_t ld_dup, uint32_t cols,
                                                          uint32_t nb, RowDiv parts, uint64_t work) {
     constexpr bool kExact = std::is_same<To, float>::value;
-    constexpr int N = kElems<L>;
     const uint64_t i = part_index<L>();
     if (i >= work) return;
-    const Place<L> p(parts, cols, i);
+    const Place<L, N> p(parts, cols, i);
     if (L == kWhole && !p.part.has(0)) return;
     float d[N], g[N], u[N];
     p.part.load(dh + p.row * ld_dh, d);
-    restore<FMT, L>(cg, p, ldc, nb, g);
-    restore<FMT, L>(cu, p, ldc, nb, u);
+    restore<FMT>(cg, p, ldc, nb, g);
+    restore<FMT>(cu, p, ldc, nb, u);
 #pragma unroll
     for (int e = 0; e < N; ++e) {
         const float s = sigmoid<kExact>(g[e]), gs = g[e] * s;
@@ -337,7 +336,7 @@ struct Tensor {
     int dtype;
 };
 struct Grid {
-    int layout;
+    int layout, elems;
     uint32_t nb;       // blocks of a row
     RowDiv parts;
     uint64_t work;
@@ -350,20 +349,23 @@ Grid grid_of(int64_t rows, int64_t cols, std::initializer_list<Tensor> tensors) 
         return cols % n == 0;
     };
     Grid g;
-    g.layout = by(kElems<kWhole>) ? kWhole : by(2) ? kPairs : kSingles;
+    g.layout = by(16) || by(8) ? kWhole : by(2) ? kPairs : kSingles;
+    g.elems = by(16) ? 16 : 8;
     g.nb = (uint32_t)((cols + 31) / 32);
-    // a lane pair per block, so that both lanes of a last half block are there
-    const uint32_t parts = g.layout == kWhole ? 2 * g.nb : parts_of(g.layout, kElems<kSingles>, cols);
+    // whole: parts for all of the last block, so that its lanes are all there
+    const uint32_t parts = g.layout == kWhole ? 32 / g.elems * g.nb : parts_of(g.layout, g.elems, cols);
     g.parts = make_rowdiv(parts);
     g.work = (uint64_t)rows * parts;
     g.ctas = (unsigned)((threads_of(g.layout, g.work) + kThreads - 1) / kThreads);
     return g;
 }
+// Calls f with the layout and the elements of a thread.
 template <class F>
-void by_layout(int layout, F f) {
-    if (layout == kWhole) f(Int<kWhole>());
-    else if (layout == kPairs) f(Int<kPairs>());
-    else f(Int<kSingles>());
+void by_layout(const Grid &g, F f) {
+    if (g.layout == kWhole && g.elems == 16) f(Int<kWhole>(), Int<16>());
+    else if (g.layout == kWhole) f(Int<kWhole>(), Int<8>());
+    else if (g.layout == kPairs) f(Int<kPairs>(), Int<8>());
+    else f(Int<kSingles>(), Int<8>());
 }
 template <class F>
 void by_format(int fmt, F f) {
@@ -379,8 +381,8 @@ cudaError_t launch_ckpt_save(const void *x, int dtype, int64_t ld, const Ckpt &c
     by_type(dtype, [&](auto *t) {
         using T = Elem<decltype(t)>;
         by_format(fmt, [&](auto f) {
-            by_layout(g.layout, [&](auto w) {
-                k_ckpt_save<T, decltype(f)::value, decltype(w)::value><<<g.ctas, kThreads, 0, s>>>(
+            by_layout(g, [&](auto w, auto n) {
+                k_ckpt_save<T, decltype(f)::value, decltype(w)::value, decltype(n)::value><<<g.ctas, kThreads, 0, s>>>(
                     static_cast<const T *>(x), ld, c, ckpt_ld(cols), (uint32_t)cols, g.nb, g.parts, g.work);
             });
         });
@@ -394,8 +396,8 @@ cudaError_t launch_ckpt_load(const Ckpt &c, int fmt, int64_t rows, int64_t cols,
     by_type(dtype, [&](auto *t) {
         using T = Elem<decltype(t)>;
         by_format(fmt, [&](auto f) {
-            by_layout(g.layout, [&](auto w) {
-                k_ckpt_load<T, decltype(f)::value, decltype(w)::value><<<g.ctas, kThreads, 0, s>>>(
+            by_layout(g, [&](auto w, auto n) {
+                k_ckpt_load<T, decltype(f)::value, decltype(w)::value, decltype(n)::value><<<g.ctas, kThreads, 0, s>>>(
                     c, ckpt_ld(cols), static_cast<T *>(x), ld, (uint32_t)cols, g.nb, g.parts, g.work);
             });
         });
@@ -411,9 +413,9 @@ cudaError_t launch_swiglu(const void *gate, int64_t ld_gate, const void *up, int
         using Ti = Elem<decltype(ti)>;
         by_type(h_dtype, [&](auto *to) {
             using To = Elem<decltype(to)>;
-            by_layout(gr.layout, [&](auto w) {
+            by_layout(gr, [&](auto w, auto n) {
                 auto go = [&](auto f) {
-                    k_swiglu<Ti, To, decltype(f)::value, decltype(w)::value><<<gr.ctas, kThreads, 0, s>>>(
+                    k_swiglu<Ti, To, decltype(f)::value, decltype(w)::value, decltype(n)::value><<<gr.ctas, kThreads, 0, s>>>(
                         static_cast<const Ti *>(gate), ld_gate, static_cast<const Ti *>(up), ld_up,
                         static_cast<To *>(h), ld_h, cg, cu, ckpt_ld(cols), (uint32_t)cols, gr.nb, gr.parts, gr.work);
                 };
@@ -434,8 +436,8 @@ cudaError_t launch_swiglu_bwd(const void *dh, int dh_dtype, int64_t ld_dh, const
         by_type(out_dtype, [&](auto *to) {
             using To = Elem<decltype(to)>;
             by_format(fmt, [&](auto f) {
-                by_layout(g.layout, [&](auto w) {
-                    k_swiglu_bwd<Td, To, decltype(f)::value, decltype(w)::value><<<g.ctas, kThreads, 0, s>>>(
+                by_layout(g, [&](auto w, auto n) {
+                    k_swiglu_bwd<Td, To, decltype(f)::value, decltype(w)::value, decltype(n)::value><<<g.ctas, kThreads, 0, s>>>(
                         static_cast<const Td *>(dh), ld_dh, cg, cu, ckpt_ld(cols), static_cast<To *>(dgate), ld_dgate,
                         static_cast<To *>(dup), ld_dup, (uint32_t)cols, g.nb, g.parts, g.work);
                 });

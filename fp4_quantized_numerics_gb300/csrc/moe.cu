@@ -250,10 +250,6 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine(const Ty *__restrict__
 // 8192 x 2 rows of 8192 BF16 102 us (98 %).
 constexpr int kBatch = 4;
 
-// Elements of a thread: 32 bytes of y in the whole layout.
-template <class Ty, int L>
-constexpr int kBwdElems = L == kWhole && sizeof(Ty) == 2 ? 16 : 8;
-
 // y's elements of one part: raw in the whole layout, else as fp32.
 template <class Ty, int L, int N>
 struct Held {
@@ -264,13 +260,12 @@ struct Held {
     }
 };
 
-template <class Td, class Ty, class To, int L, uint32_t G>
+template <class Td, class Ty, class To, int L, int N, uint32_t G>
 __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(
     const Td *__restrict__ dout, int64_t ld_dout, const Ty *__restrict__ y, int64_t ld_y,
     const int32_t *__restrict__ pos, const float *__restrict__ weights, const int64_t *__restrict__ routed_at,
     To *__restrict__ dy, int64_t ld_dy, float *__restrict__ dw, int topk, uint32_t hidden, uint32_t parts,
     uint32_t tokens) {
-    constexpr int N = kBwdElems<Ty, L>;
     __shared__ float sums[kThreads / 32][kBatch];
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x / 32;
     const uint32_t mine = threadIdx.x / G, in_group = threadIdx.x % G;
@@ -408,10 +403,11 @@ cudaError_t launch_moe_combine(const void *y, int y_dtype, int64_t hidden, int64
                rows_by(out, ld_out, type_size(out_dtype), n);
     };
     by_type(y_dtype, [&](auto *yp) {
+        using Ty = Elem<decltype(yp)>;
         by_type(out_dtype, [&](auto *op) {
-            // 32 bytes of y a thread
-            if (y_dtype == 0 && by(16)) go(yp, op, Int<kWhole>(), Int<16>());
-            else if (by(8)) go(yp, op, Int<kWhole>(), Int<8>());
+            if constexpr (sizeof(Ty) == 2)   // 32 bytes of y a thread where rows allow it
+                if (by(16)) return go(yp, op, Int<kWhole>(), Int<16>());
+            if (by(8)) go(yp, op, Int<kWhole>(), Int<8>());
             else if (by(2)) go(yp, op, Int<kPairs>(), Int<8>());
             else go(yp, op, Int<kSingles>(), Int<8>());
         });
@@ -432,12 +428,12 @@ cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_
             using Ty = Elem<decltype(yp)>;
             by_type(dy_dtype, [&](auto *op) {
                 using To = Elem<decltype(op)>;
-                auto go = [&](auto layout) {
-                    constexpr int L = decltype(layout)::value, N = kBwdElems<Ty, L>;
+                auto go = [&](auto layout, auto elems) {
+                    constexpr int L = decltype(layout)::value, N = decltype(elems)::value;
                     const uint32_t parts = parts_of(L, N, hidden);
                     auto with = [&](auto group) {
                         constexpr uint32_t G = decltype(group)::value;
-                        k_moe_combine_bwd<Td, Ty, To, L, G><<<(unsigned)ctas((uint64_t)m.tokens * G), kThreads, 0, s>>>(
+                        k_moe_combine_bwd<Td, Ty, To, L, N, G><<<(unsigned)ctas((uint64_t)m.tokens * G), kThreads, 0, s>>>(
                             static_cast<const Td *>(dout), ld_dout, static_cast<const Ty *>(y), ld_y, m.pos, weights,
                             m.offsets + m.n_experts, static_cast<To *>(dy), ld_dy, dw, m.topk, (uint32_t)hidden,
                             parts, (uint32_t)m.tokens);
@@ -451,9 +447,11 @@ cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_
                     if (threads_of(L, parts) <= 64) with(Int<32>());
                     else with(Int<128>());
                 };
-                if (by(kBwdElems<Ty, kWhole>)) go(Int<kWhole>());
-                else if (by(2)) go(Int<kPairs>());
-                else go(Int<kSingles>());
+                if constexpr (sizeof(Ty) == 2)   // 32 bytes of y a thread where rows allow it
+                    if (by(16)) return go(Int<kWhole>(), Int<16>());
+                if (by(8)) go(Int<kWhole>(), Int<8>());
+                else if (by(2)) go(Int<kPairs>(), Int<8>());
+                else go(Int<kSingles>(), Int<8>());
             });
         });
     });

@@ -29,7 +29,14 @@ struct RowDiv {
 inline RowDiv make_rowdiv(uint32_t d) { return RowDiv{d == 1 ? 0 : ~0ull / d + 1, d}; }
 __device__ __forceinline__ uint64_t row_of(uint64_t n, RowDiv f) { return f.m ? __umul64hi(n, f.m) : n; }
 
-// ------------------------------------------------------- 16 and 32 bytes
+// ---------------------------------------------------- 8, 16 and 32 bytes
+__device__ __forceinline__ void load_words(const void *p, uint32_t (&w)[2]) {
+    const uint2 v = __ldg(static_cast<const uint2 *>(p));
+    w[0] = v.x; w[1] = v.y;
+}
+__device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[2]) {
+    *static_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+}
 __device__ __forceinline__ void load_words(const void *p, uint32_t (&w)[4]) {
     const uint4 v = __ldg(static_cast<const uint4 *>(p));
     w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;

@@ -409,9 +409,10 @@ UFP4_API ufp4_status ufp4_gemm_grouped(const ufp4_qtensor *a, const ufp4_qtensor
  * Conventions of the calls in this section, beside those above:
  *   - Tensors are BF16 or FP32 (`*_dtype`: UFP4_BF16, UFP4_FP32), row-major
  *     with any row stride >= the row length, in elements, aligned to one
- *     element.  The fast path wants addresses and strides that are multiples
- *     of 32 bytes, and rows that are multiples of 16 elements long; anything
- *     else gives the same results (dw's sums in another order).
+ *     element.  Rows that are multiples of 16 elements long, at addresses
+ *     and strides that are multiples of 32 bytes, are the fastest, multiples
+ *     of 8 next; anything else gives the same results (dw's sums in another
+ *     order).
  *   - Arithmetic is fp32; each result element is rounded once, when written.
  *   - Inputs and outputs must not overlap.
  *   - hidden / cols <= UFP4_MAX_WIDTH, rows x width < 2^38, rows and
