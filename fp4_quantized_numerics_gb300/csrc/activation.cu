@@ -259,6 +259,7 @@ __device__ __forceinline__ void restore(const Ckpt &c, const Place<L, N> &p, int
 template <class T, int FMT, int L, int N>
 __global__ void __launch_bounds__(kThreads) k_ckpt_save(const T *__restrict__ x, int64_t ld, Ckpt c, int64_t ldc,
                                                         uint32_t cols, uint32_t nb, RowDiv parts, uint64_t work) {
+    begin_in_order();
     const uint64_t i = part_index<L>();
     if (i >= work) return;
     const Place<L, N> p(parts, cols, i);
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_save(const T *__restrict__ x,
 template <class T, int FMT, int L, int N>
 __global__ void __launch_bounds__(kThreads) k_ckpt_load(Ckpt c, int64_t ldc, T *__restrict__ x, int64_t ld,
                                                         uint32_t cols, uint32_t nb, RowDiv parts, uint64_t work) {
+    begin_in_order();
     const uint64_t i = part_index<L>();
     if (i >= work) return;
     const Place<L, N> p(parts, cols, i);
@@ -285,6 +287,7 @@ __global__ void __launch_bounds__(kThreads) k_swiglu(const Ti *__restrict__ gate
                                                      int64_t ld_h, Ckpt cg, Ckpt cu, int64_t ldc, uint32_t cols,
                                                      uint32_t nb, RowDiv parts, uint64_t work) {
     constexpr bool kExact = std::is_same<To, float>::value;
+    begin_in_order();
     const uint64_t i = part_index<L>();
     if (i >= work) return;
     const Place<L, N> p(parts, cols, i);
@@ -309,6 +312,7 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_bwd(const Td *__restrict__ 
                                                          To *__restrict__ dup, int64_t ld_dup, uint32_t cols,
                                                          uint32_t nb, RowDiv parts, uint64_t work) {
     constexpr bool kExact = std::is_same<To, float>::value;
+    begin_in_order();
     const uint64_t i = part_index<L>();
     if (i >= work) return;
     const Place<L, N> p(parts, cols, i);
@@ -377,37 +381,42 @@ void by_format(int fmt, F f) {
 
 cudaError_t launch_ckpt_save(const void *x, int dtype, int64_t ld, const Ckpt &c, int fmt, int64_t rows, int64_t cols,
                              cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
     const Grid g = grid_of(rows, cols, {{x, ld, dtype}});
     by_type(dtype, [&](auto *t) {
         using T = Elem<decltype(t)>;
         by_format(fmt, [&](auto f) {
             by_layout(g, [&](auto w, auto n) {
-                k_ckpt_save<T, decltype(f)::value, decltype(w)::value, decltype(n)::value><<<g.ctas, kThreads, 0, s>>>(
-                    static_cast<const T *>(x), ld, c, ckpt_ld(cols), (uint32_t)cols, g.nb, g.parts, g.work);
+                e = launch_in_order(k_ckpt_save<T, decltype(f)::value, decltype(w)::value, decltype(n)::value>, g.ctas,
+                                    kThreads, s, static_cast<const T *>(x), ld, c, ckpt_ld(cols), cols, g.nb, g.parts,
+                                    g.work);
             });
         });
     });
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_ckpt_load(const Ckpt &c, int fmt, int64_t rows, int64_t cols, void *x, int dtype, int64_t ld,
                              cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
     const Grid g = grid_of(rows, cols, {{x, ld, dtype}});
     by_type(dtype, [&](auto *t) {
         using T = Elem<decltype(t)>;
         by_format(fmt, [&](auto f) {
             by_layout(g, [&](auto w, auto n) {
-                k_ckpt_load<T, decltype(f)::value, decltype(w)::value, decltype(n)::value><<<g.ctas, kThreads, 0, s>>>(
-                    c, ckpt_ld(cols), static_cast<T *>(x), ld, (uint32_t)cols, g.nb, g.parts, g.work);
+                e = launch_in_order(k_ckpt_load<T, decltype(f)::value, decltype(w)::value, decltype(n)::value>, g.ctas,
+                                    kThreads, s, c, ckpt_ld(cols), static_cast<T *>(x), ld, cols, g.nb, g.parts,
+                                    g.work);
             });
         });
     });
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_swiglu(const void *gate, int64_t ld_gate, const void *up, int64_t ld_up, int in_dtype,
                           int64_t rows, int64_t cols, void *h, int h_dtype, int64_t ld_h, const Ckpt &cg,
                           const Ckpt &cu, int fmt, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
     const Grid gr = grid_of(rows, cols, {{gate, ld_gate, in_dtype}, {up, ld_up, in_dtype}, {h, ld_h, h_dtype}});
     by_type(in_dtype, [&](auto *ti) {
         using Ti = Elem<decltype(ti)>;
@@ -415,21 +424,23 @@ cudaError_t launch_swiglu(const void *gate, int64_t ld_gate, const void *up, int
             using To = Elem<decltype(to)>;
             by_layout(gr, [&](auto w, auto n) {
                 auto go = [&](auto f) {
-                    k_swiglu<Ti, To, decltype(f)::value, decltype(w)::value, decltype(n)::value><<<gr.ctas, kThreads, 0, s>>>(
-                        static_cast<const Ti *>(gate), ld_gate, static_cast<const Ti *>(up), ld_up,
-                        static_cast<To *>(h), ld_h, cg, cu, ckpt_ld(cols), (uint32_t)cols, gr.nb, gr.parts, gr.work);
+                    e = launch_in_order(k_swiglu<Ti, To, decltype(f)::value, decltype(w)::value, decltype(n)::value>,
+                                        gr.ctas, kThreads, s, static_cast<const Ti *>(gate), ld_gate,
+                                        static_cast<const Ti *>(up), ld_up, static_cast<To *>(h), ld_h, cg, cu,
+                                        ckpt_ld(cols), cols, gr.nb, gr.parts, gr.work);
                 };
                 if (fmt == kNone) go(Int<kNone>());
                 else by_format(fmt, go);
             });
         });
     });
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_swiglu_bwd(const void *dh, int dh_dtype, int64_t ld_dh, const Ckpt &cg, const Ckpt &cu, int fmt,
                               int64_t rows, int64_t cols, void *dgate, int64_t ld_dgate, void *dup, int64_t ld_dup,
                               int out_dtype, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
     const Grid g = grid_of(rows, cols, {{dh, ld_dh, dh_dtype}, {dgate, ld_dgate, out_dtype}, {dup, ld_dup, out_dtype}});
     by_type(dh_dtype, [&](auto *td) {
         using Td = Elem<decltype(td)>;
@@ -437,14 +448,15 @@ cudaError_t launch_swiglu_bwd(const void *dh, int dh_dtype, int64_t ld_dh, const
             using To = Elem<decltype(to)>;
             by_format(fmt, [&](auto f) {
                 by_layout(g, [&](auto w, auto n) {
-                    k_swiglu_bwd<Td, To, decltype(f)::value, decltype(w)::value, decltype(n)::value><<<g.ctas, kThreads, 0, s>>>(
-                        static_cast<const Td *>(dh), ld_dh, cg, cu, ckpt_ld(cols), static_cast<To *>(dgate), ld_dgate,
-                        static_cast<To *>(dup), ld_dup, (uint32_t)cols, g.nb, g.parts, g.work);
+                    e = launch_in_order(k_swiglu_bwd<Td, To, decltype(f)::value, decltype(w)::value, decltype(n)::value>,
+                                        g.ctas, kThreads, s, static_cast<const Td *>(dh), ld_dh, cg, cu, ckpt_ld(cols),
+                                        static_cast<To *>(dgate), ld_dgate, static_cast<To *>(dup), ld_dup, cols, g.nb,
+                                        g.parts, g.work);
                 });
             });
         });
     });
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace ufp4

@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32
     __shared__ uint32_t hist[kSortWarps * (kMaxGroups + 1)];   // [warp][bucket]
     __shared__ uint32_t sums[kMaxGroups + 1];                  // this CTA's, read by the others
     __shared__ uint32_t warp_sum[kSortWarps];
+    begin_in_order();
     const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, B = E + 1, W = blockDim.x / 32;
     const uint32_t rank = cluster_rank(), nctas = cluster_size();
     const uint32_t warps = nctas * W;
@@ -181,6 +182,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *__restric
                                                            const int32_t *__restrict__ pos,
                                                            const int64_t *__restrict__ routed_at, int topk,
                                                            uint32_t width, RowDiv units, uint64_t work) {
+    begin_in_order();
     uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
     if constexpr (N > 1) i /= 32;
     if (i >= work) return;
@@ -218,6 +220,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine(const Ty *__restrict__
                                                           const int64_t *__restrict__ routed_at, To *__restrict__ out,
                                                           int64_t ld_out, int topk, uint32_t hidden, RowDiv parts,
                                                           uint64_t work) {
+    begin_in_order();
     uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
     if (L != kWhole) i /= 32;
     if (i >= work) return;
@@ -267,6 +270,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(
     To *__restrict__ dy, int64_t ld_dy, float *__restrict__ dw, int topk, uint32_t hidden, uint32_t parts,
     uint32_t tokens) {
     __shared__ float sums[kThreads / 32][kBatch];
+    begin_in_order();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x / 32;
     const uint32_t mine = threadIdx.x / G, in_group = threadIdx.x % G;
     const uint32_t t = blockIdx.x * (kThreads / G) + mine;
@@ -337,14 +341,14 @@ int sort_ctas(uint32_t n) { return n <= 1024 ? 1 : n <= 8192 ? 8 : kMaxSortCtas;
 inline uint64_t ctas(uint64_t work) { return (work + kThreads - 1) / kThreads; }
 
 template <class Unit, int N>
-void dispatch(const void *x, int64_t ldx, void *xs, int64_t ldxs, int64_t row_bytes, const MoePlan &m,
-              cudaStream_t s) {
+cudaError_t dispatch(const void *x, int64_t ldx, void *xs, int64_t ldxs, int64_t row_bytes, const MoePlan &m,
+                     cudaStream_t s) {
     const int64_t size = sizeof(Unit);
     const uint32_t width = (uint32_t)(row_bytes / size), units = N > 1 ? parts_of(kSingles, N, width) : width;
     const uint64_t work = (uint64_t)m.tokens * units;
-    k_moe_dispatch<Unit, N><<<(unsigned)ctas(work * (N > 1 ? 32 : 1)), kThreads, 0, s>>>(
-        static_cast<const Unit *>(x), ldx / size, static_cast<Unit *>(xs), ldxs / size, m.pos,
-        m.offsets + m.n_experts, m.topk, width, make_rowdiv(units), work);
+    return launch_in_order(k_moe_dispatch<Unit, N>, ctas(work * (N > 1 ? 32 : 1)), kThreads, s,
+                           static_cast<const Unit *>(x), ldx / size, static_cast<Unit *>(xs), ldxs / size, m.pos,
+                           m.offsets + m.n_experts, m.topk, width, make_rowdiv(units), work);
 }
 
 }  // namespace
@@ -352,16 +356,18 @@ void dispatch(const void *x, int64_t ldx, void *xs, int64_t ldxs, int64_t row_by
 cudaError_t launch_moe_sort(const void *ids, int id_bytes, const MoePlan &m, cudaStream_t s) {
     uint32_t n = (uint32_t)(m.tokens * m.topk), E = (uint32_t)m.n_experts;
     int ctas = sort_ctas(n);
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2]{};
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)ctas;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(ctas > 1 ? kSortThreads : 32u * std::max((E + 32u) / 32u, std::min(32u, (n + 31u) / 32u)));
     cfg.stream = s;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     auto go = [&](auto *t) {
         using Id = std::remove_pointer_t<decltype(t)>;
         if (ctas > 8) {
@@ -380,23 +386,23 @@ cudaError_t launch_moe_dispatch(const void *x, int dtype, int64_t hidden, int64_
     const int64_t esz = dtype == 0 ? 2 : 4, row = hidden * esz;
     const uint64_t all = (uint64_t)(uintptr_t)x | (uint64_t)(uintptr_t)xs | (uint64_t)(ld_x * esz) |
                          (uint64_t)(ld_xs * esz) | (uint64_t)row;
-    if (all % 16 == 0) dispatch<uint4, 1>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
-    else if (esz == 4) dispatch<uint32_t, 8>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
-    else dispatch<uint16_t, 8>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
-    return cudaGetLastError();
+    if (all % 16 == 0) return dispatch<uint4, 1>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
+    if (esz == 4) return dispatch<uint32_t, 8>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
+    return dispatch<uint16_t, 8>(x, ld_x * esz, xs, ld_xs * esz, row, m, s);
 }
 
 cudaError_t launch_moe_combine(const void *y, int y_dtype, int64_t hidden, int64_t ld_y, const MoePlan &m,
                                const float *weights, void *out, int out_dtype, int64_t ld_out, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
     auto go = [&](auto *yp, auto *op, auto layout, auto elems) {
         constexpr int L = decltype(layout)::value, N = decltype(elems)::value;
         const uint32_t parts = parts_of(L, N, hidden);
         const uint64_t work = (uint64_t)m.tokens * parts;
         using Ty = Elem<decltype(yp)>;
         using To = Elem<decltype(op)>;
-        k_moe_combine<Ty, To, L, N><<<(unsigned)ctas(threads_of(L, work)), kThreads, 0, s>>>(
-            static_cast<const Ty *>(y), ld_y, m.pos, weights, m.offsets + m.n_experts, static_cast<To *>(out), ld_out,
-            m.topk, (uint32_t)hidden, make_rowdiv(parts), work);
+        e = launch_in_order(k_moe_combine<Ty, To, L, N>, ctas(threads_of(L, work)), kThreads, s,
+                            static_cast<const Ty *>(y), ld_y, m.pos, weights, m.offsets + m.n_experts,
+                            static_cast<To *>(out), ld_out, m.topk, hidden, make_rowdiv(parts), work);
     };
     const auto by = [&](int n) {
         return hidden % n == 0 && rows_by(y, ld_y, type_size(y_dtype), n) &&
@@ -412,7 +418,7 @@ cudaError_t launch_moe_combine(const void *y, int y_dtype, int64_t hidden, int64
             else go(yp, op, Int<kSingles>(), Int<8>());
         });
     });
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_dout, const void *y, int y_dtype,
@@ -422,6 +428,7 @@ cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_
         return hidden % n == 0 && rows_by(dout, ld_dout, type_size(dout_dtype), n) &&
                rows_by(y, ld_y, type_size(y_dtype), n) && rows_by(dy, ld_dy, type_size(dy_dtype), n);
     };
+    cudaError_t e = cudaSuccess;
     by_type(dout_dtype, [&](auto *dp) {
         using Td = Elem<decltype(dp)>;
         by_type(y_dtype, [&](auto *yp) {
@@ -433,10 +440,11 @@ cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_
                     const uint32_t parts = parts_of(L, N, hidden);
                     auto with = [&](auto group) {
                         constexpr uint32_t G = decltype(group)::value;
-                        k_moe_combine_bwd<Td, Ty, To, L, N, G><<<(unsigned)ctas((uint64_t)m.tokens * G), kThreads, 0, s>>>(
-                            static_cast<const Td *>(dout), ld_dout, static_cast<const Ty *>(y), ld_y, m.pos, weights,
-                            m.offsets + m.n_experts, static_cast<To *>(dy), ld_dy, dw, m.topk, (uint32_t)hidden,
-                            parts, (uint32_t)m.tokens);
+                        e = launch_in_order(k_moe_combine_bwd<Td, Ty, To, L, N, G>, ctas((uint64_t)m.tokens * G),
+                                            kThreads, s, static_cast<const Td *>(dout), ld_dout,
+                                            static_cast<const Ty *>(y), ld_y, m.pos, weights,
+                                            m.offsets + m.n_experts, static_cast<To *>(dy), ld_dy, dw, m.topk, hidden,
+                                            parts, m.tokens);
                     };
                     // 128 threads a token unless most would idle.  Measured
                     // (32 / 64 / 128 / 256, rows of 2048): 16384 tokens x 6
@@ -455,7 +463,7 @@ cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_
             });
         });
     });
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace ufp4

@@ -19,6 +19,30 @@
 
 namespace ufp4 {
 
+// The row kernels are launched with programmatic stream serialization: the
+// grid is set up while the last CTAs of the kernel before it in the stream
+// end.  Each begins by waiting until its predecessor has completed and its
+// writes are visible; nothing but parameters is read before, and every CTA
+// waits, so a kernel's end implies the end of all before it.  Against plain
+// launches, back to back: 3 to 5 us less between a pass's kernels of 80 to
+// 430 us; 493 x 1408 gated forward 2.6 -> 2.2 us, 128 tokens' combine gradient
+// 4.2 -> 4.0 us.  Allowing the successor explicitly from the start makes the
+// short kernels slower (2.9, 4.6 us): its waiting CTAs take the SMs early.
+__device__ __forceinline__ void begin_in_order() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class... Params, class... Args>
+cudaError_t launch_in_order(void (*kernel)(Params...), uint64_t grid, unsigned block, cudaStream_t s, Args... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(block);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // n / d by a multiplication: q = floor(n m / 2^64) with m = ceil(2^64 / d).
 // m d exceeds 2^64 by less than d, so q is exact while n d < 2^64; the entry
 // points' limits (rows x width < 2^38, width <= 2^24) keep it there.
