@@ -13,8 +13,8 @@
 // measured" is of the 6676 GB/s of a plain copy:
 //   98304 x 1408, fp32 in, BF16 out, INT8 kept:
 //     k_swiglu 232 us, 7.2 TB/s (108 %; reads run faster than a copy), without
-//     checkpoints 190 us; k_swiglu_bwd 197 us (105 %);
-//   65536 x 8192 BF16: k_ckpt_save 249 us (98 %; INT8), k_ckpt_load 230 us
+//     checkpoints 190 us; k_swiglu_bwd 197 us (106 %);
+//   65536 x 8192 BF16: k_ckpt_save 248 us (98 %; INT8), k_ckpt_load 229 us
 //     (106 %).
 // With 8 elements a thread and 16-byte accesses these were 232, 241, 462 and
 // 372 us: too few bytes in flight, and the scale's arithmetic shared by half
@@ -26,7 +26,7 @@
 // block, in singles the warp.  Those two are bound by instructions (72 % of
 // the issue slots in k_ckpt_save): 65536 x 1002 and 1001 BF16 73 and 67 us
 // saved (41 and 44 % of measured), 52 and 56 us restored; x 1000 (whole, by
-// eights) 57 and 39 us, in fp32 52 and 51 us (95 and 97 %).
+// eights) 43 and 38 us, in fp32 50 and 50 us (99 and 98 %).
 #include "common.cuh"
 #include "internal.h"
 #include "rowops.cuh"
@@ -260,12 +260,13 @@ template <class T, int FMT, int L, int N>
 __global__ void __launch_bounds__(kThreads) k_ckpt_save(const T *__restrict__ x, int64_t ld, Ckpt c, int64_t ldc,
                                                         uint32_t cols, uint32_t nb, RowDiv parts, uint64_t work) {
     begin_in_order();
+    // (with an early return for the threads past the end, the eights of a
+    // 65536 x 1000 BF16 tensor take 57 us instead of 44)
     const uint64_t i = part_index<L>();
-    if (i >= work) return;
     const Place<L, N> p(parts, cols, i);
     float v[N] = {};
-    if (L != kWhole || p.part.has(0)) p.part.load(x + p.row * ld, v);
-    keep<FMT>(v, p, c, ldc, nb);
+    if (i < work && (L != kWhole || p.part.has(0))) p.part.load(x + p.row * ld, v);
+    if (i < work) keep<FMT>(v, p, c, ldc, nb);
 }
 
 template <class T, int FMT, int L, int N>
