@@ -228,7 +228,7 @@ __device__ __forceinline__ void restore(const Ckpt &c, const Place<L, N> &p, int
     if constexpr (L == kWhole) {
         uint32_t w[N / 4];
         load_words(codes, w);
-        const float s = scale_of(__ldg(scales));
+        const float s = scale_of(*scales);
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) values4<FMT>(w[i], s, x + 4 * i);
     } else {
@@ -237,14 +237,14 @@ __device__ __forceinline__ void restore(const Ckpt &c, const Place<L, N> &p, int
         const uint32_t lanes = kLanes == 32 ? 0xFFFFFFFFu : 0xFFFFu << first;
         float mine = 0.0f;   // lane k: the scale of the k-th block
         if (k < 8 / kStep && (col - kStep * k) + p.part.at((int)k * kStep) < p.part.cols)
-            mine = scale_of(__ldg(scales + k * kStep));
+            mine = scale_of(scales[k * kStep]);
         uint32_t w[8 / kStep];
 #pragma unroll
         for (int i = 0; i < 8; i += kStep) {
             if constexpr (kStep == 2)
-                w[i / 2] = p.part.has(i) ? __ldg(reinterpret_cast<const uint16_t *>(codes + p.part.at(i))) : 0u;
+                w[i / 2] = p.part.has(i) ? *reinterpret_cast<const uint16_t *>(codes + p.part.at(i)) : 0u;
             else
-                w[i] = p.part.has(i) ? __ldg(codes + p.part.at(i)) : 0u;
+                w[i] = p.part.has(i) ? codes[p.part.at(i)] : 0u;
         }
 #pragma unroll
         for (int i = 0; i < 8; i += kStep) {
@@ -257,12 +257,12 @@ __device__ __forceinline__ void restore(const Ckpt &c, const Place<L, N> &p, int
 
 // ---------------------------------------------------------------- kernels
 template <class T, int FMT, int L, int N>
-__global__ void __launch_bounds__(kThreads) k_ckpt_save(const T *__restrict__ x, int64_t ld, Ckpt c, int64_t ldc,
+__global__ void __launch_bounds__(kThreads) k_ckpt_save(const T *x, int64_t ld, Ckpt c, int64_t ldc,
                                                         uint32_t cols, uint32_t nb, RowDiv parts, uint64_t work) {
-    begin_in_order();
+    const uint32_t zero = begin_in_order();
     // (with an early return for the threads past the end, the eights of a
     // 65536 x 1000 BF16 tensor take 57 us instead of 44)
-    const uint64_t i = part_index<L>();
+    const uint64_t i = part_index<L>() + zero;
     const Place<L, N> p(parts, cols, i);
     float v[N] = {};
     if (i < work && (L != kWhole || p.part.has(0))) p.part.load(x + p.row * ld, v);
@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_save(const T *__restrict__ x,
 template <class T, int FMT, int L, int N>
 __global__ void __launch_bounds__(kThreads) k_ckpt_load(Ckpt c, int64_t ldc, T *__restrict__ x, int64_t ld,
                                                         uint32_t cols, uint32_t nb, RowDiv parts, uint64_t work) {
-    begin_in_order();
-    const uint64_t i = part_index<L>();
+    const uint32_t zero = begin_in_order();
+    const uint64_t i = part_index<L>() + zero;
     if (i >= work) return;
     const Place<L, N> p(parts, cols, i);
     if (L == kWhole && !p.part.has(0)) return;
@@ -283,13 +283,13 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_load(Ckpt c, int64_t ldc, T *
 }
 
 template <class Ti, class To, int FMT, int L, int N>
-__global__ void __launch_bounds__(kThreads) k_swiglu(const Ti *__restrict__ gate, int64_t ld_gate,
-                                                     const Ti *__restrict__ up, int64_t ld_up, To *__restrict__ h,
+__global__ void __launch_bounds__(kThreads) k_swiglu(const Ti *gate, int64_t ld_gate,
+                                                     const Ti *up, int64_t ld_up, To *__restrict__ h,
                                                      int64_t ld_h, Ckpt cg, Ckpt cu, int64_t ldc, uint32_t cols,
                                                      uint32_t nb, RowDiv parts, uint64_t work) {
     constexpr bool kExact = std::is_same<To, float>::value;
-    begin_in_order();
-    const uint64_t i = part_index<L>();
+    const uint32_t zero = begin_in_order();
+    const uint64_t i = part_index<L>() + zero;
     if (i >= work) return;
     const Place<L, N> p(parts, cols, i);
     float g[N] = {}, u[N] = {};
@@ -308,13 +308,13 @@ __global__ void __launch_bounds__(kThreads) k_swiglu(const Ti *__restrict__ gate
 }
 
 template <class Td, class To, int FMT, int L, int N>
-__global__ void __launch_bounds__(kThreads) k_swiglu_bwd(const Td *__restrict__ dh, int64_t ld_dh, Ckpt cg, Ckpt cu,
+__global__ void __launch_bounds__(kThreads) k_swiglu_bwd(const Td *dh, int64_t ld_dh, Ckpt cg, Ckpt cu,
                                                          int64_t ldc, To *__restrict__ dgate, int64_t ld_dgate,
                                                          To *__restrict__ dup, int64_t ld_dup, uint32_t cols,
                                                          uint32_t nb, RowDiv parts, uint64_t work) {
     constexpr bool kExact = std::is_same<To, float>::value;
-    begin_in_order();
-    const uint64_t i = part_index<L>();
+    const uint32_t zero = begin_in_order();
+    const uint64_t i = part_index<L>() + zero;
     if (i >= work) return;
     const Place<L, N> p(parts, cols, i);
     if (L == kWhole && !p.part.has(0)) return;

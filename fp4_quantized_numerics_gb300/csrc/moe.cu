@@ -69,7 +69,7 @@ __device__ __forceinline__ uint32_t cluster_load(const uint32_t *p, uint32_t ran
 
 template <class Id>
 __device__ __forceinline__ uint32_t bucket_of(const Id *ids, uint32_t i, uint32_t E) {
-    const Id id = __ldg(ids + i);
+    const Id id = ids[i];
     return id >= 0 && id < (Id)E ? (uint32_t)id : E;
 }
 
@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32
     __shared__ uint32_t hist[kSortWarps * (kMaxGroups + 1)];   // [warp][bucket]
     __shared__ uint32_t sums[kMaxGroups + 1];                  // this CTA's, read by the others
     __shared__ uint32_t warp_sum[kSortWarps];
-    begin_in_order();
-    const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, B = E + 1, W = blockDim.x / 32;
+    const uint32_t zero = begin_in_order();
+    const uint32_t tid = threadIdx.x + zero, lane = tid & 31u, warp = tid >> 5, B = E + 1, W = blockDim.x / 32;
     const uint32_t rank = cluster_rank(), nctas = cluster_size();
     const uint32_t warps = nctas * W;
     const int bits = 32 - __clz((int)E);
@@ -177,13 +177,13 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32
 // apart.  Bound by DRAM writes: 71 us, 6.6 TB/s (98 % of measured); rows of
 // 1001 BF16 elements 47 us (73 %), bound by the number of 64-byte accesses.
 template <class Unit, int N>
-__global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *__restrict__ x, int64_t ld_x,
+__global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *x, int64_t ld_x,
                                                            Unit *__restrict__ xs, int64_t ld_xs,
-                                                           const int32_t *__restrict__ pos,
-                                                           const int64_t *__restrict__ routed_at, int topk,
+                                                           const int32_t *pos,
+                                                           const int64_t *routed_at, int topk,
                                                            uint32_t width, RowDiv units, uint64_t work) {
-    begin_in_order();
-    uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+    const uint32_t zero = begin_in_order();
+    uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x + zero;
     if constexpr (N > 1) i /= 32;
     if (i >= work) return;
     const uint64_t t = row_of(i, units);
@@ -192,10 +192,10 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *__restric
     Unit v[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) v[e] = c + 32 * e < width ? x[t * ld_x + c + 32 * e] : Unit{};
-    const int32_t routed = (int32_t)__ldg(routed_at);
+    const int32_t routed = (int32_t)routed_at[zero];
     const int32_t *at = pos + t * topk;
     for (int j = 0; j < topk; ++j) {
-        const int32_t p = __ldg(at + j);
+        const int32_t p = at[j];
         Unit *to = xs + (int64_t)p * ld_xs + c;
 #pragma unroll
         for (int e = 0; e < N; ++e)
@@ -214,25 +214,25 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *__restric
 // of 1001 57 us (60 %; two rows at once 74, four 117: neighbouring accesses
 // share sectors, which more rows in flight push out of L1).
 template <class Ty, class To, int L, int N>
-__global__ void __launch_bounds__(kThreads) k_moe_combine(const Ty *__restrict__ y, int64_t ld_y,
-                                                          const int32_t *__restrict__ pos,
-                                                          const float *__restrict__ weights,
-                                                          const int64_t *__restrict__ routed_at, To *__restrict__ out,
+__global__ void __launch_bounds__(kThreads) k_moe_combine(const Ty *y, int64_t ld_y,
+                                                          const int32_t *pos,
+                                                          const float *weights,
+                                                          const int64_t *routed_at, To *__restrict__ out,
                                                           int64_t ld_out, int topk, uint32_t hidden, RowDiv parts,
                                                           uint64_t work) {
-    begin_in_order();
-    uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+    const uint32_t zero = begin_in_order();
+    uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x + zero;
     if (L != kWhole) i /= 32;
     if (i >= work) return;
     const uint64_t t = row_of(i, parts);
     const Part<L, N> part((uint32_t)(i - t * parts.d), hidden);
-    const int32_t routed = (int32_t)__ldg(routed_at);
+    const int32_t routed = (int32_t)routed_at[zero];
     float acc[N] = {};
 #pragma unroll(L == kWhole ? 4 : 1)
     for (int j = 0; j < topk; ++j) {
-        const int32_t p = __ldg(pos + t * topk + j);
+        const int32_t p = pos[t * topk + j];
         if (p >= routed) continue;
-        const float w = weights ? __ldg(weights + t * topk + j) : 1.0f;
+        const float w = weights ? weights[t * topk + j] : 1.0f;
         float v[N];
         part.load(y + (int64_t)p * ld_y, v);
 #pragma unroll
@@ -265,25 +265,25 @@ struct Held {
 
 template <class Td, class Ty, class To, int L, int N, uint32_t G>
 __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(
-    const Td *__restrict__ dout, int64_t ld_dout, const Ty *__restrict__ y, int64_t ld_y,
-    const int32_t *__restrict__ pos, const float *__restrict__ weights, const int64_t *__restrict__ routed_at,
+    const Td *dout, int64_t ld_dout, const Ty *y, int64_t ld_y,
+    const int32_t *pos, const float *weights, const int64_t *routed_at,
     To *__restrict__ dy, int64_t ld_dy, float *__restrict__ dw, int topk, uint32_t hidden, uint32_t parts,
     uint32_t tokens) {
     __shared__ float sums[kThreads / 32][kBatch];
-    begin_in_order();
+    const uint32_t zero = begin_in_order();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x / 32;
     const uint32_t mine = threadIdx.x / G, in_group = threadIdx.x % G;
-    const uint32_t t = blockIdx.x * (kThreads / G) + mine;
+    const uint32_t t = blockIdx.x * (kThreads / G) + mine + zero;
     const bool live = t < tokens;
-    const int32_t routed = (int32_t)__ldg(routed_at);
+    const int32_t routed = (int32_t)routed_at[zero];
     for (int j0 = 0; j0 < topk; j0 += kBatch) {
         int32_t p[kBatch];
         float w[kBatch], dot[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const bool in = live && j0 + j < topk;
-            p[j] = in ? __ldg(pos + (int64_t)t * topk + j0 + j) : -1;
-            w[j] = in && p[j] < routed ? __ldg(weights + (int64_t)t * topk + j0 + j) : 0.0f;
+            p[j] = in ? pos[(int64_t)t * topk + j0 + j] : -1;
+            w[j] = in && p[j] < routed ? weights[(int64_t)t * topk + j0 + j] : 0.0f;
             dot[j] = 0.0f;
         }
         if (live)

@@ -28,7 +28,17 @@ namespace ufp4 {
 // 430 us; 493 x 1408 gated forward 2.6 -> 2.2 us, 128 tokens' combine gradient
 // 4.2 -> 4.0 us.  Allowing the successor explicitly from the start makes the
 // short kernels slower (2.9, 4.6 us): its waiting CTAs take the SMs early.
-__device__ __forceinline__ void begin_in_order() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+//
+// Returns 0, which the compiler does not know: added to the index that every
+// address is made from, it keeps all loads behind the wait, whatever the
+// compiler may assume of the data.  (Outputs are __restrict__, so that loads
+// move past stores; inputs are not, which would make their loads non-coherent
+// ones.)
+__device__ __forceinline__ uint32_t begin_in_order() {
+    uint32_t zero;
+    asm volatile("griddepcontrol.wait;\n\tmov.u32 %0, 0;" : "=r"(zero)::"memory");
+    return zero;
+}
 template <class... Params, class... Args>
 cudaError_t launch_in_order(void (*kernel)(Params...), uint64_t grid, unsigned block, cudaStream_t s, Args... args) {
     cudaLaunchAttribute attr{};
@@ -53,22 +63,25 @@ struct RowDiv {
 inline RowDiv make_rowdiv(uint32_t d) { return RowDiv{d == 1 ? 0 : ~0ull / d + 1, d}; }
 __device__ __forceinline__ uint64_t row_of(uint64_t n, RowDiv f) { return f.m ? __umul64hi(n, f.m) : n; }
 
-// ---------------------------------------------------- 8, 16 and 32 bytes
+// ------------------------------------------------------ 8, 16 and 32 bytes
+// Plain loads, not the non-coherent kind (__ldg), whose data has to stay as it
+// is from the launch on: these kernels are launched before their inputs are
+// complete.
 __device__ __forceinline__ void load_words(const void *p, uint32_t (&w)[2]) {
-    const uint2 v = __ldg(static_cast<const uint2 *>(p));
+    const uint2 v = *static_cast<const uint2 *>(p);
     w[0] = v.x; w[1] = v.y;
 }
-__device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[2]) {
-    *static_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-}
 __device__ __forceinline__ void load_words(const void *p, uint32_t (&w)[4]) {
-    const uint4 v = __ldg(static_cast<const uint4 *>(p));
+    const uint4 v = *static_cast<const uint4 *>(p);
     w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
 }
 __device__ __forceinline__ void load_words(const void *p, uint32_t (&w)[8]) {
-    asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+    asm("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
         : "l"(p));
+}
+__device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[2]) {
+    *static_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 __device__ __forceinline__ void store_words(void *p, const uint32_t (&w)[4]) {
     *static_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -135,14 +148,16 @@ __device__ __forceinline__ void store_whole(float *p, const float (&f)[N]) {
 }
 
 __device__ __forceinline__ float load_one(const __nv_bfloat16 *p) {
-    return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p)) << 16);
+    return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(p) << 16);
 }
-__device__ __forceinline__ float load_one(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float load_one(const float *p) { return *p; }
 __device__ __forceinline__ float2 load_two(const __nv_bfloat16 *p) {
-    const uint32_t w = __ldg(reinterpret_cast<const unsigned int *>(p));
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-__device__ __forceinline__ float2 load_two(const float *p) { return __ldg(reinterpret_cast<const float2 *>(p)); }
+__device__ __forceinline__ float2 load_two(const float *p) {
+    return *reinterpret_cast<const float2 *>(p);
+}
 __device__ __forceinline__ void store_one(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_two(__nv_bfloat16 *p, float a, float b) {
