@@ -177,11 +177,10 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32
 // apart.  Bound by DRAM writes: 71 us, 6.6 TB/s (98 % of measured); rows of
 // 1001 BF16 elements 47 us (73 %), bound by the number of 64-byte accesses.
 template <class Unit, int N>
-__global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *x, int64_t ld_x,
-                                                           Unit *__restrict__ xs, int64_t ld_xs,
-                                                           const int32_t *pos,
-                                                           const int64_t *routed_at, int topk,
-                                                           uint32_t width, RowDiv units, uint64_t work) {
+__global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *x, int64_t ld_x, Unit *__restrict__ xs,
+                                                           int64_t ld_xs, const int32_t *pos,
+                                                           const int64_t *routed_at, int topk, uint32_t width,
+                                                           RowDiv units, uint64_t work) {
     const uint32_t zero = begin_in_order();
     uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x + zero;
     if constexpr (N > 1) i /= 32;
@@ -214,12 +213,10 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *x, int64_
 // of 1001 57 us (60 %; two rows at once 74, four 117: neighbouring accesses
 // share sectors, which more rows in flight push out of L1).
 template <class Ty, class To, int L, int N>
-__global__ void __launch_bounds__(kThreads) k_moe_combine(const Ty *y, int64_t ld_y,
-                                                          const int32_t *pos,
-                                                          const float *weights,
-                                                          const int64_t *routed_at, To *__restrict__ out,
-                                                          int64_t ld_out, int topk, uint32_t hidden, RowDiv parts,
-                                                          uint64_t work) {
+__global__ void __launch_bounds__(kThreads) k_moe_combine(const Ty *y, int64_t ld_y, const int32_t *pos,
+                                                          const float *weights, const int64_t *routed_at,
+                                                          To *__restrict__ out, int64_t ld_out, int topk,
+                                                          uint32_t hidden, RowDiv parts, uint64_t work) {
     const uint32_t zero = begin_in_order();
     uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x + zero;
     if (L != kWhole) i /= 32;
@@ -265,10 +262,9 @@ struct Held {
 
 template <class Td, class Ty, class To, int L, int N, uint32_t G>
 __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(
-    const Td *dout, int64_t ld_dout, const Ty *y, int64_t ld_y,
-    const int32_t *pos, const float *weights, const int64_t *routed_at,
-    To *__restrict__ dy, int64_t ld_dy, float *__restrict__ dw, int topk, uint32_t hidden, uint32_t parts,
-    uint32_t tokens) {
+    const Td *dout, int64_t ld_dout, const Ty *y, int64_t ld_y, const int32_t *pos, const float *weights,
+    const int64_t *routed_at, To *__restrict__ dy, int64_t ld_dy, float *__restrict__ dw, int topk, uint32_t hidden,
+    uint32_t parts, uint32_t tokens) {
     __shared__ float sums[kThreads / 32][kBatch];
     const uint32_t zero = begin_in_order();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x / 32;
@@ -287,8 +283,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(
             dot[j] = 0.0f;
         }
         if (live)
-            for (uint32_t u = L == kWhole ? in_group : in_group / 32; u < parts;
-                 u += L == kWhole ? G : G / 32) {
+            for (uint32_t u = L == kWhole ? in_group : in_group / 32; u < parts; u += L == kWhole ? G : G / 32) {
                 const Part<L, N> part(u, hidden);
                 Held<Td, L, N> d;
                 Held<Ty, L, N> v[kBatch];

@@ -495,12 +495,13 @@ try:
 except ImportError:
     _empty_strided_cuda = None
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_INT32, _INT64, _FLOAT32 = torch.int32, torch.int64, torch.float32
 
 
 def _raw_stream(stream):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(_current_device())
-    return stream.cuda_stream
+    return _current_raw_stream(_current_device()) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype, device):
@@ -513,6 +514,8 @@ def _empty(shape, dtype, device):
 def _device(device):
     """A torch.device with its index."""
     device = torch.device(device)
+    if device.type != "cuda":
+        raise TypeError("libufp4 has no CPU path")
     return device if device.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
@@ -523,12 +526,12 @@ class MoePlan:
     grouped calls; rows past offsets[-1] belong to dropped slots."""
 
     def __init__(self, pos, src, counts, offsets):
-        for t, name, dtype in ((pos, "pos", torch.int32), (src, "src", torch.int32), (counts, "counts", torch.int64),
-                               (offsets, "offsets", torch.int64)):
-            if not t.is_cuda:
-                _cuda(t, name)
-            if t.dtype != dtype or not t.is_contiguous():
-                raise ValueError("%s must be contiguous, %s" % (name, dtype))
+        if not (pos.is_cuda and src.is_cuda and counts.is_cuda and offsets.is_cuda):
+            raise TypeError("the plan's tensors must be CUDA tensors (libufp4 has no CPU path)")
+        if not (pos.dtype is _INT32 and src.dtype is _INT32 and counts.dtype is _INT64 and offsets.dtype is _INT64):
+            raise ValueError("pos and src must be int32, counts and offsets int64")
+        if not (pos.is_contiguous() and src.is_contiguous() and counts.is_contiguous() and offsets.is_contiguous()):
+            raise ValueError("the plan's tensors must be contiguous")
         if pos.dim() != 2:
             raise ValueError("pos must be [tokens, topk]")
         tokens, topk = pos.shape
@@ -550,8 +553,8 @@ class MoePlan:
     @classmethod
     def _new(cls, tokens, topk, n_experts, device):
         plan = cls.__new__(cls)
-        plan._set(_empty((tokens, topk), torch.int32, device), _empty((tokens * topk,), torch.int32, device),
-                  _empty((n_experts,), torch.int64, device), _empty((n_experts + 1,), torch.int64, device),
+        plan._set(_empty((tokens, topk), _INT32, device), _empty((tokens * topk,), _INT32, device),
+                  _empty((n_experts,), _INT64, device), _empty((n_experts + 1,), _INT64, device),
                   tokens, topk, n_experts)
         return plan
 
@@ -596,8 +599,9 @@ def _result(out, name, rows, cols, dtype, device):
 
 
 def _plan_weights(weights, plan, name="weights"):
-    _cuda(weights, name)
-    if weights.dtype != torch.float32 or weights.shape != plan.pos.shape or not weights.is_contiguous():
+    if not weights.is_cuda:
+        _cuda(weights, name)
+    if weights.dtype is not _FLOAT32 or weights.shape != plan.pos.shape or not weights.is_contiguous():
         raise ValueError("%s must be contiguous fp32 [tokens, topk]" % name)
     return weights.data_ptr()
 
@@ -608,7 +612,7 @@ def ufp4_moe_sort(ids, n_experts, out=None, stream=None):
     _cuda(ids, "ids")
     if ids.dim() != 2 or not ids.is_contiguous():
         raise ValueError("ids must be contiguous [tokens, topk]")
-    size = 8 if ids.dtype == torch.int64 else 4 if ids.dtype == torch.int32 else 0
+    size = 8 if ids.dtype is _INT64 else 4 if ids.dtype is _INT32 else 0
     if not size:
         raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
     tokens, topk = ids.shape
@@ -653,7 +657,7 @@ def ufp4_moe_combine_bwd(dout, y, plan, weights, dtype=None, dy=None, dw=None, s
     w = _plan_weights(weights, plan)
     dy, gp, gdt, gld = _result(dy, "dy", rows, hidden, dtype or dout.dtype, y.device)
     if dw is None:
-        dw = _empty((plan.tokens, plan.topk), torch.float32, y.device)
+        dw = _empty((plan.tokens, plan.topk), _FLOAT32, y.device)
     st = lib().ufp4_moe_combine_bwd(dp, ddt, dld, yp, ydt, yld, hidden, plan._c, w, gp, gdt, gld,
                                     _plan_weights(dw, plan, "dw"), _raw_stream(stream))
     _check(st, "ufp4_moe_combine_bwd")
@@ -743,11 +747,11 @@ def ufp4_ckpt_load(c, dtype=torch.bfloat16, out=None, stream=None):
     return out
 
 
-def ufp4_swiglu(gate, up, ckpt=None, dtype=None, out=None, stream=None):
+def ufp4_swiglu(gate, up, ckpt=None, dtype=None, out=None, keep=None, stream=None):
     """h = silu(gate) * up, and gate's and up's 8-bit checkpoints for the
-    backward pass (ckpt: their format, or None to keep nothing).  Returns
-    (h, keep_gate, keep_up), the latter two None without ckpt.  dtype: h's
-    (gate's by default)."""
+    backward pass (ckpt: their format, or None to keep nothing; keep: a pair
+    of Ckpts to write instead of new ones).  Returns (h, keep_gate, keep_up),
+    the latter two None if nothing is kept.  dtype: h's (gate's by default)."""
     gp, dt, gld, rows, cols = _rows2d(gate, "gate")
     up_p, udt, uld, _, _ = _rows2d(up, "up", rows, cols)
     if udt != dt:
@@ -755,7 +759,9 @@ def ufp4_swiglu(gate, up, ckpt=None, dtype=None, out=None, stream=None):
     device = gate.device
     out, hp, hdt, hld = _result(out, "out", rows, cols, dtype or gate.dtype, device)
     kg = ku = None
-    if ckpt is not None:
+    if keep is not None:
+        kg, ku = keep
+    elif ckpt is not None:
         kg, ku = Ckpt._new(2, rows, cols, ckpt, device)
     st = lib().ufp4_swiglu(gp, gld, up_p, uld, dt, rows, cols, hp, hdt, hld, kg and kg._c, ku and ku._c,
                            _raw_stream(stream))

@@ -431,7 +431,8 @@ UFP4_API ufp4_status ufp4_gemm_grouped(const ufp4_qtensor *a, const ufp4_qtensor
  *   offsets : int64 [n_experts + 1], first place of each expert; the last
  *             entry is the number of routed slots.
  * Places offsets[n_experts] .. n-1 belong to dropped slots.  pos and src
- * 4-byte, counts and offsets 8-byte aligned. */
+ * 4-byte, counts and offsets 8-byte aligned.  The calls below take the plan as
+ * ufp4_moe_sort wrote it: its contents are device data and not checked. */
 typedef struct {
     int32_t *pos;
     int32_t *src;

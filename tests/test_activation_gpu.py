@@ -185,6 +185,37 @@ def test_non_finite_gradient_flow(U, fmt):
         assert nan[0, :32].all() and nan.sum() == 32
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_kept_buffers_of_the_caller(U, fmt):
+    """Checkpoints written into the caller's, on a side stream and in a graph;
+    a pair of another shape or of two formats is refused."""
+    g = np.random.default_rng(13)
+    gate, up = _tensor(_values(g, 40, 96), BF), _tensor(_values(g, 40, 96), BF)
+    h, kg, ku = U.ufp4_swiglu(gate, up, ckpt=fmt)
+    keep = U.Ckpt.empty(40, 96, fmt), U.Ckpt.empty(40, 96, fmt)
+    out = torch.empty_like(gate)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert U.ufp4_swiglu(gate, up, out=out, keep=keep, stream=side)[1] is keep[0]
+    side.synchronize()
+    for a, b in ((keep[0], kg), (keep[1], ku)):
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+        a.codes.zero_()
+        a.scales.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        U.ufp4_swiglu(gate, up, out=out, keep=keep)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, h)
+    for a, b in ((keep[0], kg), (keep[1], ku)):
+        assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+    for bad in ((keep[0], U.Ckpt.empty(40, 96, 1 - fmt)), (keep[0], U.Ckpt.empty(40, 64, fmt))):
+        with pytest.raises(U.UFP4Error):
+            U.ufp4_swiglu(gate, up, keep=bad)
+
+
 def test_no_rows(U):
     e = torch.empty(0, 64, device="cuda")
     h, kg, ku = U.ufp4_swiglu(e, e, ckpt=0)
