@@ -14,8 +14,8 @@
 //   98304 x 1408, fp32 in, BF16 out, INT8 kept:
 //     k_swiglu 232 us, 7.2 TB/s (108 %; reads run faster than a copy), without
 //     checkpoints 190 us; k_swiglu_bwd 197 us (106 %);
-//   65536 x 8192 BF16: k_ckpt_save 248 us (98 %; INT8), k_ckpt_load 229 us
-//     (106 %).
+//   65536 x 8192 BF16: k_ckpt_save 243 us (INT8; E4M3 228; 100 and 107 %),
+//     k_ckpt_load 229 us (106 %).
 // With 8 elements a thread and 16-byte accesses these were 232, 241, 462 and
 // 372 us: too few bytes in flight, and the scale's arithmetic shared by half
 // as many elements.
@@ -24,9 +24,9 @@
 // where rows allow no more) and two (four) neighbouring lanes one 32-element
 // block; in pairs a half warp owns each
 // block, in singles the warp.  Those two are bound by instructions (72 % of
-// the issue slots in k_ckpt_save): 65536 x 1002 and 1001 BF16 73 and 67 us
-// saved (41 and 44 % of measured), 52 and 56 us restored; x 1000 (whole, by
-// eights) 43 and 38 us, in fp32 50 and 50 us (99 and 98 %).
+// the issue slots in k_ckpt_save): 65536 x 1002 and 1001 BF16 72 and 64 us
+// saved (41 and 46 % of measured), 49 and 52 us restored; x 1000 (whole, by
+// eights) 43 and 37 us, in fp32 49 and 49 us (100 %).
 #include "common.cuh"
 #include "internal.h"
 #include "rowops.cuh"
@@ -40,7 +40,9 @@ namespace ufp4 {
 
 namespace {
 
-constexpr int kThreads = 256;
+// 256 threads a CTA are up to 10 % slower where the launch counts and 3-6 % on
+// BF16 tensors, 64 up to 80 % (too few resident warps for the lighter kernels).
+constexpr int kThreads = 128;
 constexpr int kInt8 = 0, kE4M3 = 1, kNone = -1;
 
 // ------------------------------------------------------------ block scales

@@ -246,9 +246,10 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine(const Ty *y, int64_t l
 // over the warp that halves the number of sums at each step, then one
 // addition per warp in shared memory, joins them in an order that depends on
 // nothing but the sizes and the layout.  Bound by DRAM: fp32 y, BF16 dout and
-// dy 189 us, 6.7 TB/s (101 % of measured; one choice after the other 245);
-// 8192 x 2 rows of 8192 BF16 102 us (98 %).
-constexpr int kBatch = 4;
+// dy 181 us, 7.0 TB/s (106 % of measured; one choice after the other 245);
+// 8192 x 2 rows of 8192 BF16 100 us (101 %); rows of 1001 BF16 47 us (47 %).
+// One token a CTA: with two (256 threads) 188, 102 and 58 us.
+constexpr int kBatch = 4, kBwdThreads = 128;
 
 // y's elements of one part: raw in the whole layout, else as fp32.
 template <class Ty, int L, int N>
@@ -261,15 +262,15 @@ struct Held {
 };
 
 template <class Td, class Ty, class To, int L, int N, uint32_t G>
-__global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(
+__global__ void __launch_bounds__(kBwdThreads) k_moe_combine_bwd(
     const Td *dout, int64_t ld_dout, const Ty *y, int64_t ld_y, const int32_t *pos, const float *weights,
     const int64_t *routed_at, To *__restrict__ dy, int64_t ld_dy, float *__restrict__ dw, int topk, uint32_t hidden,
     uint32_t parts, uint32_t tokens) {
-    __shared__ float sums[kThreads / 32][kBatch];
+    __shared__ float sums[kBwdThreads / 32][kBatch];
     const uint32_t zero = begin_in_order();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x / 32;
     const uint32_t mine = threadIdx.x / G, in_group = threadIdx.x % G;
-    const uint32_t t = blockIdx.x * (kThreads / G) + mine + zero;
+    const uint32_t t = blockIdx.x * (kBwdThreads / G) + mine + zero;
     const bool live = t < tokens;
     const int32_t routed = (int32_t)routed_at[zero];
     for (int j0 = 0; j0 < topk; j0 += kBatch) {
@@ -435,8 +436,8 @@ cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_
                     const uint32_t parts = parts_of(L, N, hidden);
                     auto with = [&](auto group) {
                         constexpr uint32_t G = decltype(group)::value;
-                        e = launch_in_order(k_moe_combine_bwd<Td, Ty, To, L, N, G>, ctas((uint64_t)m.tokens * G),
-                                            kThreads, s, static_cast<const Td *>(dout), ld_dout,
+                        e = launch_in_order(k_moe_combine_bwd<Td, Ty, To, L, N, G>, ((uint64_t)m.tokens * G + kBwdThreads - 1) / kBwdThreads,
+                                            kBwdThreads, s, static_cast<const Td *>(dout), ld_dout,
                                             static_cast<const Ty *>(y), ld_y, m.pos, weights,
                                             m.offsets + m.n_experts, static_cast<To *>(dy), ld_dy, dw, m.topk, hidden,
                                             parts, m.tokens);
