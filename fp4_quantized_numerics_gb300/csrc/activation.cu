@@ -124,8 +124,8 @@ __device__ __forceinline__ void values4(uint32_t w, float scale, float *x) {
 
 // ------------------------------------------------------------- activation
 // 1 / (1 + exp(-g)).  EXACT (fp32 results): the library's exp and division;
-// otherwise the fast forms, whose relative error (below 2^-20 where the
-// result is not tiny) disappears in the rounding to bf16.
+// otherwise the fast forms, whose relative error (within (6 + 1.2 |g|) 2^-23,
+// and a result below 2^-118 may become 0) disappears in the rounding to bf16.
 template <bool EXACT>
 __device__ __forceinline__ float sigmoid(float g) {
     if constexpr (EXACT) return 1.0f / (1.0f + expf(-g));

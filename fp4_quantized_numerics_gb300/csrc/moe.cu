@@ -205,20 +205,25 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *x, int64_
 // ---------------------------------------------------------------- combine
 // A thread owns N elements of an output row (32 bytes of y in the whole
 // layout); the topk rows are added in ascending order of choice, in fp32, and
-// rounded once.  Bound by DRAM reads: fp32 to BF16 125 us, 7.0 TB/s (104 % of
-// measured: reads run faster than a copy); 16384 x 8 BF16 rows of 4096 179 us
-// (101 %; 203 us with 16-byte accesses).  Loading the rows of several choices
+// rounded once.  Bound by DRAM reads: fp32 to BF16 124 us, 7.0 TB/s (105 % of
+// measured: reads run faster than a copy); 16384 x 8 BF16 rows of 4096 178 us
+// (102 %; 203 us with 16-byte accesses).  Loading the rows of several choices
 // before adding them takes registers, and so warps: 155 us.  Off the whole
-// layout the loop stays rolled: rows of 1002 BF16 45 us (77 %; unrolled 53),
-// of 1001 57 us (60 %; two rows at once 74, four 117: neighbouring accesses
+// layout the loop stays rolled: rows of 1002 BF16 43 us (80 %; unrolled 53),
+// of 1001 54 us (64 %; two rows at once 74, four 117: neighbouring accesses
 // share sectors, which more rows in flight push out of L1).
+//
+// CTAs of 128 threads are 1-5 % faster, and 4 % slower with 16 elements a
+// thread.
+template <int N>
+constexpr int kCombineThreads = N == 16 ? 256 : 128;
+
 template <class Ty, class To, int L, int N>
-__global__ void __launch_bounds__(kThreads) k_moe_combine(const Ty *y, int64_t ld_y, const int32_t *pos,
-                                                          const float *weights, const int64_t *routed_at,
-                                                          To *__restrict__ out, int64_t ld_out, int topk,
-                                                          uint32_t hidden, RowDiv parts, uint64_t work) {
+__global__ void __launch_bounds__(kCombineThreads<N>)
+    k_moe_combine(const Ty *y, int64_t ld_y, const int32_t *pos, const float *weights, const int64_t *routed_at,
+                  To *__restrict__ out, int64_t ld_out, int topk, uint32_t hidden, RowDiv parts, uint64_t work) {
     const uint32_t zero = begin_in_order();
-    uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x + zero;
+    uint64_t i = (uint64_t)blockIdx.x * kCombineThreads<N> + threadIdx.x + zero;
     if (L != kWhole) i /= 32;
     if (i >= work) return;
     const uint64_t t = row_of(i, parts);
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kBwdThreads) k_moe_combine_bwd(
 // 9.0 / 5.8 / 6.0 us, 98304 slots 72 / 14 / 10 us.
 int sort_ctas(uint32_t n) { return n <= 1024 ? 1 : n <= 8192 ? 8 : kMaxSortCtas; }
 
-inline uint64_t ctas(uint64_t work) { return (work + kThreads - 1) / kThreads; }
+inline uint64_t ctas(uint64_t work, int threads = kThreads) { return (work + threads - 1) / threads; }
 
 template <class Unit, int N>
 cudaError_t dispatch(const void *x, int64_t ldx, void *xs, int64_t ldxs, int64_t row_bytes, const MoePlan &m,
@@ -396,7 +401,8 @@ cudaError_t launch_moe_combine(const void *y, int y_dtype, int64_t hidden, int64
         const uint64_t work = (uint64_t)m.tokens * parts;
         using Ty = Elem<decltype(yp)>;
         using To = Elem<decltype(op)>;
-        e = launch_in_order(k_moe_combine<Ty, To, L, N>, ctas(threads_of(L, work)), kThreads, s,
+        e = launch_in_order(k_moe_combine<Ty, To, L, N>, ctas(threads_of(L, work), kCombineThreads<N>),
+                            kCombineThreads<N>, s,
                             static_cast<const Ty *>(y), ld_y, m.pos, weights, m.offsets + m.n_experts,
                             static_cast<To *>(out), ld_out, m.topk, hidden, make_rowdiv(parts), work);
     };
@@ -436,11 +442,11 @@ cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_
                     const uint32_t parts = parts_of(L, N, hidden);
                     auto with = [&](auto group) {
                         constexpr uint32_t G = decltype(group)::value;
-                        e = launch_in_order(k_moe_combine_bwd<Td, Ty, To, L, N, G>, ((uint64_t)m.tokens * G + kBwdThreads - 1) / kBwdThreads,
-                                            kBwdThreads, s, static_cast<const Td *>(dout), ld_dout,
-                                            static_cast<const Ty *>(y), ld_y, m.pos, weights,
-                                            m.offsets + m.n_experts, static_cast<To *>(dy), ld_dy, dw, m.topk, hidden,
-                                            parts, m.tokens);
+                        e = launch_in_order(
+                            k_moe_combine_bwd<Td, Ty, To, L, N, G>, ctas((uint64_t)m.tokens * G, kBwdThreads),
+                            kBwdThreads, s, static_cast<const Td *>(dout), ld_dout, static_cast<const Ty *>(y), ld_y,
+                            m.pos, weights, m.offsets + m.n_experts, static_cast<To *>(dy), ld_dy, dw, m.topk, hidden,
+                            parts, m.tokens);
                     };
                     // 128 threads a token unless most would idle.  Measured
                     // (32 / 64 / 128 / 256, rows of 2048): 16384 tokens x 6
