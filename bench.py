@@ -642,7 +642,8 @@ def run_kernel(args):
     after `warmup` launches, the tensor amax given (quant_resident_e1m2: W,
     F x H, both ways with its maxima, the on-chip single pass; quant_grouped_dual_e1m2:
     the MoE-7.9B X both ways, its amax pass included; moe_*, ckpt_*, swiglu*:
-    the calls around that layer's grouped GEMMs).  --shape dense: T, H, F = 8192, 2048, 5632; moe124b: 65536, 8192, 2048.  Prints the mean event
+    the calls around that layer's grouped GEMMs).  --shape dense: T, H, F =
+    8192, 2048, 5632; moe124b: 65536, 8192, 2048.  Prints the mean event
     time."""
     import torch
     from fp4_quantized_numerics_gb300 import build, inputs, ufp4 as U

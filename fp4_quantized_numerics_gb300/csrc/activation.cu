@@ -24,9 +24,10 @@
 // where rows allow no more) and two (four) neighbouring lanes one 32-element
 // block; in pairs a half warp owns each
 // block, in singles the warp.  Those two are bound by instructions (72 % of
-// the issue slots in k_ckpt_save): 65536 x 1002 and 1001 BF16 72 and 64 us
-// saved (41 and 46 % of measured), 49 and 52 us restored; x 1000 (whole, by
-// eights) 43 and 37 us, in fp32 49 and 49 us (100 %).
+// the issue slots in k_ckpt_save): 65536 x 1002 and 1001 BF16 58 and 64 us
+// saved (52 and 47 % of measured; with a warp reduction per block 72 and 64),
+// 49 and 52 us restored; x 1000 (whole, by eights) 43 and 37 us, in fp32 49
+// and 49 us (100 %).
 #include "common.cuh"
 #include "internal.h"
 #include "rowops.cuh"
@@ -191,27 +192,34 @@ __device__ __forceinline__ void keep(const float (&x)[N], const Place<L, N> &p, 
         for (int i = 0; i < N / 4; ++i) w[i] = b == 255u ? 0u : codes4<FMT>(x + 4 * i, inv);
         store_words(codes, w);
     } else {
-        // the blocks' maxima reach all their lanes; lane k of a block's lanes
-        // turns the k-th maximum into a scale and writes it, and the others
-        // take the factor from there
+        // 8 / kStep maxima over 32 / kStep lanes: three (two) exchanges that
+        // halve their number and two that join; lanes 4 k .. 4 k + 3 of a
+        // block's lanes end up with the k-th, turn it into a scale, and the
+        // others take the factor from there
         constexpr int kStep = L == kPairs ? 2 : 1, kLanes = 32 / kStep;
-        const uint32_t lane = threadIdx.x & 31u, k = lane % kLanes, first = lane - k;
-        const uint32_t lanes = kLanes == 32 ? 0xFFFFFFFFu : 0xFFFFu << first;
-        uint32_t mine = 0;
+        const uint32_t lane = threadIdx.x & 31u, first = lane & ~(kLanes - 1u), k = lane % kLanes / 4;
+        uint32_t m[8 / kStep];
 #pragma unroll
-        for (int i = 0; i < 8; i += kStep) {
-            uint32_t m = abs_bits(x[i]);
-            if (kStep == 2) m = max(m, abs_bits(x[i + 1]));
-            m = __reduce_max_sync(lanes, m);
-            if (k == (uint32_t)(i / kStep)) mine = m;
+        for (int i = 0; i < 8; i += kStep)
+            m[i / kStep] = kStep == 2 ? max(abs_bits(x[i]), abs_bits(x[i + kStep - 1])) : abs_bits(x[i]);
+#pragma unroll
+        for (int n = 4 / kStep, d = kLanes / 2; n; n /= 2, d /= 2) {
+            const bool upper = lane & d;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const uint32_t mine = upper ? m[i + n] : m[i], theirs = upper ? m[i] : m[i + n];
+                m[i] = max(mine, __shfl_xor_sync(0xFFFFFFFFu, theirs, d));
+            }
         }
-        const uint32_t b = scale_byte<FMT>(mine);
-        if (k < 8 / kStep && (col - kStep * k) + p.part.at((int)k * kStep) < p.part.cols)
-            scales[k * kStep] = (uint8_t)b;
+        m[0] = max(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], 2));
+        m[0] = max(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], 1));
+        const uint32_t b = scale_byte<FMT>(m[0]);
+        const uint32_t start = col - kStep * (lane - first) + p.part.at((int)k * kStep);   // of the k-th block
+        if (lane % 4 == 0 && start < p.part.cols) scales[k * kStep] = (uint8_t)b;
         const float inv = scale_inv(b);
 #pragma unroll
         for (int i = 0; i < 8; i += kStep) {
-            const float f = __shfl_sync(lanes, inv, first + i / kStep);
+            const float f = __shfl_sync(0xFFFFFFFFu, inv, first + 4 * (i / kStep));
             if (!p.part.has(i)) continue;
             const uint32_t c0 = block_code<FMT>(x[i], f);
             if constexpr (kStep == 2)
@@ -451,8 +459,9 @@ cudaError_t launch_swiglu_bwd(const void *dh, int dh_dtype, int64_t ld_dh, const
             using To = Elem<decltype(to)>;
             by_format(fmt, [&](auto f) {
                 by_layout(g, [&](auto w, auto n) {
-                    e = launch_in_order(k_swiglu_bwd<Td, To, decltype(f)::value, decltype(w)::value, decltype(n)::value>,
-                                        g.ctas, kThreads, s, static_cast<const Td *>(dh), ld_dh, cg, cu, ckpt_ld(cols),
+                    constexpr int kL = decltype(w)::value, N = decltype(n)::value;
+                    e = launch_in_order(k_swiglu_bwd<Td, To, decltype(f)::value, kL, N>, g.ctas, kThreads, s,
+                                        static_cast<const Td *>(dh), ld_dh, cg, cu, ckpt_ld(cols),
                                         static_cast<To *>(dgate), ld_dgate, static_cast<To *>(dup), ld_dup, cols, g.nb,
                                         g.parts, g.work);
                 });
