@@ -32,13 +32,14 @@ constexpr int kThreads = 256;
 //   3. A warp takes 32 slots at a time; lanes of one expert find each other
 //      by one ballot per bit of the expert's number, and a lane's place is
 //      the warp's running place plus the number of such lanes before it.
-// One launch and no scratch memory: 98304 slots take 10 us, of which about 4
+// One launch and no scratch memory: 98304 slots take 9 us, of which about 4
 // are the steps between the passes and the launch; the passes are bound by
 // the integer pipe of the cluster's 16 SMs (142 warp instructions per 32
-// slots at 256 experts; 524288 slots 33 us).  Measured slower: one CTA (72
-// us), __match_any_sync for the ballots (12), ranks kept from the first pass
-// through pos (12).  More clusters and two more kernels that join them win
-// only above some 200000 slots (524288: 18 us; 98304: 9 to 10).
+// slots at 256 experts; 524288 slots 31 us).  Measured slower: one CTA (71
+// us), __match_any_sync for the ballots (2 us more), ranks kept from the
+// first pass through pos (2 us more).  More clusters and two more kernels
+// that join them win only above some 200000 slots (524288: 18 us; 98304: 9
+// to 10).
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxSortCtas = 16;
@@ -106,24 +107,26 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32
     for (uint32_t i = lo + lane; i < hi; i += 32) atomicAdd(mine + bucket_of(ids, i, E), 1u);
     __syncthreads();
 
+    uint32_t total = 0, before_me = 0;   // of bucket tid: in all CTAs, in those before this one
     if (tid < B) {
-        uint32_t t = 0;
 #pragma unroll 8
-        for (uint32_t w = 0; w < W; ++w) t += hist[w * B + tid];
-        sums[tid] = t;
+        for (uint32_t w = 0; w < W; ++w) total += hist[w * B + tid];
+        sums[tid] = total;
     }
-    cluster_arrive();
-    cluster_wait();
-    uint32_t total = 0, before_me = 0;
-    if (tid < B) {
+    if (nctas > 1) {
+        cluster_arrive();
+        cluster_wait();
+        if (tid < B) {
+            total = 0;
 #pragma unroll 8
-        for (uint32_t r = 0; r < nctas; ++r) {
-            const uint32_t c = cluster_load(sums + tid, r);
-            total += c;
-            before_me += r < rank ? c : 0u;
+            for (uint32_t r = 0; r < nctas; ++r) {
+                const uint32_t c = cluster_load(sums + tid, r);
+                total += c;
+                before_me += r < rank ? c : 0u;
+            }
         }
+        cluster_arrive();   // this CTA has read the others' sums; waited for before it ends
     }
-    cluster_arrive();   // this CTA has read the others' sums; waited for before it ends
     // exclusive sum of the totals over the buckets
     uint32_t incl = total;
 #pragma unroll
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32
             src[p] = (int32_t)i;
         }
     }
-    cluster_wait();
+    if (nctas > 1) cluster_wait();
 }
 
 // --------------------------------------------------------------- dispatch
@@ -333,10 +336,10 @@ __global__ void __launch_bounds__(kBwdThreads) k_moe_combine_bwd(
     }
 }
 
-// CTAs of the sort's cluster.  The steps between the passes cost about 3 us
-// in one CTA, 4 in several; the passes cost 0.8 us per 1024 slots of a CTA.
-// Measured (1 / 8 / 16 CTAs): 6 slots 3.0 / 3.8 / 3.8 us, 6144 slots
-// 9.0 / 5.8 / 6.0 us, 98304 slots 72 / 14 / 10 us.
+// CTAs of the sort's cluster: the steps between the passes cost 1 us more in
+// several, the passes 0.7 us per 1024 slots of a CTA.  Measured over 64
+// experts (1 / 8 / 16 CTAs): 512 slots 2.3 / 3.5 / 3.7 us, 2048 slots 4.3 /
+// 4.2 / 4.5, 8192 slots 8.3 / 4.4 / 4.5, 98304 slots 71 / 13 / 9.0.
 int sort_ctas(uint32_t n) { return n <= 1024 ? 1 : n <= 8192 ? 8 : kMaxSortCtas; }
 
 inline uint64_t ctas(uint64_t work, int threads = kThreads) { return (work + threads - 1) / threads; }
