@@ -523,7 +523,8 @@ UFP4_API ufp4_status ufp4_ckpt_load(const ufp4_ckpt *c, void *x, int32_t dtype, 
 
 /* The gated activation between an expert's two products, h = silu(gate) * up
  * with silu(g) = g / (1 + exp(-g)), and, from the same read, the 8-bit
- * checkpoints that ufp4_swiglu_bwd takes.
+ * checkpoints that ufp4_swiglu_bwd takes.  Where 1 / (1 + exp(-g)) is below
+ * 2^-251 (g < -174), it may be taken as 0, here and in the gradients.
  *   gate, up : rows x cols of in_dtype (two halves of one product's output,
  *              or two tensors; each with its own row stride);
  *   h        : rows x cols of h_dtype, from the unrounded gate and up;
