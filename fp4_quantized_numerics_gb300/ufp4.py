@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the hot path runs in the library's
 CUDA kernels.  PyTorch provides device memory and the current stream.  There
 is no fallback: if libufp4.so is missing or a tensor is not on a CUDA device,
-the calls raise.
+the calls raise.  The library launches on the current device: tensors and
+streams of another one are refused (call under torch.cuda.device).
 
 The functions carry the C names:
   ufp4_quantize(x, grid, ...) -> QTensor
@@ -178,15 +179,30 @@ def _check(status, what):
         raise UFP4Error(status, what)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
+    else:
+        _here(stream.device_index, "stream")
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _cuda(t, name):
+def _on_gpu(t, name):
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise TypeError("%s must be a CUDA tensor (libufp4 has no CPU path)" % name)
+
+
+def _cuda(t, name):
+    _on_gpu(t, name)
+    _here(t.get_device(), name)
+
+
+def _here(index, name):
+    if index != _current_device():
+        raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, index, _current_device()))
 
 
 _workspaces = {}
@@ -474,6 +490,8 @@ def ufp4_quantize_grouped_dual(x, grid, seg_rows, rht=False, rht_seed=0, round=U
 def ufp4_gemm_grouped(a, b, groups, stream=None):
     """groups: list of dicts with keys M, N, K, a_row, a_k, b_row, b_k, a_seg,
     b_seg and c (an fp32 CUDA tensor view of M x N with unit column stride)."""
+    _cuda(a.codes, "a.codes")
+    _cuda(b.codes, "b.codes")
     arr = (GemmGroupC * max(len(groups), 1))()
     for i, g in enumerate(groups):
         c = g["c"]
@@ -494,21 +512,40 @@ try:
     from torch._C._dynamo.guards import _empty_strided_cuda
 except ImportError:
     _empty_strided_cuda = None
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _INT32, _INT64, _FLOAT32 = torch.int32, torch.int64, torch.float32
 
 
-def _raw_stream(stream):
-    return _current_raw_stream(_current_device()) if stream is None else stream.cuda_stream
+def _place(t, name):
+    """Device index of a call's first operand: the current device."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        _on_gpu(t, name)
+    dev = t.get_device()
+    if dev != _current_device():
+        _here(dev, name)
+    return dev
 
 
-def _empty(shape, dtype, device):
-    """A fresh contiguous tensor (one or two dims) on a CUDA device."""
-    if _empty_strided_cuda is not None and device.index == _current_device():
+def _same_place(index, dev, name):
+    if index < 0:
+        raise TypeError("%s must be a CUDA tensor (libufp4 has no CPU path)" % name)
+    if index != dev:
+        raise ValueError("%s is on cuda:%d, the other operands are on cuda:%d" % (name, index, dev))
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return _current_raw_stream(dev)
+    _same_place(stream.device_index, dev, "stream")
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype, dev):
+    """A fresh contiguous tensor (one or two dims) on the current device."""
+    if _empty_strided_cuda is not None:
         return _empty_strided_cuda(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
-    return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
 
 
 def _device(device):
@@ -528,6 +565,9 @@ class MoePlan:
     def __init__(self, pos, src, counts, offsets):
         if not (pos.is_cuda and src.is_cuda and counts.is_cuda and offsets.is_cuda):
             raise TypeError("the plan's tensors must be CUDA tensors (libufp4 has no CPU path)")
+        dev = pos.get_device()
+        if not (src.get_device() == dev and counts.get_device() == dev and offsets.get_device() == dev):
+            raise ValueError("the plan's tensors must be on one device")
         if not (pos.dtype is _INT32 and src.dtype is _INT32 and counts.dtype is _INT64 and offsets.dtype is _INT64):
             raise ValueError("pos and src must be int32, counts and offsets int64")
         if not (pos.is_contiguous() and src.is_contiguous() and counts.is_contiguous() and offsets.is_contiguous()):
@@ -538,24 +578,26 @@ class MoePlan:
         n_experts = counts.numel()
         if src.numel() != tokens * topk or offsets.numel() != n_experts + 1:
             raise ValueError("src must have pos's elements, offsets one more than counts")
-        self._set(pos, src, counts, offsets, tokens, topk, n_experts)
+        self._set(pos, src, counts, offsets, tokens, topk, n_experts, dev)
 
-    def _set(self, pos, src, counts, offsets, tokens, topk, n_experts):
+    def _set(self, pos, src, counts, offsets, tokens, topk, n_experts, dev):
         self.pos, self.src, self.counts, self.offsets = pos, src, counts, offsets
-        self.tokens, self.topk, self.n_experts = tokens, topk, n_experts
+        self.tokens, self.topk, self.n_experts, self._dev = tokens, topk, n_experts, dev
         self._c = ctypes.byref(MoePlanC(pos.data_ptr(), src.data_ptr(), counts.data_ptr(), offsets.data_ptr(),
                                         tokens, topk, n_experts, 0))
 
     @classmethod
     def empty(cls, tokens, topk, n_experts, device="cuda"):
-        return cls._new(tokens, topk, n_experts, _device(device))
+        device = _device(device)
+        with torch.cuda.device(device):
+            return cls._new(tokens, topk, n_experts, device.index)
 
     @classmethod
-    def _new(cls, tokens, topk, n_experts, device):
+    def _new(cls, tokens, topk, n_experts, dev):
         plan = cls.__new__(cls)
-        plan._set(_empty((tokens, topk), _INT32, device), _empty((tokens * topk,), _INT32, device),
-                  _empty((n_experts,), _INT64, device), _empty((n_experts + 1,), _INT64, device),
-                  tokens, topk, n_experts)
+        plan._set(_empty((tokens, topk), _INT32, dev), _empty((tokens * topk,), _INT32, dev),
+                  _empty((n_experts,), _INT64, dev), _empty((n_experts + 1,), _INT64, dev),
+                  tokens, topk, n_experts, dev)
         return plan
 
     def c(self):
@@ -565,11 +607,13 @@ class MoePlan:
 _DTYPES = {torch.bfloat16: UFP4_BF16, torch.float32: UFP4_FP32}
 
 
-def _rows2d(t, name, rows=None, cols=None):
-    """Checks a 2-D CUDA tensor with unit stride in its last dim, of the given
-    shape.  Returns its pointer, dtype code, row stride, rows and cols."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
-        _cuda(t, name)
+def _rows2d(t, name, dev, rows=None, cols=None):
+    """Checks a 2-D tensor on device `dev` with unit stride in its last dim, of
+    the given shape.  Returns its pointer, dtype code, row stride, rows and cols."""
+    if not isinstance(t, torch.Tensor):
+        _on_gpu(t, name)
+    if t.get_device() != dev:
+        _same_place(t.get_device(), dev, name)
     shape = t.shape
     if len(shape) != 2:
         raise ValueError("%s must be 2-D" % name)
@@ -585,22 +629,29 @@ def _rows2d(t, name, rows=None, cols=None):
     return t.data_ptr(), _dtype_code(t) if dt is None else dt, ld, r, c
 
 
-def _result(out, name, rows, cols, dtype, device):
+def _result(out, name, rows, cols, dtype, dev):
     """A fresh rows x cols result, or the caller's, checked: the tensor, its
     pointer, dtype code and row stride."""
     if out is None:
         dt = _DTYPES.get(dtype)
         if dt is None:
             raise TypeError("%s must be bf16 or fp32, got %s" % (name, dtype))
-        out = _empty((rows, cols), dtype, device)
+        out = _empty((rows, cols), dtype, dev)
         return out, out.data_ptr(), dt, cols
-    p, dt, ld, _, _ = _rows2d(out, name, rows, cols)
+    p, dt, ld, _, _ = _rows2d(out, name, dev, rows, cols)
     return out, p, dt, ld
 
 
-def _plan_weights(weights, plan, name="weights"):
-    if not weights.is_cuda:
-        _cuda(weights, name)
+def _struct(held, dev, name="plan"):
+    """The C struct of a plan or checkpoint on device `dev`."""
+    if held._dev != dev:
+        _same_place(held._dev, dev, name)
+    return held._c
+
+
+def _plan_weights(weights, plan, dev, name="weights"):
+    if weights.get_device() != dev:
+        _same_place(weights.get_device(), dev, name)
     if weights.dtype is not _FLOAT32 or weights.shape != plan.pos.shape or not weights.is_contiguous():
         raise ValueError("%s must be contiguous fp32 [tokens, topk]" % name)
     return weights.data_ptr()
@@ -609,18 +660,19 @@ def _plan_weights(weights, plan, name="weights"):
 def ufp4_moe_sort(ids, n_experts, out=None, stream=None):
     """Stable sort of the slots of ids ([tokens, topk], int32 or int64) by
     expert; ids outside [0, n_experts) are dropped.  Returns a MoePlan."""
-    _cuda(ids, "ids")
+    dev = _place(ids, "ids")
     if ids.dim() != 2 or not ids.is_contiguous():
         raise ValueError("ids must be contiguous [tokens, topk]")
     size = 8 if ids.dtype is _INT64 else 4 if ids.dtype is _INT32 else 0
     if not size:
         raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
     tokens, topk = ids.shape
+    s = _raw_stream(stream, dev)
     if out is None:
-        out = MoePlan._new(tokens, topk, n_experts, ids.device)
+        out = MoePlan._new(tokens, topk, n_experts, dev)
     elif (out.tokens, out.topk, out.n_experts) != (tokens, topk, n_experts):
         raise ValueError("out is a plan of another size")
-    st = lib().ufp4_moe_sort(ids.data_ptr(), size, out._c, _raw_stream(stream))
+    st = lib().ufp4_moe_sort(ids.data_ptr(), size, _struct(out, dev, "out"), s)
     _check(st, "ufp4_moe_sort")
     return out
 
@@ -628,11 +680,13 @@ def ufp4_moe_sort(ids, n_experts, out=None, stream=None):
 def ufp4_moe_dispatch(x, plan, out=None, stream=None):
     """x ([tokens, hidden]) in expert order: [tokens * topk, hidden], dropped
     slots' rows (the last ones) zero.  Gradient: ufp4_moe_combine(dxs, plan)."""
-    xp, dt, ld, _, hidden = _rows2d(x, "x", plan.tokens)
-    out, op, odt, old = _result(out, "out", plan.tokens * plan.topk, hidden, x.dtype, x.device)
+    dev = _place(x, "x")
+    pc, s = _struct(plan, dev), _raw_stream(stream, dev)
+    xp, dt, ld, _, hidden = _rows2d(x, "x", dev, plan.tokens)
+    out, op, odt, old = _result(out, "out", plan.tokens * plan.topk, hidden, x.dtype, dev)
     if odt != dt:
         raise TypeError("out must have x's dtype")
-    st = lib().ufp4_moe_dispatch(xp, dt, hidden, ld, plan._c, op, old, _raw_stream(stream))
+    st = lib().ufp4_moe_dispatch(xp, dt, hidden, ld, pc, op, old, s)
     _check(st, "ufp4_moe_dispatch")
     return out
 
@@ -641,10 +695,12 @@ def ufp4_moe_combine(y, plan, weights=None, dtype=None, out=None, stream=None):
     """y ([tokens * topk, hidden], expert order) back in token order: the sum
     over each token's routed slots, times weights ([tokens, topk] fp32) if
     given.  dtype: the result's (y's by default)."""
-    yp, dt, ld, _, hidden = _rows2d(y, "y", plan.tokens * plan.topk)
-    w = None if weights is None else _plan_weights(weights, plan)
-    out, op, odt, old = _result(out, "out", plan.tokens, hidden, dtype or y.dtype, y.device)
-    st = lib().ufp4_moe_combine(yp, dt, hidden, ld, plan._c, w, op, odt, old, _raw_stream(stream))
+    dev = _place(y, "y")
+    pc, s = _struct(plan, dev), _raw_stream(stream, dev)
+    yp, dt, ld, _, hidden = _rows2d(y, "y", dev, plan.tokens * plan.topk)
+    w = None if weights is None else _plan_weights(weights, plan, dev)
+    out, op, odt, old = _result(out, "out", plan.tokens, hidden, dtype or y.dtype, dev)
+    st = lib().ufp4_moe_combine(yp, dt, hidden, ld, pc, w, op, odt, old, s)
     _check(st, "ufp4_moe_combine")
     return out
 
@@ -652,14 +708,17 @@ def ufp4_moe_combine(y, plan, weights=None, dtype=None, out=None, stream=None):
 def ufp4_moe_combine_bwd(dout, y, plan, weights, dtype=None, dy=None, dw=None, stream=None):
     """Gradients of ufp4_moe_combine(y, plan, weights): (dy, dw).  dtype: dy's
     (dout's by default)."""
-    yp, ydt, yld, rows, hidden = _rows2d(y, "y", plan.tokens * plan.topk)
-    dp, ddt, dld, _, _ = _rows2d(dout, "dout", plan.tokens, hidden)
-    w = _plan_weights(weights, plan)
-    dy, gp, gdt, gld = _result(dy, "dy", rows, hidden, dtype or dout.dtype, y.device)
+    dev = _place(y, "y")
+    pc, s = _struct(plan, dev), _raw_stream(stream, dev)
+    yp, ydt, yld, rows, hidden = _rows2d(y, "y", dev, plan.tokens * plan.topk)
+    dp, ddt, dld, _, _ = _rows2d(dout, "dout", dev, plan.tokens, hidden)
+    w = _plan_weights(weights, plan, dev)
+    dwp = None if dw is None else _plan_weights(dw, plan, dev, "dw")
+    dy, gp, gdt, gld = _result(dy, "dy", rows, hidden, dtype or dout.dtype, dev)
     if dw is None:
-        dw = _empty((plan.tokens, plan.topk), _FLOAT32, y.device)
-    st = lib().ufp4_moe_combine_bwd(dp, ddt, dld, yp, ydt, yld, hidden, plan._c, w, gp, gdt, gld,
-                                    _plan_weights(dw, plan, "dw"), _raw_stream(stream))
+        dw = _empty((plan.tokens, plan.topk), _FLOAT32, dev)
+        dwp = dw.data_ptr()
+    st = lib().ufp4_moe_combine_bwd(dp, ddt, dld, yp, ydt, yld, hidden, pc, w, gp, gdt, gld, dwp, s)
     _check(st, "ufp4_moe_combine_bwd")
     return dy, dw
 
@@ -670,14 +729,15 @@ class Ckpt:
 
     def __init__(self, codes, scales, rows, cols, format):
         for t, name, width in ((codes, "codes", self._ld(cols)), (scales, "scales", self._blocks(cols))):
-            _cuda(t, name)
+            _on_gpu(t, name)
             if t.dtype != torch.uint8 or tuple(t.shape) != (rows, width) or not t.is_contiguous():
                 raise ValueError("%s must be contiguous uint8 [%d, %d]" % (name, rows, width))
-        self._codes, self._scales, self.device = codes, scales, codes.device
-        self._set(codes.data_ptr(), scales.data_ptr(), rows, cols, format)
+        _same_place(scales.get_device(), codes.get_device(), "scales")
+        self._codes, self._scales = codes, scales
+        self._set(codes.data_ptr(), scales.data_ptr(), rows, cols, format, codes.get_device())
 
-    def _set(self, codes, scales, rows, cols, format):
-        self.rows, self.cols, self.format = rows, cols, int(format)
+    def _set(self, codes, scales, rows, cols, format, dev):
+        self.rows, self.cols, self.format, self._dev = rows, cols, int(format), dev
         self._c = ctypes.byref(CkptC(codes, scales, rows, cols, self.format, 0))
 
     @staticmethod
@@ -690,25 +750,31 @@ class Ckpt:
 
     @classmethod
     def empty(cls, rows, cols, format, device="cuda"):
-        return cls._new(1, rows, cols, format, _device(device))[0]
+        device = _device(device)
+        with torch.cuda.device(device):
+            return cls._new(1, rows, cols, format, device.index)[0]
 
     @classmethod
-    def _new(cls, count, rows, cols, format, device):
+    def _new(cls, count, rows, cols, format, dev):
         """`count` checkpoints of one shape in one buffer; the views of their
         codes and scales are made when asked for."""
         n = rows * cls._ld(cols)
         step = (n + rows * cls._blocks(cols) + 15) // 16 * 16
-        buf = _empty((count * step,), torch.uint8, device)
+        buf = _empty((count * step,), torch.uint8, dev)
         at, made = buf.data_ptr(), []
         for k in range(count):
             c = cls.__new__(cls)
-            c._buf, c._at, c._codes, c._scales, c.device = buf, k * step, None, None, device
-            c._set(at + k * step, at + k * step + n, rows, cols, format)
+            c._buf, c._at, c._codes, c._scales = buf, k * step, None, None
+            c._set(at + k * step, at + k * step + n, rows, cols, format, dev)
             made.append(c)
         return made
 
     def _view(self, first, rows, width):
         return self._buf[self._at + first:self._at + first + rows * width].view(rows, width)
+
+    @property
+    def device(self):
+        return torch.device("cuda", self._dev)
 
     @property
     def codes(self):
@@ -729,20 +795,25 @@ class Ckpt:
 def ufp4_ckpt_save(x, format=UFP4_CKPT_INT8, out=None, stream=None):
     """x (2-D bf16 / fp32) in 8 bits with a power-of-two scale per 32
     elements of a row.  Returns a Ckpt."""
-    xp, dt, ld, rows, cols = _rows2d(x, "x")
+    dev = _place(x, "x")
+    xp, dt, ld, rows, cols = _rows2d(x, "x", dev)
+    s = _raw_stream(stream, dev)
     if out is None:
-        out = Ckpt._new(1, rows, cols, format, x.device)[0]
+        out = Ckpt._new(1, rows, cols, format, dev)[0]
     elif (out.rows, out.cols, out.format) != (rows, cols, format):
         raise ValueError("out is a checkpoint of another shape or format")
-    st = lib().ufp4_ckpt_save(xp, dt, ld, out._c, _raw_stream(stream))
+    st = lib().ufp4_ckpt_save(xp, dt, ld, _struct(out, dev, "out"), s)
     _check(st, "ufp4_ckpt_save")
     return out
 
 
 def ufp4_ckpt_load(c, dtype=torch.bfloat16, out=None, stream=None):
     """The values of a checkpoint (exact in bf16 and fp32)."""
-    out, op, odt, old = _result(out, "out", c.rows, c.cols, dtype, c.device)
-    st = lib().ufp4_ckpt_load(c._c, op, odt, old, _raw_stream(stream))
+    dev = c._dev
+    _here(dev, "c")
+    s = _raw_stream(stream, dev)
+    out, op, odt, old = _result(out, "out", c.rows, c.cols, dtype, dev)
+    st = lib().ufp4_ckpt_load(c._c, op, odt, old, s)
     _check(st, "ufp4_ckpt_load")
     return out
 
@@ -752,19 +823,20 @@ def ufp4_swiglu(gate, up, ckpt=None, dtype=None, out=None, keep=None, stream=Non
     backward pass (ckpt: their format, or None to keep nothing; keep: a pair
     of Ckpts to write instead of new ones).  Returns (h, keep_gate, keep_up),
     the latter two None if nothing is kept.  dtype: h's (gate's by default)."""
-    gp, dt, gld, rows, cols = _rows2d(gate, "gate")
-    up_p, udt, uld, _, _ = _rows2d(up, "up", rows, cols)
+    dev = _place(gate, "gate")
+    gp, dt, gld, rows, cols = _rows2d(gate, "gate", dev)
+    up_p, udt, uld, _, _ = _rows2d(up, "up", dev, rows, cols)
     if udt != dt:
         raise TypeError("gate and up must have one dtype")
-    device = gate.device
-    out, hp, hdt, hld = _result(out, "out", rows, cols, dtype or gate.dtype, device)
+    s = _raw_stream(stream, dev)
+    out, hp, hdt, hld = _result(out, "out", rows, cols, dtype or gate.dtype, dev)
     kg = ku = None
     if keep is not None:
         kg, ku = keep
     elif ckpt is not None:
-        kg, ku = Ckpt._new(2, rows, cols, ckpt, device)
-    st = lib().ufp4_swiglu(gp, gld, up_p, uld, dt, rows, cols, hp, hdt, hld, kg and kg._c, ku and ku._c,
-                           _raw_stream(stream))
+        kg, ku = Ckpt._new(2, rows, cols, ckpt, dev)
+    st = lib().ufp4_swiglu(gp, gld, up_p, uld, dt, rows, cols, hp, hdt, hld, kg and _struct(kg, dev, "keep"),
+                           ku and _struct(ku, dev, "keep"), s)
     _check(st, "ufp4_swiglu")
     return out, kg, ku
 
@@ -772,13 +844,14 @@ def ufp4_swiglu(gate, up, ckpt=None, dtype=None, out=None, keep=None, stream=Non
 def ufp4_swiglu_bwd(dh, keep_gate, keep_up, dtype=None, dgate=None, dup=None, stream=None):
     """Gradients of ufp4_swiglu from its checkpoints: (dgate, dup).  dtype:
     the gradients' (dh's by default)."""
+    dev = _place(dh, "dh")
+    kg, ku, s = _struct(keep_gate, dev, "keep_gate"), _struct(keep_up, dev, "keep_up"), _raw_stream(stream, dev)
     rows, cols = keep_gate.rows, keep_gate.cols
-    dp, ddt, dld, _, _ = _rows2d(dh, "dh", rows, cols)
-    device = dh.device
-    dgate, gp, gdt, gld = _result(dgate, "dgate", rows, cols, dtype or dh.dtype, device)
-    dup, up, udt, uld = _result(dup, "dup", rows, cols, dgate.dtype, device)
+    dp, ddt, dld, _, _ = _rows2d(dh, "dh", dev, rows, cols)
+    dgate, gp, gdt, gld = _result(dgate, "dgate", rows, cols, dtype or dh.dtype, dev)
+    dup, up, udt, uld = _result(dup, "dup", rows, cols, dgate.dtype, dev)
     if udt != gdt:
         raise TypeError("dgate and dup must have one dtype")
-    st = lib().ufp4_swiglu_bwd(dp, ddt, dld, keep_gate._c, keep_up._c, gp, gld, up, uld, gdt, _raw_stream(stream))
+    st = lib().ufp4_swiglu_bwd(dp, ddt, dld, kg, ku, gp, gld, up, uld, gdt, s)
     _check(st, "ufp4_swiglu_bwd")
     return dgate, dup

@@ -24,6 +24,9 @@
  *     never frees, and keeps no state between calls.
  *   - Work is enqueued on `stream` and returns without synchronising, except
  *     where a call is documented to synchronise (it returns host values).
+ *   - Kernels are launched on the calling thread's current device; every
+ *     tensor and the stream belong to it (the library cannot tell: the Python
+ *     binding checks it).
  *   - Argument errors are found on the host before anything is launched and
  *     return UFP4_ERR_INVALID (or UFP4_ERR_UNSUPPORTED for a valid request
  *     this library does not implement); a failed launch returns UFP4_ERR_CUDA.
