@@ -6,6 +6,12 @@ is no fallback: if libufp4.so is missing or a tensor is not on a CUDA device,
 the calls raise.  The library launches on the current device: tensors and
 streams of another one are refused (call under torch.cuda.device).
 
+Where a call takes stream=, the results that it makes belong to that stream,
+as if made under torch.cuda.stream(stream): work of another stream that uses
+them waits for it and, if they may be dropped before it ends, marks them
+(Tensor.record_stream).  The same holds the other way round for operands made
+on another stream.
+
 The functions carry the C names:
   ufp4_quantize(x, grid, ...) -> QTensor
   ufp4_dequantize(q, ...)     -> fp32 tensor
@@ -534,15 +540,23 @@ def _same_place(index, dev, name):
         raise ValueError("%s is on cuda:%d, the other operands are on cuda:%d" % (name, index, dev))
 
 
-def _raw_stream(stream, dev):
+def _streams(stream, dev):
+    """The handle of the stream to launch on, and that stream where it is not
+    the current one: results have to be made there, because the caching
+    allocator gives out a block in the order of one stream's work."""
     if stream is None:
-        return _current_raw_stream(dev)
+        return _current_raw_stream(dev), None
     _same_place(stream.device_index, dev, "stream")
-    return stream.cuda_stream
+    raw = stream.cuda_stream
+    return raw, None if raw == _current_raw_stream(dev) else stream
 
 
-def _empty(shape, dtype, dev):
-    """A fresh contiguous tensor (one or two dims) on the current device."""
+def _empty(shape, dtype, dev, on=None):
+    """A fresh contiguous tensor (one or two dims) on the current device, for
+    use on stream `on` (None: the current one)."""
+    if on is not None:
+        with torch.cuda.stream(on):
+            return _empty(shape, dtype, dev)
     if _empty_strided_cuda is not None:
         return _empty_strided_cuda(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
     return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
@@ -593,10 +607,10 @@ class MoePlan:
             return cls._new(tokens, topk, n_experts, device.index)
 
     @classmethod
-    def _new(cls, tokens, topk, n_experts, dev):
+    def _new(cls, tokens, topk, n_experts, dev, on=None):
         plan = cls.__new__(cls)
-        plan._set(_empty((tokens, topk), _INT32, dev), _empty((tokens * topk,), _INT32, dev),
-                  _empty((n_experts,), _INT64, dev), _empty((n_experts + 1,), _INT64, dev),
+        plan._set(_empty((tokens, topk), _INT32, dev, on), _empty((tokens * topk,), _INT32, dev, on),
+                  _empty((n_experts,), _INT64, dev, on), _empty((n_experts + 1,), _INT64, dev, on),
                   tokens, topk, n_experts, dev)
         return plan
 
@@ -629,14 +643,14 @@ def _rows2d(t, name, dev, rows=None, cols=None):
     return t.data_ptr(), _dtype_code(t) if dt is None else dt, ld, r, c
 
 
-def _result(out, name, rows, cols, dtype, dev):
+def _result(out, name, rows, cols, dtype, dev, on):
     """A fresh rows x cols result, or the caller's, checked: the tensor, its
     pointer, dtype code and row stride."""
     if out is None:
         dt = _DTYPES.get(dtype)
         if dt is None:
             raise TypeError("%s must be bf16 or fp32, got %s" % (name, dtype))
-        out = _empty((rows, cols), dtype, dev)
+        out = _empty((rows, cols), dtype, dev, on)
         return out, out.data_ptr(), dt, cols
     p, dt, ld, _, _ = _rows2d(out, name, dev, rows, cols)
     return out, p, dt, ld
@@ -667,9 +681,9 @@ def ufp4_moe_sort(ids, n_experts, out=None, stream=None):
     if not size:
         raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
     tokens, topk = ids.shape
-    s = _raw_stream(stream, dev)
+    s, on = _streams(stream, dev)
     if out is None:
-        out = MoePlan._new(tokens, topk, n_experts, dev)
+        out = MoePlan._new(tokens, topk, n_experts, dev, on)
     elif (out.tokens, out.topk, out.n_experts) != (tokens, topk, n_experts):
         raise ValueError("out is a plan of another size")
     st = lib().ufp4_moe_sort(ids.data_ptr(), size, _struct(out, dev, "out"), s)
@@ -681,9 +695,9 @@ def ufp4_moe_dispatch(x, plan, out=None, stream=None):
     """x ([tokens, hidden]) in expert order: [tokens * topk, hidden], dropped
     slots' rows (the last ones) zero.  Gradient: ufp4_moe_combine(dxs, plan)."""
     dev = _place(x, "x")
-    pc, s = _struct(plan, dev), _raw_stream(stream, dev)
+    pc, (s, on) = _struct(plan, dev), _streams(stream, dev)
     xp, dt, ld, _, hidden = _rows2d(x, "x", dev, plan.tokens)
-    out, op, odt, old = _result(out, "out", plan.tokens * plan.topk, hidden, x.dtype, dev)
+    out, op, odt, old = _result(out, "out", plan.tokens * plan.topk, hidden, x.dtype, dev, on)
     if odt != dt:
         raise TypeError("out must have x's dtype")
     st = lib().ufp4_moe_dispatch(xp, dt, hidden, ld, pc, op, old, s)
@@ -696,10 +710,10 @@ def ufp4_moe_combine(y, plan, weights=None, dtype=None, out=None, stream=None):
     over each token's routed slots, times weights ([tokens, topk] fp32) if
     given.  dtype: the result's (y's by default)."""
     dev = _place(y, "y")
-    pc, s = _struct(plan, dev), _raw_stream(stream, dev)
+    pc, (s, on) = _struct(plan, dev), _streams(stream, dev)
     yp, dt, ld, _, hidden = _rows2d(y, "y", dev, plan.tokens * plan.topk)
     w = None if weights is None else _plan_weights(weights, plan, dev)
-    out, op, odt, old = _result(out, "out", plan.tokens, hidden, dtype or y.dtype, dev)
+    out, op, odt, old = _result(out, "out", plan.tokens, hidden, dtype or y.dtype, dev, on)
     st = lib().ufp4_moe_combine(yp, dt, hidden, ld, pc, w, op, odt, old, s)
     _check(st, "ufp4_moe_combine")
     return out
@@ -709,14 +723,14 @@ def ufp4_moe_combine_bwd(dout, y, plan, weights, dtype=None, dy=None, dw=None, s
     """Gradients of ufp4_moe_combine(y, plan, weights): (dy, dw).  dtype: dy's
     (dout's by default)."""
     dev = _place(y, "y")
-    pc, s = _struct(plan, dev), _raw_stream(stream, dev)
+    pc, (s, on) = _struct(plan, dev), _streams(stream, dev)
     yp, ydt, yld, rows, hidden = _rows2d(y, "y", dev, plan.tokens * plan.topk)
     dp, ddt, dld, _, _ = _rows2d(dout, "dout", dev, plan.tokens, hidden)
     w = _plan_weights(weights, plan, dev)
     dwp = None if dw is None else _plan_weights(dw, plan, dev, "dw")
-    dy, gp, gdt, gld = _result(dy, "dy", rows, hidden, dtype or dout.dtype, dev)
+    dy, gp, gdt, gld = _result(dy, "dy", rows, hidden, dtype or dout.dtype, dev, on)
     if dw is None:
-        dw = _empty((plan.tokens, plan.topk), _FLOAT32, dev)
+        dw = _empty((plan.tokens, plan.topk), _FLOAT32, dev, on)
         dwp = dw.data_ptr()
     st = lib().ufp4_moe_combine_bwd(dp, ddt, dld, yp, ydt, yld, hidden, pc, w, gp, gdt, gld, dwp, s)
     _check(st, "ufp4_moe_combine_bwd")
@@ -755,12 +769,12 @@ class Ckpt:
             return cls._new(1, rows, cols, format, device.index)[0]
 
     @classmethod
-    def _new(cls, count, rows, cols, format, dev):
+    def _new(cls, count, rows, cols, format, dev, on=None):
         """`count` checkpoints of one shape in one buffer; the views of their
         codes and scales are made when asked for."""
         n = rows * cls._ld(cols)
         step = (n + rows * cls._blocks(cols) + 15) // 16 * 16
-        buf = _empty((count * step,), torch.uint8, dev)
+        buf = _empty((count * step,), torch.uint8, dev, on)
         at, made = buf.data_ptr(), []
         for k in range(count):
             c = cls.__new__(cls)
@@ -797,9 +811,9 @@ def ufp4_ckpt_save(x, format=UFP4_CKPT_INT8, out=None, stream=None):
     elements of a row.  Returns a Ckpt."""
     dev = _place(x, "x")
     xp, dt, ld, rows, cols = _rows2d(x, "x", dev)
-    s = _raw_stream(stream, dev)
+    s, on = _streams(stream, dev)
     if out is None:
-        out = Ckpt._new(1, rows, cols, format, dev)[0]
+        out = Ckpt._new(1, rows, cols, format, dev, on)[0]
     elif (out.rows, out.cols, out.format) != (rows, cols, format):
         raise ValueError("out is a checkpoint of another shape or format")
     st = lib().ufp4_ckpt_save(xp, dt, ld, _struct(out, dev, "out"), s)
@@ -811,8 +825,8 @@ def ufp4_ckpt_load(c, dtype=torch.bfloat16, out=None, stream=None):
     """The values of a checkpoint (exact in bf16 and fp32)."""
     dev = c._dev
     _here(dev, "c")
-    s = _raw_stream(stream, dev)
-    out, op, odt, old = _result(out, "out", c.rows, c.cols, dtype, dev)
+    s, on = _streams(stream, dev)
+    out, op, odt, old = _result(out, "out", c.rows, c.cols, dtype, dev, on)
     st = lib().ufp4_ckpt_load(c._c, op, odt, old, s)
     _check(st, "ufp4_ckpt_load")
     return out
@@ -828,13 +842,13 @@ def ufp4_swiglu(gate, up, ckpt=None, dtype=None, out=None, keep=None, stream=Non
     up_p, udt, uld, _, _ = _rows2d(up, "up", dev, rows, cols)
     if udt != dt:
         raise TypeError("gate and up must have one dtype")
-    s = _raw_stream(stream, dev)
-    out, hp, hdt, hld = _result(out, "out", rows, cols, dtype or gate.dtype, dev)
+    s, on = _streams(stream, dev)
+    out, hp, hdt, hld = _result(out, "out", rows, cols, dtype or gate.dtype, dev, on)
     kg = ku = None
     if keep is not None:
         kg, ku = keep
     elif ckpt is not None:
-        kg, ku = Ckpt._new(2, rows, cols, ckpt, dev)
+        kg, ku = Ckpt._new(2, rows, cols, ckpt, dev, on)
     st = lib().ufp4_swiglu(gp, gld, up_p, uld, dt, rows, cols, hp, hdt, hld, kg and _struct(kg, dev, "keep"),
                            ku and _struct(ku, dev, "keep"), s)
     _check(st, "ufp4_swiglu")
@@ -845,11 +859,12 @@ def ufp4_swiglu_bwd(dh, keep_gate, keep_up, dtype=None, dgate=None, dup=None, st
     """Gradients of ufp4_swiglu from its checkpoints: (dgate, dup).  dtype:
     the gradients' (dh's by default)."""
     dev = _place(dh, "dh")
-    kg, ku, s = _struct(keep_gate, dev, "keep_gate"), _struct(keep_up, dev, "keep_up"), _raw_stream(stream, dev)
+    kg, ku = _struct(keep_gate, dev, "keep_gate"), _struct(keep_up, dev, "keep_up")
+    s, on = _streams(stream, dev)
     rows, cols = keep_gate.rows, keep_gate.cols
     dp, ddt, dld, _, _ = _rows2d(dh, "dh", dev, rows, cols)
-    dgate, gp, gdt, gld = _result(dgate, "dgate", rows, cols, dtype or dh.dtype, dev)
-    dup, up, udt, uld = _result(dup, "dup", rows, cols, dgate.dtype, dev)
+    dgate, gp, gdt, gld = _result(dgate, "dgate", rows, cols, dtype or dh.dtype, dev, on)
+    dup, up, udt, uld = _result(dup, "dup", rows, cols, dgate.dtype, dev, on)
     if udt != gdt:
         raise TypeError("dgate and dup must have one dtype")
     st = lib().ufp4_swiglu_bwd(dp, ddt, dld, kg, ku, gp, gld, up, uld, gdt, s)

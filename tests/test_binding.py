@@ -54,7 +54,7 @@ class Machine:
             yield
             self.stream = before
 
-        patch.setattr(U, "_empty_strided_cuda", None)
+        patch.setattr(U, "_empty_strided_cuda", lambda shape, strides, dtype: empty(shape, dtype=dtype))
         patch.setattr(U, "_current_device", lambda: self.current)
         patch.setattr(U, "_current_raw_stream", lambda dev: 100)
         patch.setattr(U, "lib", lambda: self)
@@ -139,6 +139,17 @@ def test_streams_of_another_device_are_refused(machine, name):
     assert not machine.calls
     getattr(U, name)(**given, stream=Stream(0, 300))
     assert machine.calls == [(name, 300)]
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("stream,where", [(None, 100), (Stream(0, 100), 100), (Stream(0, 300), 300)])
+def test_results_are_made_on_the_stream_of_the_call(machine, name, stream, where):
+    given = {k: m(On0) for k, m in CALLS[name].items() if k not in OUTPUTS}
+    if name == "ufp4_swiglu":
+        given["ckpt"] = 0
+    getattr(U, name)(**given, stream=stream)
+    assert machine.calls == [(name, where)] and machine.made
+    assert {s for _, s in machine.made} == {where}
 
 
 def test_a_plan_or_checkpoint_is_on_one_device(machine):
