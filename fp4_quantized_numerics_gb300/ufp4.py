@@ -22,6 +22,7 @@ The functions carry the C names:
   ufp4_ckpt_save(x, fmt) -> Ckpt;  ufp4_ckpt_load(c) -> tensor
   ufp4_swiglu(gate, up, ...)  -> (h, Ckpt, Ckpt);  ufp4_swiglu_bwd(dh, ...) -> (dgate, dup)
 """
+import contextlib
 import ctypes
 import os
 
@@ -196,6 +197,14 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _for(stream):
+    """Allocations for `stream` (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    _here(stream.device_index, "stream")
+    return torch.cuda.stream(stream)
+
+
 def _on_gpu(t, name):
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise TypeError("%s must be a CUDA tensor (libufp4 has no CPU path)" % name)
@@ -215,7 +224,8 @@ _workspaces = {}
 
 
 def workspace(device=None):
-    """A per-device scratch buffer of ufp4_workspace_bytes() (allocated once)."""
+    """A per-device scratch buffer of ufp4_workspace_bytes() (allocated once);
+    calls that may run at the same time on several streams need their own (ws=)."""
     dev = torch.device("cuda") if device is None else torch.device(device)
     if dev.index is None:
         dev = torch.device(dev.type, torch.cuda.current_device())
@@ -225,6 +235,11 @@ def workspace(device=None):
         ws = torch.empty(int(lib().ufp4_workspace_bytes()), dtype=torch.uint8, device=dev)
         _workspaces[key] = ws
     return ws
+
+
+def _workspace_for(stream, device):
+    with _for(stream):
+        return workspace(device)
 
 
 class QTensor:
@@ -290,9 +305,10 @@ def ufp4_quantize(x, grid, rht=False, rht_seed=0, round=UFP4_RTNE, sr_seed=0, sr
     rows, cols = x.shape
     out_rows, k = (cols, rows) if colwise else (rows, cols)
     if out is None:
-        out = QTensor.empty(out_rows, k, grid, x.device)
+        with _for(stream):
+            out = QTensor.empty(out_rows, k, grid, x.device)
     if ws is None:
-        ws = workspace(x.device)
+        ws = _workspace_for(stream, x.device)
     p = qparams(grid, rht, rht_seed, round, sr_seed, sr_counter, colwise, amax_in)
     qc = out.c()
     st = lib().ufp4_quantize(x.data_ptr(), _dtype_code(x), rows, cols, x.stride(0), ctypes.byref(p),
@@ -310,12 +326,13 @@ def ufp4_quantize_dual(x, grid, rht=False, rht_seed=0, round=UFP4_RTNE, sr_seed=
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be 2-D with unit stride in its last dim")
     rows, cols = x.shape
-    if out_row is None:
-        out_row = QTensor.empty(rows, cols, grid, x.device)
-    if out_col is None:
-        out_col = QTensor.empty(cols, rows, grid, x.device)
+    with _for(stream):
+        if out_row is None:
+            out_row = QTensor.empty(rows, cols, grid, x.device)
+        if out_col is None:
+            out_col = QTensor.empty(cols, rows, grid, x.device)
     if ws is None:
-        ws = workspace(x.device)
+        ws = _workspace_for(stream, x.device)
     pr = qparams(grid, rht, rht_seed, round, sr_seed, sr_counter_row, False, amax_row)
     pc = qparams(grid, rht, rht_seed, round, sr_seed, sr_counter_col, True, amax_col)
     qr, qc = out_row.c(), out_col.c()
@@ -333,7 +350,8 @@ def ufp4_check(ws=None, stream=None):
 def ufp4_dequantize(q, inverse_rht=False, rht_seed=0, out=None, stream=None):
     _cuda(q.codes, "q.codes")
     if out is None:
-        out = torch.empty(q.rows, q.k, dtype=torch.float32, device=q.codes.device)
+        with _for(stream):
+            out = torch.empty(q.rows, q.k, dtype=torch.float32, device=q.codes.device)
     qc = q.c()
     st = lib().ufp4_dequantize(ctypes.byref(qc), int(bool(inverse_rht)), int(rht_seed),
                                out.data_ptr(), out.stride(0), _stream(stream))
@@ -347,7 +365,8 @@ def ufp4_gemm(a, b, out=None, stream=None):
     _cuda(b.codes, "b.codes")
     if out is None:   # row stride rounded up to 4 floats (16 bytes), as the ABI requires
         ld = (b.rows + 3) // 4 * 4
-        out = torch.empty(a.rows, ld, dtype=torch.float32, device=a.codes.device)[:, : b.rows]
+        with _for(stream):
+            out = torch.empty(a.rows, ld, dtype=torch.float32, device=a.codes.device)[:, : b.rows]
     ac, bc = a.c(), b.c()
     st = lib().ufp4_gemm(ctypes.byref(ac), ctypes.byref(bc), out.data_ptr(), out.stride(0),
                          _stream(stream))
@@ -361,11 +380,12 @@ def ufp4_gemm_amax(a, b, rht=False, rht_seed=0, out=None, amax=None, stream=None
     Returns (C, amax); pass amax as the amax_in of ufp4_quantize(C, ...)."""
     _cuda(a.codes, "a.codes")
     _cuda(b.codes, "b.codes")
-    if out is None:
-        ld = (b.rows + 3) // 4 * 4
-        out = torch.empty(a.rows, ld, dtype=torch.float32, device=a.codes.device)[:, : b.rows]
-    if amax is None:
-        amax = torch.empty(1, dtype=torch.float32, device=a.codes.device)
+    with _for(stream):
+        if out is None:
+            ld = (b.rows + 3) // 4 * 4
+            out = torch.empty(a.rows, ld, dtype=torch.float32, device=a.codes.device)[:, : b.rows]
+        if amax is None:
+            amax = torch.empty(1, dtype=torch.float32, device=a.codes.device)
     ac, bc = a.c(), b.c()
     st = lib().ufp4_gemm_amax(ctypes.byref(ac), ctypes.byref(bc), out.data_ptr(), out.stride(0),
                               int(bool(rht)), int(rht_seed) & (2**64 - 1), amax.data_ptr(), _stream(stream))
@@ -383,9 +403,10 @@ def ufp4_quantize_stats(x, grid, rht=False, rht_seed=0, round=UFP4_RTNE, sr_seed
     rows, cols = x.shape
     out_rows, k = (cols, rows) if colwise else (rows, cols)
     if out is None:
-        out = QTensor.empty(out_rows, k, grid, x.device)
+        with _for(stream):
+            out = QTensor.empty(out_rows, k, grid, x.device)
     if ws is None:
-        ws = workspace(x.device)
+        ws = _workspace_for(stream, x.device)
     p = qparams(grid, rht, rht_seed, round, sr_seed, sr_counter, colwise, amax_in)
     qc = out.c()
     res = StatsC()
@@ -402,7 +423,7 @@ def ufp4_stats(x, q, rht=False, rht_seed=0, round=UFP4_RTNE, sr_seed=0, sr_count
     _cuda(x, "x")
     rows, cols = x.shape
     if ws is None:
-        ws = workspace(x.device)
+        ws = _workspace_for(stream, x.device)
     p = qparams(q.grid, rht, rht_seed, round, sr_seed, sr_counter, colwise, amax_in)
     qc = q.c()
     out = StatsC()
@@ -450,10 +471,11 @@ def ufp4_quantize_grouped(x, grid, seg_rows, rht=False, rht_seed=0, round=UFP4_R
     else:
         rows, k = grouped_rows(seg_rows), cols
     if out is None:
-        out = QTensor.empty(rows, k, grid, x.device)
-        out.tensor_scale = torch.empty(max(n, 1), dtype=torch.float32, device=x.device)
+        with _for(stream):
+            out = QTensor.empty(rows, k, grid, x.device)
+            out.tensor_scale = torch.empty(max(n, 1), dtype=torch.float32, device=x.device)
     if ws is None:
-        ws = workspace(x.device)
+        ws = _workspace_for(stream, x.device)
     p = qparams(grid, rht, rht_seed, round, sr_seed, sr_counter, colwise)
     qc = out.c()
     st = lib().ufp4_quantize_grouped(x.data_ptr(), _dtype_code(x), cols, x.stride(0),
@@ -472,14 +494,15 @@ def ufp4_quantize_grouped_dual(x, grid, seg_rows, rht=False, rht_seed=0, round=U
     _cuda(x, "x")
     cols = x.shape[1]
     n = len(seg_rows)
-    if out_row is None:
-        out_row = QTensor.empty(grouped_rows(seg_rows), cols, grid, x.device)
-        out_row.tensor_scale = torch.empty(max(n, 1), dtype=torch.float32, device=x.device)
-    if out_col is None:
-        out_col = QTensor.empty(cols, grouped_kpad(seg_rows), grid, x.device)
-        out_col.tensor_scale = torch.empty(max(n, 1), dtype=torch.float32, device=x.device)
+    with _for(stream):
+        if out_row is None:
+            out_row = QTensor.empty(grouped_rows(seg_rows), cols, grid, x.device)
+            out_row.tensor_scale = torch.empty(max(n, 1), dtype=torch.float32, device=x.device)
+        if out_col is None:
+            out_col = QTensor.empty(cols, grouped_kpad(seg_rows), grid, x.device)
+            out_col.tensor_scale = torch.empty(max(n, 1), dtype=torch.float32, device=x.device)
     if ws is None:
-        ws = workspace(x.device)
+        ws = _workspace_for(stream, x.device)
     pr = qparams(grid, rht, rht_seed, round, sr_seed, sr_counter_row, False)
     pc = qparams(grid, rht, rht_seed, round, sr_seed, sr_counter_col, True)
     qr, qc = out_row.c(), out_col.c()

@@ -63,8 +63,9 @@ class Machine:
         patch.setattr(torch.cuda, "current_stream", lambda *a: Stream(self.current, 100))
 
     def __getattr__(self, name):
-        if name in ("ufp4_codes_bytes", "ufp4_scales_bytes"):
-            return lambda rows, k: 64
+        if name in ("ufp4_codes_bytes", "ufp4_scales_bytes", "ufp4_grouped_rows", "ufp4_grouped_kpad",
+                    "ufp4_workspace_bytes"):
+            return lambda *args: 64
         if not name.startswith("ufp4_"):
             raise AttributeError(name)
 
@@ -174,6 +175,10 @@ OLDER = {
     "ufp4_quantize_stats": (lambda k, s: U.ufp4_quantize_stats(_t(k, 4, 32), U.UFP4_E2M1, ws=_t(k, 8), stream=s)),
     "ufp4_stats": (lambda k, s: U.ufp4_stats(_t(k, 4, 32), _q(k), ws=_t(k, 8), stream=s)),
     "ufp4_gemm_grouped": (lambda k, s: U.ufp4_gemm_grouped(_q(k), _q(k), [], stream=s)),
+    "ufp4_quantize_grouped": (lambda k, s: U.ufp4_quantize_grouped(_t(k, 4, 32), U.UFP4_E1M2, [4], ws=_t(k, 8),
+                                                                   stream=s)),
+    "ufp4_quantize_grouped_dual": (lambda k, s: U.ufp4_quantize_grouped_dual(_t(k, 4, 32), U.UFP4_E1M2, [4],
+                                                                             ws=_t(k, 8), stream=s)),
 }
 
 
@@ -186,3 +191,18 @@ def test_quantizer_and_gemm_calls_of_another_device_are_refused(machine, name):
     assert not machine.calls
     OLDER[name](On0, Stream(0, 300))
     assert machine.calls == [(name, 300)]
+
+
+@pytest.mark.parametrize("name", OLDER)
+@pytest.mark.parametrize("stream,where", [(None, 100), (Stream(0, 300), 300)])
+def test_quantizer_and_gemm_results_are_made_on_the_stream_of_the_call(machine, name, stream, where):
+    OLDER[name](On0, stream)
+    assert machine.calls[-1] == (name, where)
+    assert machine.made or name in ("ufp4_stats", "ufp4_gemm_grouped")
+    assert {s for _, s in machine.made} <= {where}
+
+
+def test_the_workspace_is_made_on_the_stream_of_the_first_call(machine, monkeypatch):
+    monkeypatch.setattr(U, "_workspaces", {})
+    U.ufp4_quantize(_t(On0, 4, 32), U.UFP4_E2M1, stream=Stream(0, 300))
+    assert ((64,), 300) in machine.made and {s for _, s in machine.made} == {300}

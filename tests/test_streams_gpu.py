@@ -23,6 +23,8 @@ def _calls(U):
     ids = torch.randint(0, 8, (ROWS, 1), device="cuda")
     plan, w = U.ufp4_moe_sort(ids, 8), torch.ones(ROWS, 1, device="cuda")
     h, kg, ku = U.ufp4_swiglu(x, x, ckpt=U.UFP4_CKPT_INT8)
+    a = torch.randn(1024, 1024, device="cuda", dtype=torch.bfloat16)
+    q = U.ufp4_quantize(a, U.UFP4_E1M2)
     many = torch.randint(0, 8, (ROWS * COLS, 1), device="cuda")
     return {
         "moe_sort": lambda s: U.ufp4_moe_sort(many, 8, stream=s).pos,
@@ -32,12 +34,17 @@ def _calls(U):
         "ckpt_save": lambda s: U.ufp4_ckpt_save(x, stream=s).codes[:, :COLS],   # (rows' padding is not written)
         "ckpt_load": lambda s: U.ufp4_ckpt_load(kg, stream=s),
         "swiglu": lambda s: U.ufp4_swiglu(x, x, stream=s)[0],
+        "quantize": lambda s: U.ufp4_quantize(a, U.UFP4_E1M2, stream=s).codes,
+        "quantize_dual": lambda s: U.ufp4_quantize_dual(a, U.UFP4_E1M2, stream=s)[1].codes,
+        "quantize_grouped": lambda s: U.ufp4_quantize_grouped(a, U.UFP4_E1M2, [512, 512], stream=s).codes,
+        "dequantize": lambda s: U.ufp4_dequantize(q, stream=s),
+        "gemm": lambda s: U.ufp4_gemm(q, q, stream=s),
         "swiglu_bwd": lambda s: U.ufp4_swiglu_bwd(x, kg, ku, stream=s)[0],
     }
 
 
 NAMES = ["moe_sort", "moe_dispatch", "moe_combine", "moe_combine_bwd", "ckpt_save", "ckpt_load", "swiglu",
-         "swiglu_bwd"]
+         "swiglu_bwd", "quantize", "quantize_dual", "quantize_grouped", "dequantize", "gemm"]
 
 
 @pytest.mark.parametrize("name", NAMES)
