@@ -666,16 +666,20 @@ def _rows2d(t, name, dev, rows=None, cols=None):
     return t.data_ptr(), _dtype_code(t) if dt is None else dt, ld, r, c
 
 
-def _result(out, name, rows, cols, dtype, dev, on):
-    """A fresh rows x cols result, or the caller's, checked: the tensor, its
-    pointer, dtype code and row stride."""
+def _result(out, name, rows, cols, dtype, default, dev, on):
+    """A fresh rows x cols result (of `dtype`, or of the default's where that
+    is None), or the caller's, checked: the tensor, its pointer, dtype code and
+    row stride."""
     if out is None:
+        dtype = dtype or default
         dt = _DTYPES.get(dtype)
         if dt is None:
             raise TypeError("%s must be bf16 or fp32, got %s" % (name, dtype))
         out = _empty((rows, cols), dtype, dev, on)
         return out, out.data_ptr(), dt, cols
     p, dt, ld, _, _ = _rows2d(out, name, dev, rows, cols)
+    if dtype is not None and out.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, out.dtype))
     return out, p, dt, ld
 
 
@@ -720,9 +724,7 @@ def ufp4_moe_dispatch(x, plan, out=None, stream=None):
     dev = _place(x, "x")
     pc, (s, on) = _struct(plan, dev), _streams(stream, dev)
     xp, dt, ld, _, hidden = _rows2d(x, "x", dev, plan.tokens)
-    out, op, odt, old = _result(out, "out", plan.tokens * plan.topk, hidden, x.dtype, dev, on)
-    if odt != dt:
-        raise TypeError("out must have x's dtype")
+    out, op, _, old = _result(out, "out", plan.tokens * plan.topk, hidden, x.dtype, None, dev, on)
     st = lib().ufp4_moe_dispatch(xp, dt, hidden, ld, pc, op, old, s)
     _check(st, "ufp4_moe_dispatch")
     return out
@@ -736,7 +738,7 @@ def ufp4_moe_combine(y, plan, weights=None, dtype=None, out=None, stream=None):
     pc, (s, on) = _struct(plan, dev), _streams(stream, dev)
     yp, dt, ld, _, hidden = _rows2d(y, "y", dev, plan.tokens * plan.topk)
     w = None if weights is None else _plan_weights(weights, plan, dev)
-    out, op, odt, old = _result(out, "out", plan.tokens, hidden, dtype or y.dtype, dev, on)
+    out, op, odt, old = _result(out, "out", plan.tokens, hidden, dtype, y.dtype, dev, on)
     st = lib().ufp4_moe_combine(yp, dt, hidden, ld, pc, w, op, odt, old, s)
     _check(st, "ufp4_moe_combine")
     return out
@@ -751,7 +753,7 @@ def ufp4_moe_combine_bwd(dout, y, plan, weights, dtype=None, dy=None, dw=None, s
     dp, ddt, dld, _, _ = _rows2d(dout, "dout", dev, plan.tokens, hidden)
     w = _plan_weights(weights, plan, dev)
     dwp = None if dw is None else _plan_weights(dw, plan, dev, "dw")
-    dy, gp, gdt, gld = _result(dy, "dy", rows, hidden, dtype or dout.dtype, dev, on)
+    dy, gp, gdt, gld = _result(dy, "dy", rows, hidden, dtype, dout.dtype, dev, on)
     if dw is None:
         dw = _empty((plan.tokens, plan.topk), _FLOAT32, dev, on)
         dwp = dw.data_ptr()
@@ -844,12 +846,13 @@ def ufp4_ckpt_save(x, format=UFP4_CKPT_INT8, out=None, stream=None):
     return out
 
 
-def ufp4_ckpt_load(c, dtype=torch.bfloat16, out=None, stream=None):
-    """The values of a checkpoint (exact in bf16 and fp32)."""
+def ufp4_ckpt_load(c, dtype=None, out=None, stream=None):
+    """The values of a checkpoint (exact in bf16 and fp32).  dtype: the
+    result's (bf16 by default)."""
     dev = c._dev
     _here(dev, "c")
     s, on = _streams(stream, dev)
-    out, op, odt, old = _result(out, "out", c.rows, c.cols, dtype, dev, on)
+    out, op, odt, old = _result(out, "out", c.rows, c.cols, dtype, torch.bfloat16, dev, on)
     st = lib().ufp4_ckpt_load(c._c, op, odt, old, s)
     _check(st, "ufp4_ckpt_load")
     return out
@@ -858,20 +861,24 @@ def ufp4_ckpt_load(c, dtype=torch.bfloat16, out=None, stream=None):
 def ufp4_swiglu(gate, up, ckpt=None, dtype=None, out=None, keep=None, stream=None):
     """h = silu(gate) * up, and gate's and up's 8-bit checkpoints for the
     backward pass (ckpt: their format, or None to keep nothing; keep: a pair
-    of Ckpts to write instead of new ones).  Returns (h, keep_gate, keep_up),
-    the latter two None if nothing is kept.  dtype: h's (gate's by default)."""
+    of Ckpts to write instead of new ones, of that format if it is given).
+    Returns (h, keep_gate, keep_up), the latter two None if nothing is kept.
+    dtype: h's (gate's by default).  New checkpoints share one buffer, which
+    is held until both are dropped."""
     dev = _place(gate, "gate")
     gp, dt, gld, rows, cols = _rows2d(gate, "gate", dev)
     up_p, udt, uld, _, _ = _rows2d(up, "up", dev, rows, cols)
     if udt != dt:
         raise TypeError("gate and up must have one dtype")
     s, on = _streams(stream, dev)
-    out, hp, hdt, hld = _result(out, "out", rows, cols, dtype or gate.dtype, dev, on)
     kg = ku = None
     if keep is not None:
         kg, ku = keep
+        if ckpt is not None and not (kg and ku and kg.format == ku.format == ckpt):
+            raise ValueError("keep must be two checkpoints of the format ckpt=%s" % ckpt)
     elif ckpt is not None:
         kg, ku = Ckpt._new(2, rows, cols, ckpt, dev, on)
+    out, hp, hdt, hld = _result(out, "out", rows, cols, dtype, gate.dtype, dev, on)
     st = lib().ufp4_swiglu(gp, gld, up_p, uld, dt, rows, cols, hp, hdt, hld, kg and _struct(kg, dev, "keep"),
                            ku and _struct(ku, dev, "keep"), s)
     _check(st, "ufp4_swiglu")
@@ -886,10 +893,8 @@ def ufp4_swiglu_bwd(dh, keep_gate, keep_up, dtype=None, dgate=None, dup=None, st
     s, on = _streams(stream, dev)
     rows, cols = keep_gate.rows, keep_gate.cols
     dp, ddt, dld, _, _ = _rows2d(dh, "dh", dev, rows, cols)
-    dgate, gp, gdt, gld = _result(dgate, "dgate", rows, cols, dtype or dh.dtype, dev, on)
-    dup, up, udt, uld = _result(dup, "dup", rows, cols, dgate.dtype, dev, on)
-    if udt != gdt:
-        raise TypeError("dgate and dup must have one dtype")
+    dgate, gp, gdt, gld = _result(dgate, "dgate", rows, cols, dtype, dh.dtype, dev, on)
+    dup, up, udt, uld = _result(dup, "dup", rows, cols, dgate.dtype, None, dev, on)
     st = lib().ufp4_swiglu_bwd(dp, ddt, dld, kg, ku, gp, gld, up, uld, gdt, s)
     _check(st, "ufp4_swiglu_bwd")
     return dgate, dup

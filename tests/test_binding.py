@@ -206,3 +206,40 @@ def test_the_workspace_is_made_on_the_stream_of_the_first_call(machine, monkeypa
     monkeypatch.setattr(U, "_workspaces", {})
     U.ufp4_quantize(_t(On0, 4, 32), U.UFP4_E2M1, stream=Stream(0, 300))
     assert ((64,), 300) in machine.made and {s for _, s in machine.made} == {300}
+
+
+# ----------------------------------------------------- arguments that disagree
+DTYPED = {"ufp4_moe_combine": ["out"], "ufp4_moe_combine_bwd": ["dy"], "ufp4_ckpt_load": ["out"],
+          "ufp4_swiglu": ["out"], "ufp4_swiglu_bwd": ["dgate", "dup"]}
+
+
+@pytest.mark.parametrize("name,result", [(n, r) for n, results in DTYPED.items() for r in results])
+def test_a_dtype_that_a_given_result_does_not_have_is_refused(machine, name, result):
+    given = {k: m(On0) for k, m in CALLS[name].items() if k not in OUTPUTS or k == result}
+    with pytest.raises(TypeError):
+        getattr(U, name)(**given, dtype=BF)
+    assert not machine.calls
+    getattr(U, name)(**given, dtype=FP)
+    getattr(U, name)(**given)
+    assert len(machine.calls) == 2
+
+
+def test_results_of_another_dtype_than_each_other_are_refused(machine):
+    with pytest.raises(TypeError):
+        U.ufp4_moe_dispatch(_t(On0, 4, 32), _plan(On0), out=_t(On0, 8, 32, dtype=BF))
+    with pytest.raises(TypeError):
+        U.ufp4_swiglu_bwd(_t(On0, 4, 32), _ckpt(On0), _ckpt(On0), dgate=_t(On0, 4, 32),
+                          dup=_t(On0, 4, 32, dtype=BF))
+    assert not machine.calls
+
+
+def test_a_format_that_the_kept_checkpoints_do_not_have_is_refused(machine):
+    x = _t(On0, 4, 32)
+    for keep in ((_ckpt(On0, 0), _ckpt(On0, 0)), (_ckpt(On0, 1), _ckpt(On0, 0)), (None, None)):
+        with pytest.raises(ValueError):
+            U.ufp4_swiglu(x, x, ckpt=U.UFP4_CKPT_E4M3, keep=keep)
+    assert not machine.calls and not machine.made
+    pair = _ckpt(On0, 1), _ckpt(On0, 1)
+    assert U.ufp4_swiglu(x, x, ckpt=U.UFP4_CKPT_E4M3, keep=pair)[1] is pair[0]
+    assert U.ufp4_swiglu(x, x, keep=pair)[2] is pair[1]
+    assert U.ufp4_ckpt_load(pair[0]).dtype is BF
