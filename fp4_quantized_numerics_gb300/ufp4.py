@@ -577,12 +577,18 @@ def _streams(stream, dev):
 def _empty(shape, dtype, dev, on=None):
     """A fresh contiguous tensor (one or two dims) on the current device, for
     use on stream `on` (None: the current one)."""
+    global _empty_strided_cuda
     if on is not None:
         with torch.cuda.stream(on):
             return _empty(shape, dtype, dev)
     if _empty_strided_cuda is not None:
-        return _empty_strided_cuda(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
-    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+        try:
+            return _empty_strided_cuda(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
+        except TypeError:
+            pass
+    out = torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    _empty_strided_cuda = None   # (not there, or of a torch where it takes other arguments)
+    return out
 
 
 def _device(device):

@@ -243,3 +243,18 @@ def test_a_format_that_the_kept_checkpoints_do_not_have_is_refused(machine):
     assert U.ufp4_swiglu(x, x, ckpt=U.UFP4_CKPT_E4M3, keep=pair)[1] is pair[0]
     assert U.ufp4_swiglu(x, x, keep=pair)[2] is pair[1]
     assert U.ufp4_ckpt_load(pair[0]).dtype is BF
+
+
+def test_results_are_made_by_the_public_call_where_the_short_one_is_another(machine, monkeypatch):
+    def takes_other_arguments(*args):
+        raise TypeError("3 arguments given")
+    monkeypatch.setattr(U, "_empty_strided_cuda", takes_other_arguments)
+    for _ in range(2):
+        assert U.ufp4_moe_dispatch(_t(On0, 4, 32), _plan(On0)).shape == (8, 32)
+    assert U._empty_strided_cuda is None and len(machine.made) == 2
+
+
+def test_a_wrong_size_leaves_the_short_call_in_use(machine):
+    with pytest.raises(TypeError):
+        U.ufp4_moe_sort(_t(On0, 4, 2, dtype=torch.int64), "three")
+    assert U._empty_strided_cuda is not None
