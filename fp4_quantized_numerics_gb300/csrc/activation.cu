@@ -12,13 +12,13 @@
 // Bound by memory: at most 3 instructions a byte moved.  One GB300, "of
 // measured" is of the 6676 GB/s of a plain copy:
 //   98304 x 1408, fp32 in, BF16 out, INT8 kept:
-//     k_swiglu 232 us, 7.2 TB/s (108 %; reads run faster than a copy), without
+//     k_swiglu 233 us, 7.2 TB/s (107 %; reads run faster than a copy), without
 //     checkpoints 190 us; k_swiglu_bwd 197 us (106 %);
 //   65536 x 8192 BF16: k_ckpt_save 243 us (INT8; E4M3 228; 100 and 107 %),
 //     k_ckpt_load 229 us (106 %).
-// With 8 elements a thread and 16-byte accesses these were 232, 241, 462 and
-// 372 us: too few bytes in flight, and the scale's arithmetic shared by half
-// as many elements.
+// With 8 elements a thread k_ckpt_save takes 321 us (E4M3 301) and k_ckpt_load
+// 277: too few bytes in flight, and the scale's arithmetic shared by half as
+// many elements.  The activation's kernels, which hold more, take the same.
 //
 // In the whole layout (rowops.cuh) a thread owns 16 consecutive elements (8
 // where rows allow no more) and two (four) neighbouring lanes one 32-element
@@ -26,8 +26,10 @@
 // block, in singles the warp.  Those two are bound by instructions (72 % of
 // the issue slots in k_ckpt_save): 65536 x 1002 and 1001 BF16 58 and 64 us
 // saved (52 and 47 % of measured; with a warp reduction per block 72 and 64),
-// 49 and 52 us restored; x 1000 (whole, by eights) 43 and 37 us, in fp32 49
-// and 49 us (100 %).
+// 49 and 52 us restored; x 1000 (whole, by eights) 43 and 38 us, in fp32 49
+// and 49 us (100 %).  The activation on 49152 rows of 1002, 1001 and 1000
+// BF16: forward 90, 109 and 69 us (66, 55 and 86 %), without checkpoints 45,
+// 57 and 43, backward 94, 119 and 68 us (63, 50 and 88 %).
 #include "common.cuh"
 #include "internal.h"
 #include "rowops.cuh"
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(kThreads) k_swiglu(const Ti *gate, int64_t ld_
             keep<FMT>(u, p, cu, ldc, nb);
         }
     };
-    // (49152 x 1001 BF16 in the other order 117 us instead of 110; in the whole
+    // (49152 x 1001 BF16 in the other order 117 us instead of 109; in the whole
     // layout, checkpoints first, 98304 x 1408 233 us both ways, x 1000 72, not 69)
     if constexpr (L != kWhole) keep_both();
     if (in) {

@@ -33,13 +33,15 @@ constexpr int kThreads = 256;
 //      by one ballot per bit of the expert's number, and a lane's place is
 //      the warp's running place plus the number of such lanes before it.
 // One launch and no scratch memory: 98304 slots take 9 us, of which about 4
-// are the steps between the passes and the launch; the passes are bound by
-// the integer pipe of the cluster's 16 SMs (142 warp instructions per 32
-// slots at 256 experts; 524288 slots 31 us).  Measured slower: one CTA (71
-// us), __match_any_sync for the ballots (2 us more), ranks kept from the
-// first pass through pos (2 us more).  More clusters and two more kernels
-// that join them win only above some 200000 slots (524288: 18 us; 98304: 9
-// to 10).
+// are the steps between the passes and the launch; 524288 slots of 256 experts
+// 31 us.  The passes are bound by the 16 of 152 SMs that a cluster has, none of
+// whose units is full: at 524288 slots the integer pipe is 58 % busy, 54 % of
+// the issue slots are used (142 warp instructions per 32 slots), and a third of
+// a warp's time it waits for ids.  Measured slower at 98304: one CTA (71 us),
+// __match_any_sync for the ballots (2 us more), ranks kept from the first pass
+// through pos (2 us more).  Several clusters and two more kernels that join
+// them are faster above some 200000 slots (524288: 18 us; 98304: 9 to 10) and
+// not built.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxSortCtas = 16;
@@ -177,8 +179,8 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const Id *ids, uint32
 // A thread reads its part of a token's row once and writes it topk times (not:
 // a thread per result row, which would read x topk times): one 16-byte unit
 // where all rows are 16-byte aligned, else eight elements a warp's width
-// apart.  Bound by DRAM writes: 71 us, 6.6 TB/s (98 % of measured); rows of
-// 1001 BF16 elements 47 us (73 %), bound by the number of 64-byte accesses.
+// apart.  Bound by DRAM writes: 71 us, 6.7 TB/s (100 % of measured); rows of
+// 1001 BF16 elements 45 us (76 %), bound by the number of 64-byte accesses.
 template <class Unit, int N>
 __global__ void __launch_bounds__(kThreads) k_moe_dispatch(const Unit *x, int64_t ld_x, Unit *__restrict__ xs,
                                                            int64_t ld_xs, const int32_t *pos,
@@ -255,8 +257,9 @@ __global__ void __launch_bounds__(kCombineThreads<N>)
 // addition per warp in shared memory, joins them in an order that depends on
 // nothing but the sizes and the layout.  Bound by DRAM: fp32 y, BF16 dout and
 // dy 181 us, 7.0 TB/s (106 % of measured; one choice after the other 245);
-// 8192 x 2 rows of 8192 BF16 100 us (101 %); rows of 1001 BF16 47 us (47 %).
-// One token a CTA: with two (256 threads) 188, 102 and 58 us.
+// 8192 x 2 rows of 8192 BF16 100 us (101 %); 8192 x 4 rows of 1001 BF16 46 us
+// (48 %), of 1002 44 us (51 %).  One token a CTA: with two (256 threads) 188,
+// 102 and 58 us.
 constexpr int kBatch = 4, kBwdThreads = 128;
 
 // y's elements of one part: raw in the whole layout, else as fp32.
@@ -452,11 +455,11 @@ cudaError_t launch_moe_combine_bwd(const void *dout, int dout_dtype, int64_t ld_
                             parts, m.tokens);
                     };
                     // 128 threads a token unless most would idle.  Measured
-                    // (32 / 64 / 128 / 256, rows of 2048): 16384 tokens x 6
-                    // 195 / 189 / 190 / 214 us, 128 tokens 9.4 / 6.2 / 4.3 /
-                    // 3.8 us; the count is a constant of the kernel, which
-                    // lets its loop over the row be unrolled (8192 x 2 of
-                    // 8192 BF16: 115 us with a variable, 103 us so).
+                    // (32 / 64 / 128): 16384 tokens x 6 of 2048 194 / 187 /
+                    // 182 us, 128 tokens 8.5 / 5.2 / 3.8 us, 8192 x 4 of
+                    // 1001 BF16 52 / 48 / 46 us.  The count is a constant of
+                    // the kernel, which lets its loop over the row be
+                    // unrolled (with a variable the last takes 59 us).
                     if (threads_of(L, parts) <= 64) with(Int<32>());
                     else with(Int<128>());
                 };

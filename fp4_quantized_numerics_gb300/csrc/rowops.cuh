@@ -29,11 +29,12 @@ namespace ufp4 {
 // 4.2 -> 4.0 us.  Allowing the successor explicitly from the start makes the
 // short kernels slower (2.9, 4.6 us): its waiting CTAs take the SMs early.
 //
-// Returns 0, which the compiler does not know: added to the index that every
-// address is made from, it keeps all loads behind the wait, whatever the
-// compiler may assume of the data.  (Outputs are __restrict__, so that loads
-// move past stores; inputs are not, which would make their loads non-coherent
-// ones.)
+// Returns 0 out of the asm statement: added to the index that every address is
+// made from, it keeps the front end, to which the value is unknown, from
+// moving loads above the wait, whatever it may assume of the data.  Behind the
+// front end the order is the instruction's own: no access to memory passes
+// griddepcontrol.wait.  (Outputs are __restrict__, so that loads move past
+// stores; inputs are not, which would make their loads non-coherent ones.)
 __device__ __forceinline__ uint32_t begin_in_order() {
     uint32_t zero;
     asm volatile("griddepcontrol.wait;\n\tmov.u32 %0, 0;" : "=r"(zero)::"memory");
