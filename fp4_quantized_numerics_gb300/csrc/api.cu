@@ -604,6 +604,188 @@ ufp4_status ufp4_swiglu_bwd(const void *dh, int32_t dh_dtype, int64_t ld_dh, con
 
 }  // extern "C"
 
+// ------------------------------------------- answering with a quantized model
+
+namespace {
+
+// A tokens x heads x dim operand, checked when it has elements.
+bool valid_heads(const void *p, int32_t dtype, int64_t tokens, int64_t heads, int64_t dim, int64_t ld, int64_t head) {
+    if (!valid_dtype(dtype) || head < dim || ld < dim) return false;
+    if (tokens == 0) return true;
+    return p && aligned(p, dtype == UFP4_BF16 ? 2 : 4);
+}
+bool strides_within_limits(int64_t ld, int64_t head) { return ld <= UFP4_MAX_DIM && head <= UFP4_MAX_DIM; }
+
+ufp4_status check_cache(const ufp4_cache *c, Cache *out) {
+    if (!c || c->reserved != 0 || c->pages < 0 || c->heads < 1) return UFP4_ERR_INVALID;
+    if (c->grid != UFP4_E2M1 && c->grid != UFP4_E1M2 && c->grid != UFP4_E2M1C)
+        return c->grid == UFP4_MXFP4 ? UFP4_ERR_UNSUPPORTED : UFP4_ERR_INVALID;
+    if (c->rht != 0 && c->rht != 1) return UFP4_ERR_INVALID;
+    if (c->page < 1 || (c->page & (c->page - 1)) || c->head_dim < 16 || c->head_dim % 16) return UFP4_ERR_INVALID;
+    if (c->page < 16 || c->page > 32768 || c->head_dim > 256) return UFP4_ERR_UNSUPPORTED;
+    if (c->pages > UFP4_MAX_DIM || c->heads > (1 << 16)) return UFP4_ERR_UNSUPPORTED;
+    if (c->pages > 0)
+        for (const void *p : {(const void *)c->k_codes, (const void *)c->k_scales, (const void *)c->k_row_scale,
+                              (const void *)c->v_codes, (const void *)c->v_scales, (const void *)c->v_row_scale})
+            if (!p || !aligned(p, 16)) return UFP4_ERR_INVALID;
+    int shift = 0;
+    while ((1 << shift) < c->page) ++shift;
+    *out = Cache{{c->k_codes, c->k_scales, c->k_row_scale}, {c->v_codes, c->v_scales, c->v_row_scale},
+                 c->pages, c->heads, shift, c->head_dim, cache_padded(c->head_dim), c->grid, c->rht, c->rht_seed};
+    return UFP4_OK;
+}
+
+ufp4_status cache_rows(const void *kx, const void *vx, void *ky, void *vy, int32_t dtype, int64_t tokens, int64_t ld_k,
+                       int64_t head_k, int64_t ld_v, int64_t head_v, const int64_t *slots, const ufp4_cache *cache,
+                       CacheRows *l) {
+    ufp4_status st = check_cache(cache, &l->cache);
+    if (st != UFP4_OK) return st;
+    if (tokens < 0) return UFP4_ERR_INVALID;
+    const void *k = kx ? kx : ky, *v = vx ? vx : vy;
+    const int64_t h = l->cache.heads, d = l->cache.dim;
+    if (!valid_heads(k, dtype, tokens, h, d, ld_k, head_k) || !valid_heads(v, dtype, tokens, h, d, ld_v, head_v))
+        return UFP4_ERR_INVALID;
+    if (tokens > 0 && (!slots || !aligned(slots, 8))) return UFP4_ERR_INVALID;
+    if (!strides_within_limits(ld_k, head_k) || !strides_within_limits(ld_v, head_v) || tokens > (1LL << 31) / h)
+        return UFP4_ERR_UNSUPPORTED;
+    l->x[0] = kx; l->x[1] = vx;
+    l->y[0] = ky; l->y[1] = vy;
+    l->dtype = dtype;
+    l->tokens = tokens;
+    l->ld_token[0] = ld_k; l->ld_token[1] = ld_v;
+    l->ld_head[0] = head_k; l->ld_head[1] = head_v;
+    l->slots = slots;
+    return UFP4_OK;
+}
+
+// Weights of a few-token product.
+ufp4_status check_weights(const ufp4_qtensor *w, int32_t rht) {
+    if (!valid_qtensor(w) || (rht != 0 && rht != 1)) return UFP4_ERR_INVALID;
+    if (w->grid == UFP4_MXFP4 || w->k > UFP4_MAX_WIDTH || !within_limits(w->rows, w->k)) return UFP4_ERR_UNSUPPORTED;
+    return UFP4_OK;
+}
+
+// k = 0: the sums have no terms.
+ufp4_status write_zeros(void *y, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, cudaStream_t s) {
+    const size_t esz = dtype == UFP4_BF16 ? 2 : 4;
+    return from_cuda(cudaMemset2DAsync(y, ld * esz, 0, cols * esz, rows, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+ufp4_status ufp4_gemv(const void *x, int32_t x_dtype, int64_t tokens, int64_t ld_x, const ufp4_qtensor *w, int32_t rht,
+                      uint64_t rht_seed, void *y, int32_t y_dtype, int64_t ld_y, ufp4_stream_t stream) {
+    ufp4_status st = check_weights(w, rht);
+    if (st != UFP4_OK) return st;
+    if (!valid_rows(x, x_dtype, tokens, w->k, ld_x) || !valid_rows(y, y_dtype, tokens, w->rows, ld_y))
+        return UFP4_ERR_INVALID;
+    if (std::max({tokens, ld_x, ld_y}) > UFP4_MAX_DIM) return UFP4_ERR_UNSUPPORTED;
+    if (tokens == 0 || w->rows == 0) return UFP4_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (w->k == 0) return write_zeros(y, y_dtype, tokens, w->rows, ld_y, s);
+    GemvLaunch l{};
+    l.x = x; l.x_dtype = x_dtype; l.tokens = tokens; l.ld_x = ld_x;
+    l.codes = w->codes; l.scales = w->scales; l.tensor_scale = w->tensor_scale;
+    l.rows = w->rows; l.k = w->k; l.grid = w->grid;
+    l.rht = rht; l.rht_seed = rht_seed;
+    l.y = y; l.y_dtype = y_dtype; l.ld_y = ld_y;
+    return from_cuda(launch_gemv(l, s));
+}
+
+ufp4_status ufp4_gemv_grouped(const void *x, int32_t x_dtype, int64_t ld_x, int32_t gather, const ufp4_qtensor *w,
+                              int64_t rows, const ufp4_moe_plan *plan, int32_t rht, uint64_t rht_seed, void *y,
+                              int32_t y_dtype, int64_t ld_y, ufp4_stream_t stream) {
+    MoePlan m;
+    ufp4_status st = check_plan(plan, &m);
+    if (st != UFP4_OK) return st;
+    st = check_weights(w, rht);
+    if (st != UFP4_OK) return st;
+    if (gather != 0 && gather != 1) return UFP4_ERR_INVALID;
+    if (rows < 0 || rows > UFP4_MAX_DIM || w->rows != m.n_experts * rpad_of(rows)) return UFP4_ERR_INVALID;
+    const int64_t slots = m.tokens * m.topk;
+    if (!valid_rows(x, x_dtype, gather ? m.tokens : slots, w->k, ld_x) || !valid_rows(y, y_dtype, slots, rows, ld_y))
+        return UFP4_ERR_INVALID;
+    if (std::max(ld_x, ld_y) > UFP4_MAX_DIM) return UFP4_ERR_UNSUPPORTED;
+    if (slots == 0 || rows == 0) return UFP4_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (w->k == 0) return write_zeros(y, y_dtype, slots, rows, ld_y, s);
+    GemvLaunch l{};
+    l.x = x; l.x_dtype = x_dtype; l.tokens = m.tokens; l.ld_x = ld_x;
+    l.codes = w->codes; l.scales = w->scales; l.tensor_scale = w->tensor_scale;
+    l.rows = rows; l.k = w->k; l.grid = w->grid;
+    l.rht = rht; l.rht_seed = rht_seed;
+    l.y = y; l.y_dtype = y_dtype; l.ld_y = ld_y;
+    l.offsets = m.offsets; l.src = m.src;
+    l.n_experts = m.n_experts; l.topk = m.topk; l.gather = gather; l.slots = slots;
+    return from_cuda(launch_gemv(l, s));
+}
+
+int64_t ufp4_cache_dim(int64_t head_dim) { return head_dim <= 0 || head_dim > 256 ? 0 : cache_padded((int)head_dim); }
+
+ufp4_status ufp4_cache_append(const void *k, const void *v, int32_t dtype, int64_t tokens, int64_t ld_k,
+                              int64_t head_k, int64_t ld_v, int64_t head_v, const int64_t *slots,
+                              const ufp4_cache *cache, ufp4_stream_t stream) {
+    CacheRows l{};
+    ufp4_status st = cache_rows(k, v, nullptr, nullptr, dtype, tokens, ld_k, head_k, ld_v, head_v, slots, cache, &l);
+    if (st != UFP4_OK || tokens == 0 || l.cache.pages == 0) return st;
+    return from_cuda(launch_cache_append(l, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+ufp4_status ufp4_cache_load(const ufp4_cache *cache, const int64_t *slots, int64_t tokens, void *k, void *v,
+                            int32_t dtype, int64_t ld_k, int64_t head_k, int64_t ld_v, int64_t head_v,
+                            ufp4_stream_t stream) {
+    CacheRows l{};
+    ufp4_status st = cache_rows(nullptr, nullptr, k, v, dtype, tokens, ld_k, head_k, ld_v, head_v, slots, cache, &l);
+    if (st != UFP4_OK || tokens == 0) return st;
+    return from_cuda(launch_cache_load(l, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t ufp4_cache_attn_workspace_bytes(int64_t batch, int32_t m, int32_t heads, int64_t width,
+                                       const ufp4_cache *cache) {
+    Cache c;
+    if (check_cache(cache, &c) != UFP4_OK || batch <= 0 || m < 1 || m > UFP4_MAX_NEW || heads < 1 || width < 0 ||
+        heads % c.heads || width > UFP4_MAX_DIM >> c.page_shift || batch > UFP4_MAX_DIM / heads / m)
+        return 0;
+    return cache_attn_workspace(batch, m, heads, c.heads, c.padded, width << c.page_shift);
+}
+
+ufp4_status ufp4_cache_attn(const void *q, int32_t q_dtype, int64_t ld_q, int64_t head_q, int64_t batch, int32_t m,
+                            int32_t heads, const ufp4_cache *cache, const int32_t *table, int64_t ld_table,
+                            int64_t width, const int32_t *lens, const uint64_t *mask, float scale, void *out,
+                            int32_t out_dtype, int64_t ld_out, int64_t head_out, float *lse, void *workspace,
+                            size_t workspace_bytes, ufp4_stream_t stream) {
+    CacheAttn l{};
+    ufp4_status st = check_cache(cache, &l.cache);
+    if (st != UFP4_OK) return st;
+    if (batch < 0 || m < 1 || heads < 1 || heads % l.cache.heads || width < 0 || ld_table < width)
+        return UFP4_ERR_INVALID;
+    const int64_t d = l.cache.dim;
+    if (!valid_heads(q, q_dtype, batch, heads, d, ld_q, head_q) ||
+        !valid_heads(out, out_dtype, batch, heads, d, ld_out, head_out))
+        return UFP4_ERR_INVALID;
+    if (batch > 0 && (!lens || !aligned(lens, 4) || (width > 0 && (!table || !aligned(table, 4)))))
+        return UFP4_ERR_INVALID;
+    if ((mask && !aligned(mask, 8)) || (lse && !aligned(lse, 4)) || !(scale - scale == 0.0f)) return UFP4_ERR_INVALID;
+    if (m > UFP4_MAX_NEW || width > UFP4_MAX_DIM >> l.cache.page_shift || ld_table > UFP4_MAX_DIM ||
+        batch > UFP4_MAX_DIM / heads / m || !strides_within_limits(ld_q, head_q) ||
+        !strides_within_limits(ld_out, head_out))
+        return UFP4_ERR_UNSUPPORTED;
+    if (batch == 0) return UFP4_OK;
+    const size_t need = cache_attn_workspace(batch, m, heads, l.cache.heads, l.cache.padded, width << l.cache.page_shift);
+    if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return UFP4_ERR_INVALID;
+    l.q = q; l.q_dtype = q_dtype; l.q_token = ld_q; l.q_head = head_q;
+    l.batch = batch; l.m = m; l.heads = heads;
+    l.table = table; l.ld_table = ld_table; l.width = width;
+    l.lens = lens; l.mask = mask; l.scale = scale;
+    l.out = out; l.out_dtype = out_dtype; l.o_token = ld_out; l.o_head = head_out;
+    l.lse = lse; l.workspace = workspace;
+    return from_cuda(launch_cache_attn(l, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
 // ---------------------------------------------------------------------------
 // ufp4_quantize_noalloc: ufp4_quantize for callers that cannot allocate
 // device memory.  Some host programs may not call cudaMalloc at the point

@@ -1,0 +1,828 @@
+// cache.cu -- keys and values kept in 4 bits: written row by row as they
+// come, read back, and attended over by new tokens.  (include/ufp4.h:
+// ufp4_cache_append, ufp4_cache_load, ufp4_cache_attn.)
+#include "common.cuh"
+#include "dequant.cuh"
+#include "internal.h"
+#include "rowops.cuh"
+
+#include <algorithm>
+
+namespace ufp4 {
+namespace {
+
+// ------------------------------------------------------------ write and read
+// A row (one token's key or value of one head) is quantized by itself: its
+// largest magnitude takes the place of the tensor's in ufp4_quantize.  A
+// thread has one 16-block, the 4, 8 or 16 threads of a row exchange their
+// maxima.  Bound by memory: 2 or 4 bytes an element in, 0.6 out.
+struct RowArgs {
+    CacheHalf half[2];
+    const void *x[2];            // append: k and v; load: unused
+    void *y[2];
+    int64_t ld_token[2], ld_head[2];
+    int32_t fp32, wide;          // wide: rows of x / y in 32-byte accesses
+    const int64_t *slots;
+    int64_t places;              // pages x page
+    int32_t heads, page_shift, dim, blocks, grid, rht;
+    uint64_t rht_seed;
+    RowDiv by_heads;
+    uint64_t rows;               // tokens x heads
+};
+
+// Index of the cache's row for head h of a place.
+__device__ __forceinline__ int64_t cache_row(int64_t slot, int32_t h, int32_t heads, int32_t page_shift) {
+    const int64_t page = slot >> page_shift;
+    return ((page * heads + h) << page_shift) + (slot & ((1 << page_shift) - 1));
+}
+
+template <class T>
+__device__ __forceinline__ void load16(const T *p, bool wide, float (&v)[16]) {
+    if (wide) {
+        load_whole<16>(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = load_one(p + i);
+    }
+}
+template <class T>
+__device__ __forceinline__ void store16(T *p, bool wide, const float (&v)[16]) {
+    if (wide) {
+        store_whole<16>(p, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) store_one(p + i, v[i]);
+    }
+}
+
+template <class T, int G>       // G threads a row
+__global__ void __launch_bounds__(128) k_append(RowArgs a) {
+    const uint32_t zero = begin_in_order();
+    const int which = blockIdx.y;
+    const uint64_t at = (uint64_t)blockIdx.x * 128 + threadIdx.x;
+    const uint64_t row = at / G;
+    const int b = (int)(at % G);
+    if (row >= a.rows) return;
+    const uint64_t token = row_of(row, a.by_heads);
+    const int32_t h = (int32_t)(row - token * a.heads);
+    const int64_t slot = a.slots[zero + token];
+    if (slot < 0 || slot >= a.places) return;
+    float v[16] = {};
+    const bool mine = b * 16 < a.dim;
+    if (mine) {
+        const T *p = static_cast<const T *>(a.x[which]) + token * a.ld_token[which] + h * a.ld_head[which] + b * 16;
+        load16(p, a.wide, v);
+        if (a.rht) rotate16(v, rht_sign_mask(a.rht_seed));
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) top = max3_nan(top, fabsf(v[i]), fabsf(v[i + 1]));
+    float all = top;
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t group = (G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1u)) << (lane & ~(G - 1u));
+#pragma unroll
+    for (int d = 1; d < G; d <<= 1) all = max_nan(all, __shfl_xor_sync(group, all, d));
+    const bool finite = all < __uint_as_float(0x7F800000u);
+    const float qmax = grid_qmax(a.grid), range = 448.0f * qmax;
+    const float enc = all > 0.0f ? fminf(__fdiv_rn(range, all), kFltMax) : 1.0f;
+    const float dec = all > 0.0f ? __fdiv_rn(all, range) : 1.0f;
+    uint32_t e = e4m3_from_f32(__fmul_rn(__fdiv_rn(top, qmax), enc));
+    if (!finite) e = 0;
+    const float ev = e4m3_to_f32(e), r = e ? __fdiv_rn(enc, ev) : 0.0f;
+    uint32_t w[2] = {0u, 0u};
+    if (e) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float p = __fmul_rn(v[i], r), q = __fmul_rn(v[i + 1], r);
+            uint32_t two;
+            if (a.grid == kE2M1) {
+                two = e2m1x2_rn(p, q);
+            } else {
+                const float most = (float)grid_top(a.grid);
+                two = e1m2_rn(p, most) | (e1m2_rn(q, most) << 4);
+            }
+            w[i / 8] |= two << (4 * (i % 8));
+        }
+    }
+    if (b >= a.blocks) return;
+    const CacheHalf c = a.half[which];
+    const int64_t to = cache_row(slot, h, a.heads, a.page_shift);
+    *reinterpret_cast<uint2 *>(c.codes + to * (a.blocks * 8) + b * 8) = make_uint2(w[0], w[1]);
+    c.scales[to * a.blocks + b] = (uint8_t)e;
+    if (b == 0) c.row_scale[to] = finite ? dec : __uint_as_float(0x7FC00000u);
+}
+
+template <class T, int G>
+__global__ void __launch_bounds__(128) k_load(RowArgs a) {
+    const uint32_t zero = begin_in_order();
+    const int which = blockIdx.y;
+    const uint64_t at = (uint64_t)blockIdx.x * 128 + threadIdx.x;
+    const uint64_t row = at / G;
+    const int b = (int)(at % G);
+    if (row >= a.rows || b * 16 >= a.dim) return;
+    const uint64_t token = row_of(row, a.by_heads);
+    const int32_t h = (int32_t)(row - token * a.heads);
+    const int64_t slot = a.slots[zero + token];
+    float v[16] = {};
+    if (slot >= 0 && slot < a.places) {
+        const CacheHalf c = a.half[which];
+        const int64_t from = cache_row(slot, h, a.heads, a.page_shift);
+        const uint2 w = *reinterpret_cast<const uint2 *>(c.codes + from * (a.blocks * 8) + b * 8);
+        const float e = e4m3_to_f32(c.scales[from * a.blocks + b]), s = c.row_scale[from];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint32_t code = (i < 8 ? w.x : w.y) >> (4 * (i % 8));
+            const float m = __fmul_rn(grid_value(a.grid, code), e);
+            v[i] = __fmul_rn(code & 8u ? -m : m, s);
+        }
+        if (a.rht) rotate16_back(v, rht_sign_mask(a.rht_seed));
+    }
+    T *p = static_cast<T *>(a.y[which]) + token * a.ld_token[which] + h * a.ld_head[which] + b * 16;
+    store16(p, a.wide, v);
+}
+
+// ---------------------------------------------------------------- attention
+// out = softmax(scale q K^T) V over a sequence's rows of the cache, for the
+// `m` new tokens that end it; a group of query heads shares a head of the
+// cache, and group x m queries are the columns of both products.
+//
+// Bound by reading the cache for one token (76 bytes for a row of 128 and 1024
+// flops a query head).  A warp takes 32 rows at a time through both products
+// by itself, with its own running maximum and sum:
+//  * rows come by cp.async, 16 bytes a lane, a few tiles ahead, into shared
+//    memory of the warp's own (no barrier in the loop);
+//  * S^T = K q^T: keys are the 16-row operand, so a lane decodes 8 to 32 bytes
+//    of a row's codes, which share 1 to 4 block scales, and a score's row scale
+//    is a factor of the accumulator;
+//  * O^T = V^T P^T: a lane decodes the same elements of four keys and pairs
+//    them up by permutes; P^T becomes the other operand by movmatrix.
+// The probabilities enter the product times their key's row scale, brought
+// below 2^15 by a power of two that follows the largest scale seen, as FP16
+// (11 bits; two of them for fp32 results), and the sums are fp32.  Keys of a
+// sequence are spread over warps, and over CTAs (splits) where sequences and
+// heads are too few; the parts are joined in a fixed order.
+struct AttnArgs {
+    const void *q;
+    int64_t q_token, q_head;
+    int32_t q_fp32, planes, two_p;
+    CacheHalf k, v;
+    const int32_t *table;
+    int64_t ld_table;
+    int32_t width, pages, page_shift;
+    const int32_t *lens;
+    const uint64_t *mask;
+    int32_t batch, m, heads, kv, group, dim, rht, qtiles, splits;
+    uint64_t rht_seed;
+    float scale;
+    void *out;
+    int64_t o_token, o_head;
+    int32_t out_fp32;
+    float *lse;
+    float *part_o, *part_m, *part_l;     // splits > 1: of each split and query
+};
+
+constexpr int kAttnWarps = 4, kTileKeys = 32, kSplitKeys = 128;   // a split's keys are a multiple of the last
+
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+// Keys [first, last) of a sequence of `len` that split s of n takes.
+__device__ __forceinline__ void split_range(int len, int s, int n, int &first, int &last) {
+    const int per = ((len + n - 1) / n + kSplitKeys - 1) / kSplitKeys * kSplitKeys;
+    first = (int)min((int64_t)s * per, (int64_t)len);
+    last = min(first + per, len);
+}
+
+// Ends a row: O / l, back from the rotation, rounded once.  A lane has the 8
+// elements 8 lane .. 8 lane + 7 (lanes past the row none).
+__device__ __forceinline__ void finish_row(const AttnArgs &a, float (&o)[8], float m2, float l, int b, int q, int kvh,
+                                           int lane) {
+    const int node = q / a.group, head = kvh * a.group + q % a.group;
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;      // (NaN stays)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= inv;
+    if (a.rht) {
+        // the butterflies of 16 over two neighbouring lanes
+        const uint32_t signs = rht_sign_mask(a.rht_seed) >> (lane & 1) * 8;
+        fwht8(o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, o[i], 1);
+            const float v = (lane & 1 ? other - o[i] : o[i] + other) * 0.25f;
+            o[i] = __uint_as_float(__float_as_uint(v) ^ ((signs << (31 - i)) & 0x80000000u));
+        }
+    }
+    const int64_t token = (int64_t)b * a.m + node;
+    const int64_t at = token * a.o_token + head * a.o_head + lane * 8;
+    if (lane * 8 < a.dim) {
+        if (a.out_fp32) {
+            float *p = static_cast<float *>(a.out) + at;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = o[i];
+        } else {
+            __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(a.out) + at;
+            if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                store_words(p, w);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i] = __float2bfloat16_rn(o[i]);
+            }
+        }
+    }
+    if (a.lse && lane == 0)
+        a.lse[token * a.heads + head] = (m2 + log2f(l)) * 0.6931471805599453f;   // no key: -inf + -inf
+}
+
+// DC: 64-element pieces of a padded row (1, 2 or 4); NT: groups of 8 queries.
+template <int GRID, int DC, int NT>
+__global__ void __launch_bounds__(kAttnWarps * 32) k_attn(AttnArgs a) {
+    constexpr int kDim = 64 * DC, kQ = 8 * NT, kRow = kDim / 2, kBlocks = kDim / 16;
+    constexpr int kStages = DC == 4 ? 2 : 3;
+    constexpr int kCodes = kTileKeys * kRow, kScales = kTileKeys * kBlocks, kRs = kTileKeys * 4;
+    constexpr int kStage = 2 * (kCodes + kScales + kRs);
+    // a stage: codes, scales and row scales of the keys, then of the values
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint4 *qs = reinterpret_cast<uint4 *>(smem);                       // [2][2 DC][kQ][4] x 16 bytes
+    float *qf = reinterpret_cast<float *>(qs + 2 * 2 * DC * kQ * 4);   // [kQ]
+    uint64_t *qm = reinterpret_cast<uint64_t *>(qf + kQ);              // [kQ]
+    uint8_t *stages = reinterpret_cast<uint8_t *>(qm + kQ);
+    const uint32_t zero = begin_in_order();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+
+    const int qt = blockIdx.x % a.qtiles, bh = blockIdx.x / a.qtiles, kvh = bh % a.kv, b = bh / a.kv;
+    const int most = a.width << a.page_shift;
+    const int len = min(max(a.lens[zero + b], 0), most);
+    int first, last;
+    split_range(len, blockIdx.y, a.splits, first, last);
+    if (a.splits > 1 && first >= last) return;        // (the join does not look)
+    const int q0 = qt * kQ, nq = min(a.group * a.m - q0, kQ);
+
+    // ---- the rows' copies
+    uint8_t *my = stages + warp * kStages * kStage;
+    const uint32_t my_s = (uint32_t)__cvta_generic_to_shared(my);
+    const int tiles = (last - first + kTileKeys - 1) / kTileKeys;
+    const int32_t *table = a.table + b * a.ld_table;
+    const auto page_of = [&](int tile, int half) -> int {
+        const int pos = first + tile * kTileKeys + half * 16;
+        return tile < tiles && pos < last ? table[zero + (pos >> a.page_shift)] : -1;
+    };
+    int next[2];
+    const auto copy = [&](int tile, int slot) {
+        const uint32_t to = my_s + slot * kStage;
+        int64_t row[2];
+        bool real[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int pos = first + tile * kTileKeys + h * 16;
+            real[h] = next[h] >= 0 && next[h] < a.pages;
+            row[h] = real[h] ? cache_row(((int64_t)next[h] << a.page_shift) + (pos & ((1 << a.page_shift) - 1)), kvh,
+                                         a.kv, a.page_shift)
+                             : 0;
+        }
+        if (tile < tiles) {
+#pragma unroll
+            for (int j = 0; j < 2 * DC; ++j) {
+                const int h = j / DC;
+                const int64_t at = row[h] * kRow + ((j % DC) * 32 + lane) * 16;
+                copy16(to + (j * 32 + lane) * 16, a.k.codes + at, real[h]);
+                copy16(to + kStage / 2 + (j * 32 + lane) * 16, a.v.codes + at, real[h]);
+            }
+#pragma unroll
+            for (int j = 0; j < (16 * DC + 31) / 32; ++j) {
+                const int i = j * 32 + lane;                     // values: the upper half of 16 DC pieces
+                if (i < 16 * DC) {
+                    const int h = i / (4 * DC) % 2, v = i / (8 * DC);
+                    const int64_t at = (h ? row[1] : row[0]) * kBlocks + i % (4 * DC) * 16;
+                    copy16(to + v * (kStage / 2) + kCodes + i % (8 * DC) * 16, (v ? a.v.scales : a.k.scales) + at,
+                           h ? real[1] : real[0]);
+                }
+            }
+            if (lane < 16) {
+                const int h = lane / 4 % 2, v = lane / 8;
+                copy16(to + v * (kStage / 2) + kCodes + kScales + lane % 8 * 16,
+                       (v ? a.v.row_scale : a.k.row_scale) + (h ? row[1] : row[0]) + lane % 4 * 4,
+                       h ? real[1] : real[0]);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const auto look = [&](int tile) {
+        next[0] = page_of(tile, 0);
+        next[1] = page_of(tile, 1);
+    };
+    look(warp);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        copy(warp + s * kAttnWarps, s);
+        look(warp + (s + 1) * kAttnWarps);
+    }
+
+    // ---- the queries as operands: [plane][word of a lane's elements][query][lane % 4]
+    const uint32_t signs = a.rht ? rht_sign_mask(a.rht_seed) : 0u;
+    uint64_t seen = 0;
+    for (int i = tid; i < kQ * kBlocks; i += kAttnWarps * 32) {
+        const int col = i / kBlocks, blk = i % kBlocks, q = q0 + col;
+        float v[16] = {};
+        if (col < nq && blk * 16 < a.dim) {
+            const int64_t at = ((int64_t)b * a.m + q / a.group) * a.q_token +
+                               (kvh * a.group + q % a.group) * a.q_head + blk * 16;
+            if (a.q_fp32) {
+                const float *p = static_cast<const float *>(a.q) + at;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = p[j];
+            } else {
+                const uint16_t *p = static_cast<const uint16_t *>(a.q) + at;
+                if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[4];
+                        load_words(p + 8 * h, w);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            v[8 * h + 2 * j] = bf16lo(w[j]);
+                            v[8 * h + 2 * j + 1] = bf16hi(w[j]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float((uint32_t)p[j] << 16);
+                }
+            }
+            if (a.rht) rotate16(v, signs);
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = max(top, finite_bits(v[j]));
+#pragma unroll
+        for (int d = 1; d < kBlocks; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const int e = top_exponent(top);
+        const float up = exp2i(14 - e);
+        if (blk == 0) {
+            qf[col] = exp2i(e - 14) * kDecoded<GRID> * a.scale * 1.4426950408889634f;
+            const int node = q / a.group;
+            qm[col] = col >= nq ? 0ull : a.mask ? a.mask[(int64_t)b * a.m + node] : ~0ull >> (63 - node);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = v[8 * h + code_order<GRID>(2 * j)] * up, y = v[8 * h + code_order<GRID>(2 * j + 1)] * up;
+                hi[j] = f16_pair(x, y);
+                lo[j] = f16_rest(x, y, hi[j]);
+            }
+            const int at = (((blk % DC) * 2 + h) * kQ + col) * 4 + blk / DC;
+            qs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            qs[2 * DC * kQ * 4 + at] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+    __syncthreads();
+    for (int i = 0; i < nq; ++i) seen |= qm[i];
+
+    float o[4 * DC][NT][4] = {};
+    float mx[NT][2], l[NT][2] = {};
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
+    int ve = -110;                                   // exponent of the largest row scale of the values
+    float qscale[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        qscale[n][0] = qf[n * 8 + 2 * t];
+        qscale[n][1] = qf[n * 8 + 2 * t + 1];
+    }
+
+    int slot = 0;
+    for (int tile = warp; tile < tiles; tile += kAttnWarps) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncwarp();
+        {
+            const int ahead = tile + (kStages - 1) * kAttnWarps;
+            copy(ahead, slot == 0 ? kStages - 1 : slot - 1);
+            look(ahead + kAttnWarps);
+        }
+        uint8_t *ks = my + slot * kStage, *vs = ks + kStage / 2;
+        slot = slot + 1 == kStages ? 0 : slot + 1;
+        const int pos0 = first + tile * kTileKeys;
+        const bool edge = pos0 + kTileKeys > len - (a.m > 1 || a.mask ? a.m : 0);
+        if (edge) {
+            // rows that nobody sees may never have been written: their scales
+            // become zero, so that whatever codes stand there count for nothing
+            const int pos = pos0 + lane, rel = pos - (len - a.m);
+            if (pos >= last || (rel >= 0 && !(seen >> rel & 1))) {
+#pragma unroll
+                for (int j = 0; j < kBlocks / 4; ++j) {
+                    reinterpret_cast<uint32_t *>(ks + kCodes + lane * kBlocks)[j] = 0;
+                    reinterpret_cast<uint32_t *>(vs + kCodes + lane * kBlocks)[j] = 0;
+                }
+                reinterpret_cast<float *>(ks + kCodes + kScales)[lane] = 0.0f;
+                reinterpret_cast<float *>(vs + kCodes + kScales)[lane] = 0.0f;
+            }
+            __syncwarp();
+        }
+
+        // ---- scores: keys 16 i + g (and + 8) by queries 8 n + 2 t (and + 1)
+        float s[2][NT][4] = {};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t kw[2][2 * DC], kb[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int key = 16 * i + 8 * r + g;
+                const uint8_t *p = ks + key * kRow + t * (kRow / 4), *sp = ks + kCodes + key * kBlocks + t * DC;
+                if constexpr (DC == 1) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+                    kw[r][0] = w.x; kw[r][1] = w.y;
+                    kb[r] = *sp;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < DC / 2; ++j) {
+                        const uint4 w = reinterpret_cast<const uint4 *>(p)[j];
+                        kw[r][4 * j] = w.x; kw[r][4 * j + 1] = w.y; kw[r][4 * j + 2] = w.z; kw[r][4 * j + 3] = w.w;
+                    }
+                    if constexpr (DC == 2) kb[r] = *reinterpret_cast<const uint16_t *>(sp);
+                    else kb[r] = *reinterpret_cast<const uint32_t *>(sp);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2 * DC; ++u) {
+                uint32_t h[2][4];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t sc = scale_pair(kb[r], (u / 2) * 0x11u);
+                    decode8<GRID>(kw[r][u], h[r]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[r][j] = mul_pair(h[r][j], sc);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint4 x = qs[(u * kQ + n * 8 + g) * 4 + t];
+                    mma_f16(s[i][n], h[0][0], h[1][0], h[0][1], h[1][1], x.x, x.y);
+                    mma_f16(s[i][n], h[0][2], h[1][2], h[0][3], h[1][3], x.z, x.w);
+                    if (a.planes == 2) {
+                        const uint4 y = qs[2 * DC * kQ * 4 + (u * kQ + n * 8 + g) * 4 + t];
+                        mma_f16(s[i][n], h[0][0], h[1][0], h[0][1], h[1][1], y.x, y.y);
+                        mma_f16(s[i][n], h[0][2], h[1][2], h[0][3], h[1][3], y.z, y.w);
+                    }
+                }
+            }
+        }
+        float krs[4], vrs[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            krs[r] = reinterpret_cast<const float *>(ks + kCodes + kScales)[8 * r + g];
+            vrs[r] = reinterpret_cast<const float *>(vs + kCodes + kScales)[8 * r + g];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][n][j] *= krs[2 * i + (j >> 1)] * qscale[n][j & 1];
+        if (edge) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint64_t bits = qm[n * 8 + 2 * t + c];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int pos = pos0 + 8 * r + g, rel = pos - (len - a.m);
+                        const bool hidden = pos >= last || (rel >= 0 && !(bits >> rel & 1));
+                        if (hidden) s[r / 2][n][(r & 1) * 2 + c] = -INFINITY;
+                    }
+                }
+        }
+
+        // ---- running maximum and sum; weights of the values
+        const uint32_t vtop = __reduce_max_sync(0xffffffffu, max(max(finite_bits(vrs[0]), finite_bits(vrs[1])),
+                                                                 max(finite_bits(vrs[2]), finite_bits(vrs[3]))));
+        const int ve_new = max(ve, top_exponent(vtop));
+        const float v_back = ve_new == ve ? 1.0f : exp2f((float)(ve - ve_new));
+        ve = ve_new;
+        const float vup = exp2i(14 - ve);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) vrs[r] *= vup;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float top = fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c]));
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                top = fmaxf(top, mx[n][c]);
+                const float base = top == -INFINITY ? 0.0f : top;
+                const float back = exp2f(mx[n][c] - base);
+                mx[n][c] = top;
+                l[n][c] *= back;
+                const float ob = back * v_back;
+#pragma unroll
+                for (int i = 0; i < 4 * DC; ++i) {
+                    o[i][n][c] *= ob;
+                    o[i][n][2 + c] *= ob;
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float &x = s[r / 2][n][(r & 1) * 2 + c];
+                    const bool hidden = x == -INFINITY;
+                    const float p = exp2f(x - base);
+                    l[n][c] += p;
+                    x = hidden ? 0.0f : p * vrs[r];
+                }
+            }
+
+        // ---- values: elements of key 16 i + 2 t, + 1, + 8, + 9
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t h = f16_pair(s[i][n][2 * r], s[i][n][2 * r + 1]);
+                    ph[n][r] = transpose8x8(h);
+                    if (a.two_p) pl[n][r] = transpose8x8(f16_rest(s[i][n][2 * r], s[i][n][2 * r + 1], h));
+                }
+            uint32_t vw[4][DC], vb[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int key = 16 * i + 2 * t + (r & 1) + (r >> 1) * 8;
+                const uint8_t *p = vs + key * kRow + g * (kRow / 8), *sp = vs + kCodes + key * kBlocks;
+                if constexpr (DC == 1) {
+                    vw[r][0] = *reinterpret_cast<const uint32_t *>(p);
+                    vb[r] = sp[g >> 1];
+                } else if constexpr (DC == 2) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+                    vw[r][0] = w.x; vw[r][1] = w.y;
+                    vb[r] = sp[g];
+                } else {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+                    vw[r][0] = w.x; vw[r][1] = w.y; vw[r][2] = w.z; vw[r][3] = w.w;
+                    vb[r] = *reinterpret_cast<const uint16_t *>(sp + 2 * g);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < DC; ++u) {
+                uint32_t h[4][4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t sc = scale_pair(vb[r], DC == 4 ? (u / 2) * 0x11u : 0u);
+                    decode8<GRID>(vw[r][u], h[r]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[r][j] = mul_pair(h[r][j], sc);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t a0 = __byte_perm(h[0][j], h[1][j], 0x5410), a1 = __byte_perm(h[0][j], h[1][j], 0x7632);
+                    const uint32_t a2 = __byte_perm(h[2][j], h[3][j], 0x5410), a3 = __byte_perm(h[2][j], h[3][j], 0x7632);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_f16(o[4 * u + j][n], a0, a1, a2, a3, ph[n][0], ph[n][1]);
+                        if (a.two_p) mma_f16(o[4 * u + j][n], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+                    }
+                }
+            }
+        }
+    }
+
+    // ---- the warps' parts together, in the stages' memory
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float *po = reinterpret_cast<float *>(stages);                 // [warp][query][kDim]
+    float *pm = po + kAttnWarps * kQ * kDim, *pl = pm + kAttnWarps * kQ;
+    const float down = exp2i(ve - 14) * kDecoded<GRID>;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float sum = l[n][c];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            const int col = n * 8 + 2 * t + c;
+            if (g == 0) {
+                pm[warp * kQ + col] = mx[n][c];
+                pl[warp * kQ + col] = sum;
+            }
+            float *row = po + (warp * kQ + col) * kDim + g * (kDim / 8);
+#pragma unroll
+            for (int u = 0; u < DC; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        row[u * 8 + code_order<GRID>(2 * j + e)] = o[4 * u + j][n][2 * e + c] * down;
+        }
+    __syncthreads();
+    for (int col = warp; col < nq; col += kAttnWarps) {
+        float top = -INFINITY, sum = 0.0f, v[8] = {};
+        for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, pm[w * kQ + col]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        for (int w = 0; w < kAttnWarps; ++w) {
+            const float f = exp2f(pm[w * kQ + col] - base);
+            sum += pl[w * kQ + col] * f;
+            if (lane * 8 < kDim) {
+                const float *row = po + (w * kQ + col) * kDim + lane * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += row[i] * f;
+            }
+        }
+        if (a.splits == 1) {
+            finish_row(a, v, top, sum, b, q0 + col, kvh, lane);
+        } else {
+            const int64_t r = ((int64_t)blockIdx.y * a.batch * a.kv + bh) * (a.group * a.m) + q0 + col;
+            if (lane * 8 < kDim) {
+                float4 *to = reinterpret_cast<float4 *>(a.part_o + r * kDim + lane * 8);
+                to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                to[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+            if (lane == 0) {
+                a.part_m[r] = top;
+                a.part_l[r] = sum;
+            }
+        }
+    }
+}
+
+// Joins the splits' parts, a warp a query.
+__global__ void __launch_bounds__(128) k_attn_join(AttnArgs a, int kdim) {
+    const uint32_t zero = begin_in_order();
+    const int lane = threadIdx.x & 31;
+    const int64_t queries = (int64_t)a.batch * a.kv * a.group * a.m;
+    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (r >= queries) return;
+    const int per = a.group * a.m;
+    const int bh = (int)(r / per), q = (int)(r % per), kvh = bh % a.kv, b = bh / a.kv;
+    const int len = min(max(a.lens[zero + b], 0), a.width << a.page_shift);
+    float top = -INFINITY, sum = 0.0f, v[8] = {};
+    int parts = 0;
+    for (int s = 0; s < a.splits; ++s) {
+        int first, last;
+        split_range(len, s, a.splits, first, last);
+        if (first < last) parts = s + 1;
+    }
+    for (int s = lane; s < parts; s += 32) top = fmaxf(top, a.part_m[s * queries + r + zero]);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+        const float f = exp2f(a.part_m[s * queries + r + zero] - base);
+        sum += a.part_l[s * queries + r + zero] * f;
+        if (lane * 8 < kdim) {
+            const float4 *from = reinterpret_cast<const float4 *>(a.part_o + (s * queries + r + zero) * kdim + lane * 8);
+            const float4 x = from[0], y = from[1];
+            v[0] += x.x * f; v[1] += x.y * f; v[2] += x.z * f; v[3] += x.w * f;
+            v[4] += y.x * f; v[5] += y.y * f; v[6] += y.z * f; v[7] += y.w * f;
+        }
+    }
+    finish_row(a, v, top, sum, b, q, kvh, lane);
+}
+
+// CTAs that keep the card busy; a split has 256 keys at least.
+int splits_of(int64_t batch, int64_t kv, int64_t qtiles, int64_t most_keys) {
+    const int64_t ctas = batch * kv * qtiles, want = 3 * (int64_t)num_sms();
+    int64_t s = (want + ctas - 1) / ctas;
+    s = std::min(s, (most_keys + 255) / 256);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(s, 512));
+}
+int query_tiles(int64_t queries) { return queries <= 8 ? 1 : (int)((queries + 15) / 16); }
+
+template <int GRID, int DC, int NT>
+cudaError_t attn(const AttnArgs &a, cudaStream_t s) {
+    constexpr int kDim = 64 * DC, kQ = 8 * NT;
+    constexpr int kStages = DC == 4 ? 2 : 3;
+    constexpr size_t kStage = 2 * (kTileKeys * (kDim / 2) + kTileKeys * (kDim / 16) + kTileKeys * 4);
+    constexpr size_t parts = kAttnWarps * kQ * (kDim + 2) * sizeof(float);
+    constexpr size_t bytes = 2 * 2 * DC * kQ * 4 * 16 + kQ * 12 + std::max(kAttnWarps * kStages * kStage, parts);
+    cudaError_t e = cudaFuncSetAttribute(k_attn<GRID, DC, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    e = launch_in_order_smem(k_attn<GRID, DC, NT>, dim3((unsigned)(a.batch * a.kv * a.qtiles), (unsigned)a.splits),
+                             kAttnWarps * 32, bytes, s, a);
+    if (e != cudaSuccess || a.splits == 1) return e;
+    const int64_t queries = (int64_t)a.batch * a.kv * a.group * a.m;
+    return launch_in_order(k_attn_join, (uint64_t)(queries + 3) / 4, 128, s, a, kDim);
+}
+
+template <class F>
+cudaError_t by_threads(int blocks, F f) {
+    return blocks <= 4 ? f(Int<4>()) : blocks <= 8 ? f(Int<8>()) : f(Int<16>());
+}
+
+RowArgs row_args(const CacheRows &l) {
+    RowArgs a{};
+    a.half[0] = l.cache.k;
+    a.half[1] = l.cache.v;
+    for (int i = 0; i < 2; ++i) {
+        a.x[i] = l.x[i];
+        a.y[i] = l.y[i];
+        a.ld_token[i] = l.ld_token[i];
+        a.ld_head[i] = l.ld_head[i];
+    }
+    a.fp32 = l.dtype == 1;
+    const size_t size = type_size(l.dtype);
+    a.wide = 1;
+    for (int i = 0; i < 2; ++i) {
+        const void *p = l.x[i] ? l.x[i] : l.y[i];
+        a.wide = a.wide && rows_by(p, l.ld_token[i], size, 16) && rows_by(p, l.ld_head[i], size, 16);
+    }
+    a.slots = l.slots;
+    a.places = l.cache.pages << l.cache.page_shift;
+    a.heads = l.cache.heads;
+    a.page_shift = l.cache.page_shift;
+    a.dim = l.cache.dim;
+    a.blocks = l.cache.padded / 16;
+    a.grid = l.cache.grid;
+    a.rht = l.cache.rht;
+    a.rht_seed = l.cache.rht_seed;
+    a.by_heads = make_rowdiv((uint32_t)l.cache.heads);
+    a.rows = (uint64_t)l.tokens * l.cache.heads;
+    return a;
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheRows &l, cudaStream_t s) {
+    const RowArgs a = row_args(l);
+    return by_threads(a.blocks, [&](auto g) {
+        constexpr int G = decltype(g)::value;
+        const dim3 grid((unsigned)((a.rows * G + 127) / 128), 2);
+        return a.fp32 ? launch_in_order_smem(k_append<float, G>, grid, 128, 0, s, a)
+                      : launch_in_order_smem(k_append<__nv_bfloat16, G>, grid, 128, 0, s, a);
+    });
+}
+
+cudaError_t launch_cache_load(const CacheRows &l, cudaStream_t s) {
+    const RowArgs a = row_args(l);
+    return by_threads(a.blocks, [&](auto g) {
+        constexpr int G = decltype(g)::value;
+        const dim3 grid((unsigned)((a.rows * G + 127) / 128), 2);
+        return a.fp32 ? launch_in_order_smem(k_load<float, G>, grid, 128, 0, s, a)
+                      : launch_in_order_smem(k_load<__nv_bfloat16, G>, grid, 128, 0, s, a);
+    });
+}
+
+size_t cache_attn_workspace(int64_t batch, int64_t m, int64_t heads, int64_t kv, int64_t padded, int64_t most_keys) {
+    const int64_t queries = heads / kv * m;
+    const int64_t splits = splits_of(batch, kv, query_tiles(queries), most_keys);
+    return splits == 1 ? 0 : (size_t)(splits * batch * m * heads * (padded + 2)) * sizeof(float);
+}
+
+cudaError_t launch_cache_attn(const CacheAttn &l, cudaStream_t s) {
+    AttnArgs a{};
+    a.q = l.q;
+    a.q_token = l.q_token;
+    a.q_head = l.q_head;
+    a.q_fp32 = l.q_dtype == 1;
+    a.planes = a.q_fp32 || l.cache.rht ? 2 : 1;      // (a BF16 query is an FP16 value times a power of two)
+    a.k = l.cache.k;
+    a.v = l.cache.v;
+    a.table = l.table;
+    a.ld_table = l.ld_table;
+    a.width = (int)l.width;
+    a.pages = (int)l.cache.pages;
+    a.page_shift = l.cache.page_shift;
+    a.lens = l.lens;
+    a.mask = l.mask;
+    a.batch = (int)l.batch;
+    a.m = l.m;
+    a.heads = l.heads;
+    a.kv = l.cache.heads;
+    a.group = l.heads / l.cache.heads;
+    a.dim = l.cache.dim;
+    a.rht = l.cache.rht;
+    a.rht_seed = l.cache.rht_seed;
+    a.scale = l.scale;
+    a.out = l.out;
+    a.o_token = l.o_token;
+    a.o_head = l.o_head;
+    a.out_fp32 = a.two_p = l.out_dtype == 1;
+    a.lse = l.lse;
+    const int64_t queries = (int64_t)a.group * a.m;
+    a.qtiles = query_tiles(queries);
+    a.splits = splits_of(a.batch, a.kv, a.qtiles, l.width << a.page_shift);
+    const int64_t all = (int64_t)a.batch * a.kv * queries * a.splits;
+    a.part_o = static_cast<float *>(l.workspace);
+    a.part_m = a.part_o + all * l.cache.padded;
+    a.part_l = a.part_m + all;
+    const auto with = [&](auto gr, auto dc) {
+        constexpr int G = decltype(gr)::value, D = decltype(dc)::value;
+        return queries <= 8 ? attn<G, D, 1>(a, s) : attn<G, D, 2>(a, s);
+    };
+    const auto by_dim = [&](auto gr) {
+        return l.cache.padded == 64 ? with(gr, Int<1>()) : l.cache.padded == 128 ? with(gr, Int<2>()) : with(gr, Int<4>());
+    };
+    return l.cache.grid == kE1M2 ? by_dim(Int<kE1M2>()) : by_dim(Int<kE2M1>());
+}
+
+}  // namespace ufp4

@@ -166,6 +166,73 @@ cudaError_t launch_swiglu_bwd(const void *dh, int dh_dtype, int64_t ld_dh, const
                               int64_t rows, int64_t cols, void *dgate, int64_t ld_dgate, void *dup, int64_t ld_dup,
                               int out_dtype, cudaStream_t s);
 
+// A product of tokens with a quantized matrix (validated), or with the matrix
+// of each slot's expert where `offsets` is given: matrix e begins at row
+// e round_up(rows, 128) and has tensor_scale[e].
+struct GemvLaunch {
+    const void *x;
+    int x_dtype;
+    int64_t tokens, ld_x;
+    const uint8_t *codes, *scales;
+    const float *tensor_scale;
+    int64_t rows, k;              // of a matrix
+    int grid, rht;
+    uint64_t rht_seed;
+    void *y;
+    int y_dtype;
+    int64_t ld_y;
+    const int64_t *offsets;       // first place of each expert
+    const int32_t *src;           // slot at each place
+    int n_experts, topk, gather;  // gather: x is in token order
+    int64_t slots;
+};
+cudaError_t launch_gemv(const GemvLaunch &l, cudaStream_t s);
+
+// A cache of keys and values (ufp4_cache, validated).
+struct CacheHalf {
+    uint8_t *codes, *scales;
+    float *row_scale;
+};
+struct Cache {
+    CacheHalf k, v;
+    int64_t pages;
+    int heads, page_shift, dim, padded, grid, rht;
+    uint64_t rht_seed;
+};
+inline int cache_padded(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+// Rows written (x) or read (y), keys then values, at places `slots`.
+struct CacheRows {
+    Cache cache;
+    const void *x[2];
+    void *y[2];
+    int dtype;
+    int64_t tokens, ld_token[2], ld_head[2];
+    const int64_t *slots;
+};
+cudaError_t launch_cache_append(const CacheRows &l, cudaStream_t s);
+cudaError_t launch_cache_load(const CacheRows &l, cudaStream_t s);
+// Attention of m queries a sequence over the cache.
+struct CacheAttn {
+    Cache cache;
+    const void *q;
+    int q_dtype;
+    int64_t q_token, q_head;
+    int64_t batch;
+    int m, heads;
+    const int32_t *table;
+    int64_t ld_table, width;
+    const int32_t *lens;
+    const uint64_t *mask;
+    float scale;
+    void *out;
+    int out_dtype;
+    int64_t o_token, o_head;
+    float *lse;
+    void *workspace;
+};
+size_t cache_attn_workspace(int64_t batch, int64_t m, int64_t heads, int64_t kv, int64_t padded, int64_t most_keys);
+cudaError_t launch_cache_attn(const CacheAttn &l, cudaStream_t s);
+
 // Reads and clears the sticky flag that a bounded device-side wait raises
 // when it gives up (synchronises s).
 cudaError_t read_timeout_flag(uint32_t *flag, cudaStream_t s);

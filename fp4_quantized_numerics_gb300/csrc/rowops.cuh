@@ -41,17 +41,23 @@ __device__ __forceinline__ uint32_t begin_in_order() {
     return zero;
 }
 template <class... Params, class... Args>
-cudaError_t launch_in_order(void (*kernel)(Params...), uint64_t grid, unsigned block, cudaStream_t s, Args... args) {
+cudaError_t launch_in_order_smem(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem, cudaStream_t s,
+                                 Args... args) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+template <class... Params, class... Args>
+cudaError_t launch_in_order(void (*kernel)(Params...), uint64_t grid, unsigned block, cudaStream_t s, Args... args) {
+    return launch_in_order_smem(kernel, dim3((unsigned)grid), block, 0, s, args...);
 }
 
 // n / d by a multiplication: q = floor(n m / 2^64) with m = ceil(2^64 / d).

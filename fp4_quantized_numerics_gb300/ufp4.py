@@ -21,6 +21,9 @@ The functions carry the C names:
   ufp4_moe_sort(ids, n_experts) -> MoePlan;  ufp4_moe_dispatch / _combine / _combine_bwd
   ufp4_ckpt_save(x, fmt) -> Ckpt;  ufp4_ckpt_load(c) -> tensor
   ufp4_swiglu(gate, up, ...)  -> (h, Ckpt, Ckpt);  ufp4_swiglu_bwd(dh, ...) -> (dgate, dup)
+  ufp4_gemv(x, w), ufp4_gemv_grouped(x, w, plan, rows) -> tensor (unquantized tokens times quantized weights)
+  ufp4_cache_append(k, v, slots, cache);  ufp4_cache_load(cache, slots) -> (k, v)
+  ufp4_cache_attn(q, cache, table, lens, ...) -> tensor, or (tensor, lse)
 """
 import contextlib
 import ctypes
@@ -47,7 +50,8 @@ EXPORTED = ["ufp4_kpad", "ufp4_codes_bytes", "ufp4_scales_bytes", "ufp4_workspac
             "ufp4_gemm_amax", "ufp4_quantize_stats", "ufp4_quantize_grouped_dual", "ufp4_moe_sort",
             "ufp4_moe_dispatch", "ufp4_moe_combine", "ufp4_moe_combine_bwd", "ufp4_ckpt_ld",
             "ufp4_ckpt_codes_bytes", "ufp4_ckpt_scales_bytes", "ufp4_ckpt_save", "ufp4_ckpt_load",
-            "ufp4_swiglu", "ufp4_swiglu_bwd"]
+            "ufp4_swiglu", "ufp4_swiglu_bwd", "ufp4_gemv", "ufp4_gemv_grouped", "ufp4_cache_dim",
+            "ufp4_cache_append", "ufp4_cache_load", "ufp4_cache_attn_workspace_bytes", "ufp4_cache_attn"]
 
 
 class QParamsC(ctypes.Structure):
@@ -86,6 +90,14 @@ class MoePlanC(ctypes.Structure):
 class CkptC(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("cols", ctypes.c_int64), ("format", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class CacheC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "k_row_scale", "v_codes", "v_scales",
+                                               "v_row_scale")] + \
+               [("pages", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("heads", "page", "head_dim", "grid", "rht", "reserved")] + \
+               [("rht_seed", ctypes.c_uint64)]
 
 
 class UFP4Error(RuntimeError):
@@ -156,6 +168,7 @@ def lib():
                                         ctypes.POINTER(GemmGroupC), ctypes.c_int32, vp]
         L.ufp4_gemm_grouped.restype = ctypes.c_int
         i32, plan, ck = ctypes.c_int32, ctypes.POINTER(MoePlanC), ctypes.POINTER(CkptC)
+        u64, qt, cache = ctypes.c_uint64, ctypes.POINTER(QTensorC), ctypes.POINTER(CacheC)
         for name, args in (
                 ("ufp4_moe_sort", [vp, i32, plan, vp]),
                 ("ufp4_moe_dispatch", [vp, i32, i64, i64, plan, vp, i64, vp]),
@@ -164,13 +177,22 @@ def lib():
                 ("ufp4_ckpt_save", [vp, i32, i64, ck, vp]),
                 ("ufp4_ckpt_load", [ck, vp, i32, i64, vp]),
                 ("ufp4_swiglu", [vp, i64, vp, i64, i32, i64, i64, vp, i32, i64, ck, ck, vp]),
-                ("ufp4_swiglu_bwd", [vp, i32, i64, ck, ck, vp, i64, vp, i64, i32, vp])):
+                ("ufp4_swiglu_bwd", [vp, i32, i64, ck, ck, vp, i64, vp, i64, i32, vp]),
+                ("ufp4_gemv", [vp, i32, i64, i64, qt, i32, u64, vp, i32, i64, vp]),
+                ("ufp4_gemv_grouped", [vp, i32, i64, i32, qt, i64, plan, i32, u64, vp, i32, i64, vp]),
+                ("ufp4_cache_append", [vp, vp, i32, i64, i64, i64, i64, i64, vp, cache, vp]),
+                ("ufp4_cache_load", [cache, vp, i64, vp, vp, i32, i64, i64, i64, i64, vp]),
+                ("ufp4_cache_attn", [vp, i32, i64, i64, i64, i32, i32, cache, vp, i64, i64, vp, vp, ctypes.c_float, vp,
+                                     i32, i64, i64, vp, vp, ctypes.c_size_t, vp])):
             f = getattr(L, name)
             f.argtypes, f.restype = args, ctypes.c_int
         for name, args in (("ufp4_ckpt_ld", [i64]), ("ufp4_ckpt_codes_bytes", [i64, i64]),
                            ("ufp4_ckpt_scales_bytes", [i64, i64])):
             f = getattr(L, name)
             f.argtypes, f.restype = args, i64
+        L.ufp4_cache_dim.argtypes, L.ufp4_cache_dim.restype = [i64], i64
+        L.ufp4_cache_attn_workspace_bytes.argtypes = [i64, i32, i32, i64, cache]
+        L.ufp4_cache_attn_workspace_bytes.restype = ctypes.c_size_t
         L.ufp4_status_string.argtypes = [ctypes.c_int]
         L.ufp4_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -904,3 +926,243 @@ def ufp4_swiglu_bwd(dh, keep_gate, keep_up, dtype=None, dgate=None, dup=None, st
     st = lib().ufp4_swiglu_bwd(dp, ddt, dld, kg, ku, gp, gld, up, uld, gdt, s)
     _check(st, "ufp4_swiglu_bwd")
     return dgate, dup
+
+
+# --------------------------------------- answering with a quantized model
+def _tokens(x, name, dev, k):
+    """Checks a 2-D operand of k columns; its pointer, dtype code, row stride and rows."""
+    p, dt, ld, rows, _ = _rows2d(x, name, dev, None, k)
+    return p, dt, ld, rows
+
+
+def _weights(w, dev):
+    if w.codes.get_device() != dev:
+        _same_place(w.codes.get_device(), dev, "w")
+    return ctypes.byref(w.c())
+
+
+def ufp4_gemv(x, w, rht=False, rht_seed=0, dtype=None, out=None, stream=None):
+    """x W^T for a few tokens: x [tokens, k] bf16 or fp32, not quantized, and w
+    a QTensor (rows x k).  rht: w was quantized with that rotation, and x's
+    16-blocks are rotated to match.  Returns [tokens, rows] of `dtype` (x's by
+    default)."""
+    dev = _place(x, "x")
+    xp, dt, ld, tokens = _tokens(x, "x", dev, w.k)
+    wc, (s, on) = _weights(w, dev), _streams(stream, dev)
+    out, yp, ydt, yld = _result(out, "out", tokens, w.rows, dtype, x.dtype, dev, on)
+    st = lib().ufp4_gemv(xp, dt, tokens, ld, wc, 1 if rht else 0, rht_seed, yp, ydt, yld, s)
+    _check(st, "ufp4_gemv")
+    return out
+
+
+def ufp4_gemv_grouped(x, w, plan, rows, gather=False, rht=False, rht_seed=0, dtype=None, out=None, stream=None):
+    """ufp4_gemv by expert, the counts read on the device: w is a grouped
+    row-wise QTensor of n_experts segments of `rows` rows.  x: [tokens * topk,
+    k] in expert order, or with gather=True [tokens, k], each place taking its
+    token's row.  Returns [tokens * topk, rows] in expert order; the rows of
+    dropped slots are zeros."""
+    dev = _place(x, "x")
+    pc, (s, on) = _struct(plan, dev), _streams(stream, dev)
+    slots = plan.tokens * plan.topk
+    xp, dt, ld, _, _ = _rows2d(x, "x", dev, plan.tokens if gather else slots, w.k)
+    wc = _weights(w, dev)
+    if w.tensor_scale.numel() != plan.n_experts:
+        raise ValueError("w must have one tensor scale for each of the plan's %d experts" % plan.n_experts)
+    out, yp, ydt, yld = _result(out, "out", slots, rows, dtype, x.dtype, dev, on)
+    st = lib().ufp4_gemv_grouped(xp, dt, ld, 1 if gather else 0, wc, rows, pc, 1 if rht else 0, rht_seed, yp, ydt, yld,
+                                 s)
+    _check(st, "ufp4_gemv_grouped")
+    return out
+
+
+class Cache:
+    """Keys and values in 4 bits, in pages (layouts: include/ufp4.h): for each,
+    codes uint8 [pages, heads, page, ufp4_cache_dim(head_dim) / 2], scales uint8
+    [pages, heads, page, ufp4_cache_dim(head_dim) / 16] and row_scale fp32
+    [pages, heads, page].  rht: kept rotated, with the signs of rht_seed."""
+
+    def __init__(self, k_codes, k_scales, k_row_scale, v_codes, v_scales, v_row_scale, head_dim, grid, rht=False,
+                 rht_seed=0):
+        _on_gpu(k_codes, "k_codes")
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages, heads, page, width]")
+        pages, heads, page, _ = k_codes.shape
+        dev, pad = k_codes.get_device(), self._pad(head_dim)
+        for t, name, dtype, tail in ((k_codes, "k_codes", torch.uint8, (pad // 2,)),
+                                     (v_codes, "v_codes", torch.uint8, (pad // 2,)),
+                                     (k_scales, "k_scales", torch.uint8, (pad // 16,)),
+                                     (v_scales, "v_scales", torch.uint8, (pad // 16,)),
+                                     (k_row_scale, "k_row_scale", _FLOAT32, ()),
+                                     (v_row_scale, "v_row_scale", _FLOAT32, ())):
+            if t.get_device() != dev:
+                _same_place(t.get_device(), dev, name)
+            if t.dtype is not dtype or t.shape != (pages, heads, page) + tail or not t.is_contiguous():
+                raise ValueError("%s must be contiguous %s %s" % (name, dtype, (pages, heads, page) + tail))
+        self.k_codes, self.k_scales, self.k_row_scale = k_codes, k_scales, k_row_scale
+        self.v_codes, self.v_scales, self.v_row_scale = v_codes, v_scales, v_row_scale
+        self.pages, self.heads, self.page, self.head_dim, self._dev = pages, heads, page, head_dim, dev
+        self.grid, self.rht, self.rht_seed = int(grid), bool(rht), rht_seed
+        self._c = ctypes.byref(CacheC(k_codes.data_ptr(), k_scales.data_ptr(), k_row_scale.data_ptr(),
+                                      v_codes.data_ptr(), v_scales.data_ptr(), v_row_scale.data_ptr(), pages, heads,
+                                      page, head_dim, self.grid, 1 if rht else 0, 0, rht_seed))
+
+    @staticmethod
+    def _pad(head_dim):
+        return 64 if head_dim <= 64 else 128 if head_dim <= 128 else 256
+
+    @classmethod
+    def empty(cls, pages, heads, page, head_dim, grid, rht=False, rht_seed=0, device="cuda"):
+        device, pad = _device(device), cls._pad(head_dim)
+        new = lambda *tail, dtype=torch.uint8: torch.empty((pages, heads, page) + tail, dtype=dtype,  # noqa: E731
+                                                           device=device)
+        return cls(new(pad // 2), new(pad // 16), new(dtype=_FLOAT32), new(pad // 2), new(pad // 16),
+                   new(dtype=_FLOAT32), head_dim, grid, rht, rht_seed)
+
+    @property
+    def device(self):
+        return torch.device("cuda", self._dev)
+
+    def c(self):
+        return self._c
+
+
+def _heads3d(t, name, dev, heads, dim, tokens=None):
+    """Checks a [tokens, heads, dim] tensor with unit stride in its last dim;
+    its pointer, dtype code, token stride, head stride and tokens."""
+    if not isinstance(t, torch.Tensor):
+        _on_gpu(t, name)
+    if t.get_device() != dev:
+        _same_place(t.get_device(), dev, name)
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or (tokens is not None and shape[0] != tokens):
+        raise ValueError("%s must be [%s, %d, %d], got %s" % (name, "tokens" if tokens is None else tokens, heads, dim,
+                                                              tuple(shape)))
+    ld, head, unit = t.stride()
+    if unit != 1:
+        raise ValueError("%s must have unit stride in its last dim" % name)
+    if shape[0] <= 1 and ld < dim:   # (the stride of a single one says nothing)
+        ld = dim
+    if heads == 1 and head < dim:
+        head = dim
+    dt = _DTYPES.get(t.dtype)
+    return t.data_ptr(), _dtype_code(t) if dt is None else dt, ld, head, shape[0]
+
+
+def _slots(slots, dev, tokens=None):
+    if slots.get_device() != dev:
+        _same_place(slots.get_device(), dev, "slots")
+    if slots.dtype is not _INT64 or slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous int64 vector")
+    if tokens is not None and slots.numel() != tokens:
+        raise ValueError("slots must have one place for each of the %d tokens" % tokens)
+    return slots.data_ptr()
+
+
+def _empty3(shape, dtype, dev, on):
+    return _empty((shape[0], shape[1] * shape[2]), dtype, dev, on).view(shape)
+
+
+def ufp4_cache_append(k, v, slots, cache, stream=None):
+    """Quantizes k and v ([tokens, heads, head_dim], bf16 or fp32) into the
+    cache at places slots ([tokens] int64, page number * page + offset, all
+    different); places outside the cache (-1) are skipped."""
+    dev = _place(k, "k")
+    cc, (s, _) = _struct(cache, dev, "cache"), _streams(stream, dev)
+    kp, dt, kld, kh, tokens = _heads3d(k, "k", dev, cache.heads, cache.head_dim)
+    vp, vdt, vld, vh, _ = _heads3d(v, "v", dev, cache.heads, cache.head_dim, tokens)
+    if vdt != dt:
+        raise TypeError("k and v must have one dtype")
+    st = lib().ufp4_cache_append(kp, vp, dt, tokens, kld, kh, vld, vh, _slots(slots, dev, tokens), cc, s)
+    _check(st, "ufp4_cache_append")
+
+
+def ufp4_cache_load(cache, slots, dtype=None, k=None, v=None, stream=None):
+    """The keys and values at places slots, as (k, v), each [tokens, heads,
+    head_dim] of `dtype` (bf16 by default); zeros for places outside the cache.
+    k, v: tensors to write, both or none."""
+    dev = _place(slots, "slots")
+    cc, (s, on) = _struct(cache, dev, "cache"), _streams(stream, dev)
+    sp, shape = _slots(slots, dev), (slots.numel(), cache.heads, cache.head_dim)
+    if (k is None) != (v is None):
+        raise ValueError("give both k and v, or neither")
+    if k is None:
+        dtype = dtype or torch.bfloat16
+        if dtype not in _DTYPES:
+            raise TypeError("k and v must be bf16 or fp32, got %s" % dtype)
+        k, v = _empty3(shape, dtype, dev, on), _empty3(shape, dtype, dev, on)
+    elif k.dtype is not v.dtype or (dtype is not None and k.dtype is not dtype):
+        raise TypeError("k and v must be %s" % (dtype or "of one dtype"))
+    kp, dt, kld, kh, _ = _heads3d(k, "k", dev, cache.heads, cache.head_dim, shape[0])
+    vp, _, vld, vh, _ = _heads3d(v, "v", dev, cache.heads, cache.head_dim, shape[0])
+    st = lib().ufp4_cache_load(cc, sp, shape[0], kp, vp, dt, kld, kh, vld, vh, s)
+    _check(st, "ufp4_cache_load")
+    return k, v
+
+
+def ufp4_cache_attn(q, cache, table, lens, mask=None, scale=None, dtype=None, out=None, lse=None, ws=None,
+                    stream=None):
+    """Attention of each sequence's last m tokens over its rows of the cache.
+    q: [batch * m, heads, head_dim]; table: int32 [batch, width], the pages of
+    each sequence; lens: int32 [batch], the m new tokens included; mask: int64
+    [batch, m], bit r of a token's word set where it sees new token r (None:
+    those up to itself); scale: 1 / sqrt(head_dim) by default.  lse: True or an
+    fp32 [batch * m, heads] to write for the logarithms of the softmax's sums.
+    ws: scratch of ufp4_cache_attn_workspace_bytes(...) (a new one by default).
+    Returns out [batch * m, heads, head_dim] of `dtype` (q's by default), or
+    (out, lse)."""
+    dev = _place(q, "q")
+    cc, (s, on) = _struct(cache, dev, "cache"), _streams(stream, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [batch * m, heads, head_dim]")
+    tokens, heads, dim = q.shape
+    for t, name, dtypes in ((table, "table", _INT32), (lens, "lens", _INT32)):
+        if t.get_device() != dev:
+            _same_place(t.get_device(), dev, name)
+        if t.dtype is not dtypes:
+            raise TypeError("%s must be int32, got %s" % (name, t.dtype))
+    batch = lens.numel()
+    if lens.dim() != 1 or not lens.is_contiguous():
+        raise ValueError("lens must be a contiguous vector")
+    if table.dim() != 2 or table.shape[0] != batch or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError("table must be [batch, width] with unit stride in its last dim")
+    if tokens % batch if batch else tokens:
+        raise ValueError("q must have the same number of tokens for each of the %d sequences" % batch)
+    m = tokens // batch if batch else 1
+    qp, dt, qld, qh, _ = _heads3d(q, "q", dev, heads, cache.head_dim)
+    mp = None
+    if mask is not None:
+        if mask.get_device() != dev:
+            _same_place(mask.get_device(), dev, "mask")
+        if mask.dtype is not _INT64 or mask.shape != (batch, m) or not mask.is_contiguous():
+            raise ValueError("mask must be contiguous int64 [%d, %d]" % (batch, m))
+        mp = mask.data_ptr()
+    if out is None:
+        dtype = dtype or q.dtype
+        if dtype not in _DTYPES:
+            raise TypeError("out must be bf16 or fp32, got %s" % dtype)
+        out = _empty3((tokens, heads, dim), dtype, dev, on)
+    elif dtype is not None and out.dtype is not dtype:
+        raise TypeError("out must be %s, got %s" % (dtype, out.dtype))
+    op, odt, old, oh, _ = _heads3d(out, "out", dev, heads, dim, tokens)
+    lp, want = None, lse is not None and lse is not False
+    if want:
+        if lse is True:
+            lse = _empty((tokens, heads), _FLOAT32, dev, on)
+        elif lse.get_device() != dev:
+            _same_place(lse.get_device(), dev, "lse")
+        if lse.dtype is not _FLOAT32 or lse.shape != (tokens, heads) or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous fp32 [%d, %d]" % (tokens, heads))
+        lp = lse.data_ptr()
+    L, width = lib(), table.shape[1]
+    if ws is None:
+        need = L.ufp4_cache_attn_workspace_bytes(batch, m, heads, width, cc)
+        ws = _empty((need,), torch.uint8, dev, on) if need else None
+    elif ws.get_device() != dev:
+        _same_place(ws.get_device(), dev, "ws")
+    st = L.ufp4_cache_attn(qp, dt, qld, qh, batch, m, heads, cc, table.data_ptr(),
+                           table.stride(0) if batch > 1 else max(width, 1), width, lens.data_ptr(), mp,
+                           dim ** -0.5 if scale is None else scale, op, odt, old, oh, lp,
+                           None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
+                           s)
+    _check(st, "ufp4_cache_attn")
+    return (out, lse) if want else out

@@ -546,6 +546,145 @@ UFP4_API ufp4_status ufp4_swiglu_bwd(const void *dh, int32_t dh_dtype, int64_t l
                                      const ufp4_ckpt *up, void *dgate, int64_t ld_dgate, void *dup,
                                      int64_t ld_dup, int32_t out_dtype, ufp4_stream_t stream);
 
+/* ---------------------------------------------------------------------
+ * Answering with a quantized model: a few unquantized tokens times quantized
+ * weights, and the attention of new tokens over keys and values kept in 4
+ * bits.  The pages train models ([ZC] "The fix -- UFP4"; [HP] technical
+ * approach); how one is run afterwards is left open, and the definitions here
+ * are this library's.
+ *
+ * Conventions of the calls in this section, beside those at the top:
+ *   - Unquantized tensors are BF16 or FP32 (`*_dtype`), their last dimension
+ *     contiguous, with any other strides >= the extents they step over, in
+ *     elements, aligned to one element.  Rows at addresses and strides that are
+ *     multiples of 16 bytes (32: cache rows) are the fastest; others give the
+ *     same results.
+ *   - Sums are fp32; each result element is rounded once, when written.
+ *   - Inputs and outputs must not overlap.
+ *   - Results do not depend on timing (no floating-point atomics).
+ *   - Grids: UFP4_E2M1, UFP4_E1M2, UFP4_E2M1C; UFP4_MXFP4 returns
+ *     UFP4_ERR_UNSUPPORTED.
+ *   - Everything that depends on the batch (plans, tables, lengths, slots) is
+ *     device data: a step can be captured in a CUDA graph and replayed with
+ *     other contents. */
+
+/* y = x W^T for a few tokens: y[t][n] = sum over k of x'[t][k] W[n][k], with W
+ * the values that w stands for (v e S) and x' = x, or, with rht = 1, every
+ * 16-block of x rotated by (1/4) H16 diag(d) with the signs of rht_seed: what
+ * goes with weights quantized with rht = 1 and that seed.  x is not quantized:
+ * a BF16 element not rotated enters exactly, one rotated or FP32 within 2^-22
+ * of itself, each down to 2^-29 of the largest among the 128 it lies with.
+ * Made for 1 to 32 tokens; further ones read w once more per 32.
+ *   x : tokens x w->k;  y : tokens x w->rows.  w->k <= UFP4_MAX_WIDTH.
+ * w->k = 0 writes zeros.  w->eplane is not read. */
+UFP4_API ufp4_status ufp4_gemv(const void *x, int32_t x_dtype, int64_t tokens, int64_t ld_x, const ufp4_qtensor *w,
+                               int32_t rht, uint64_t rht_seed, void *y, int32_t y_dtype, int64_t ld_y,
+                               ufp4_stream_t stream);
+
+/* ufp4_gemv by expert, for a routed batch whose counts stay on the device
+ * (ufp4_gemm_grouped takes them from the host): for every place p of the
+ * plan's expert order, with e its expert,
+ *   y[p][n] = sum over k of x'[r][k] W_e[n][k],   n < rows,
+ * r = p, or, with gather = 1, the token of the place's slot (x as it was before
+ * ufp4_moe_dispatch).  The rows of dropped slots are written as zeros.
+ *   w : the row-wise grouped layout of n_experts segments of `rows` rows each:
+ *       matrix e from row e * round_up(rows, 128), tensor_scale[e];
+ *       w->rows = n_experts * round_up(rows, 128).
+ *   x : (tokens * topk) x w->k, or tokens x w->k with gather = 1;
+ *   y : (tokens * topk) x rows. */
+UFP4_API ufp4_status ufp4_gemv_grouped(const void *x, int32_t x_dtype, int64_t ld_x, int32_t gather,
+                                       const ufp4_qtensor *w, int64_t rows, const ufp4_moe_plan *plan, int32_t rht,
+                                       uint64_t rht_seed, void *y, int32_t y_dtype, int64_t ld_y,
+                                       ufp4_stream_t stream);
+
+/* Keys and values of past tokens in 4 bits, in pages.  A row is one token's
+ * key or value of one head, head_dim elements; it is quantized by itself as
+ * ufp4_quantize does a tensor of one row (round to nearest even): its largest
+ * magnitude A gives its own fp32 scale A / (448 qmax), and every 16 elements
+ * share an E4M3 scale.  With rht = 1, K and V are kept rotated (16-blocks along
+ * head_dim, the signs of rht_seed).  A row that holds a NaN or an infinity has
+ * the scale NaN and is restored as NaN throughout.
+ *   Place s = p * page + o is offset o of page p, 0 <= s < pages * page; its
+ *   row for head h is row (p * heads + h) * page + o of
+ *     k_codes, v_codes  : [pages][heads][page][ufp4_cache_dim(head_dim) / 2]
+ *                         bytes, packed as in ufp4_qtensor, elements past
+ *                         head_dim 0;
+ *     k_scales, v_scales: [pages][heads][page][ufp4_cache_dim(head_dim) / 16]
+ *                         E4M3 bytes;
+ *     k_row_scale, v_row_scale: [pages][heads][page] fp32;
+ *   all 16-byte aligned.
+ *   page: a power of two, 16 to 32768; head_dim: a multiple of 16, 16 to 256;
+ *   ufp4_cache_dim is head_dim rounded up to 64, 128 or 256. */
+typedef struct {
+    uint8_t *k_codes;
+    uint8_t *k_scales;
+    float *k_row_scale;
+    uint8_t *v_codes;
+    uint8_t *v_scales;
+    float *v_row_scale;
+    int64_t pages;
+    int32_t heads;
+    int32_t page;
+    int32_t head_dim;
+    int32_t grid;
+    int32_t rht;
+    int32_t reserved;          /* must be 0 */
+    uint64_t rht_seed;
+} ufp4_cache;
+
+UFP4_API int64_t ufp4_cache_dim(int64_t head_dim);
+
+/* Quantizes the keys and values of `tokens` tokens into the cache: token i at
+ * place slots[i] (device int64; one outside the cache, such as -1, is skipped:
+ * padding).  The places of one call differ from one another; what two tokens
+ * leave at one place is unspecified.  Other places keep what they hold.
+ *   k, v: [tokens][heads][head_dim] of `dtype`, strides ld_* (tokens) and
+ *   head_* (heads). */
+UFP4_API ufp4_status ufp4_cache_append(const void *k, const void *v, int32_t dtype, int64_t tokens, int64_t ld_k,
+                                       int64_t head_k, int64_t ld_v, int64_t head_v, const int64_t *slots,
+                                       const ufp4_cache *cache, ufp4_stream_t stream);
+
+/* The values at places slots[0 .. tokens), rotated back where rht = 1, as
+ * k, v: [tokens][heads][head_dim] of `dtype`; zeros for a place outside the
+ * cache.  A place may be asked for more than once. */
+UFP4_API ufp4_status ufp4_cache_load(const ufp4_cache *cache, const int64_t *slots, int64_t tokens, void *k, void *v,
+                                     int32_t dtype, int64_t ld_k, int64_t head_k, int64_t ld_v, int64_t head_v,
+                                     ufp4_stream_t stream);
+
+#define UFP4_MAX_NEW 64
+
+/* Attention of each sequence's last m tokens over its rows of the cache:
+ *   out[b m + i][h] = sum over j of p_j V[j],  p = softmax(scale q . K[j]),
+ * over the positions j < lens[b] that token i sees, K and V of cache head
+ * h / (heads / cache->heads).  The m new tokens (already appended) are the last
+ * m positions; token i sees every position before them, and among them those
+ * whose bits mask[b m + i] has (bit r: position lens[b] - m + r), by which they
+ * may form a tree of drafts; with mask = NULL those up to itself.  A token that
+ * sees nothing (a sequence of length 0, say) gets zeros.  Rows that no token
+ * of the sequence sees need not have been written.
+ *   q, out : [batch * m][heads][head_dim], strides ld_* and head_*;
+ *   table  : int32 [batch][width], row stride ld_table: position j of sequence
+ *            b is at offset j % page of page table[b][j / page].  Entries past
+ *            a sequence's length are not used; a page outside the cache reads
+ *            as rows of zeros;
+ *   lens   : int32 [batch], the new tokens included; held to 0 .. width * page;
+ *   mask   : uint64 [batch * m] or NULL;
+ *   lse    : fp32 [batch * m][heads], log of the sum of exp(scale q . K[j])
+ *            (-infinity where nothing is seen), or NULL;
+ *   workspace: ufp4_cache_attn_workspace_bytes(...) bytes, 16-byte aligned, of
+ *            this call until it has run (NULL where that is 0).
+ * heads a multiple of cache->heads; m 1 .. UFP4_MAX_NEW; width * page < 2^31.
+ * Scores are fp32 of q as ufp4_gemv takes x; the probabilities enter the sum
+ * over V as FP16 relative to the largest of their row scales (11 bits; 22 where
+ * out is FP32). */
+UFP4_API size_t ufp4_cache_attn_workspace_bytes(int64_t batch, int32_t m, int32_t heads, int64_t width,
+                                                const ufp4_cache *cache);
+UFP4_API ufp4_status ufp4_cache_attn(const void *q, int32_t q_dtype, int64_t ld_q, int64_t head_q, int64_t batch,
+                                     int32_t m, int32_t heads, const ufp4_cache *cache, const int32_t *table,
+                                     int64_t ld_table, int64_t width, const int32_t *lens, const uint64_t *mask,
+                                     float scale, void *out, int32_t out_dtype, int64_t ld_out, int64_t head_out,
+                                     float *lse, void *workspace, size_t workspace_bytes, ufp4_stream_t stream);
+
 /* Quality of one quantization, in fp64 on the host ([ZC] "The cause",
  * "Compounding decay", "The RHT paradox").  A is the tensor that was
  * quantized (x, rotated when p->rht; transposed when p->colwise):
