@@ -183,8 +183,11 @@ struct AttnArgs {
 
 constexpr int kAttnWarps = 4, kTileKeys = 32, kSplitKeys = 128;   // a split's keys are a multiple of the last
 
-__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool real) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(real ? 16 : 0) : "memory");
+// 2^x, within 2 units in the last place; 0 below 2^-126.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
@@ -192,8 +195,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     return d;
 }
 // Keys [first, last) of a sequence of `len` that split s of n takes.
+__device__ __forceinline__ int split_keys(int len, int n) {
+    return max((len + n - 1) / n + kSplitKeys - 1, kSplitKeys) / kSplitKeys * kSplitKeys;
+}
 __device__ __forceinline__ void split_range(int len, int s, int n, int &first, int &last) {
-    const int per = ((len + n - 1) / n + kSplitKeys - 1) / kSplitKeys * kSplitKeys;
+    const int per = split_keys(len, n);
     first = (int)min((int64_t)s * per, (int64_t)len);
     last = min(first + per, len);
 }
@@ -246,12 +252,13 @@ __device__ __forceinline__ void finish_row(const AttnArgs &a, float (&o)[8], flo
 
 // DC: 64-element pieces of a padded row (1, 2 or 4); NT: groups of 8 queries.
 template <int GRID, int DC, int NT>
-__global__ void __launch_bounds__(kAttnWarps * 32) k_attn(AttnArgs a) {
+__global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k_attn(AttnArgs a) {
     constexpr int kDim = 64 * DC, kQ = 8 * NT, kRow = kDim / 2, kBlocks = kDim / 16;
-    constexpr int kStages = DC == 4 ? 2 : 3;
     constexpr int kCodes = kTileKeys * kRow, kScales = kTileKeys * kBlocks, kRs = kTileKeys * 4;
     constexpr int kStage = 2 * (kCodes + kScales + kRs);
-    // a stage: codes, scales and row scales of the keys, then of the values
+    // a stage: codes and scales of the keys, row scales of keys and values,
+    // codes and scales of the values
+    constexpr int kKeyRs = kCodes + kScales, kValRs = kKeyRs + kRs, kVal = kValRs + kRs;
     extern __shared__ __align__(16) uint8_t smem[];
     uint4 *qs = reinterpret_cast<uint4 *>(smem);                       // [2][2 DC][kQ][4] x 16 bytes
     float *qf = reinterpret_cast<float *>(qs + 2 * 2 * DC * kQ * 4);   // [kQ]
@@ -270,63 +277,70 @@ __global__ void __launch_bounds__(kAttnWarps * 32) k_attn(AttnArgs a) {
     const int q0 = qt * kQ, nq = min(a.group * a.m - q0, kQ);
 
     // ---- the rows' copies
-    uint8_t *my = stages + warp * kStages * kStage;
+    uint8_t *my = stages + warp * 2 * kStage;
     const uint32_t my_s = (uint32_t)__cvta_generic_to_shared(my);
     const int tiles = (last - first + kTileKeys - 1) / kTileKeys;
     const int32_t *table = a.table + b * a.ld_table;
-    const auto page_of = [&](int tile, int half) -> int {
-        const int pos = first + tile * kTileKeys + half * 16;
-        return tile < tiles && pos < last ? table[zero + (pos >> a.page_shift)] : -1;
+    int next[2];                                      // pages of the next tile's two halves
+    const auto look = [&](int tile) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int pos = first + tile * kTileKeys + h * 16;
+            next[h] = tile < tiles && pos < last ? table[zero + (pos >> a.page_shift)] : -1;
+        }
     };
-    int next[2];
-    const auto copy = [&](int tile, int slot) {
+    int64_t row[2];                                   // the cache's rows of the tile being copied
+    bool real[2];
+    const auto copy_keys = [&](int tile, int slot) {
         const uint32_t to = my_s + slot * kStage;
-        int64_t row[2];
-        bool real[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int pos = first + tile * kTileKeys + h * 16;
             real[h] = next[h] >= 0 && next[h] < a.pages;
-            row[h] = real[h] ? cache_row(((int64_t)next[h] << a.page_shift) + (pos & ((1 << a.page_shift) - 1)), kvh,
-                                         a.kv, a.page_shift)
-                             : 0;
+            row[h] = real[h] ? (((int64_t)next[h] * a.kv + kvh) << a.page_shift) + (pos & ((1 << a.page_shift) - 1)) : 0;
         }
         if (tile < tiles) {
 #pragma unroll
             for (int j = 0; j < 2 * DC; ++j) {
                 const int h = j / DC;
-                const int64_t at = row[h] * kRow + ((j % DC) * 32 + lane) * 16;
-                copy16(to + (j * 32 + lane) * 16, a.k.codes + at, real[h]);
-                copy16(to + kStage / 2 + (j * 32 + lane) * 16, a.v.codes + at, real[h]);
+                copy16(to + (j * 32 + lane) * 16, a.k.codes + row[h] * kRow + ((j % DC) * 32 + lane) * 16, real[h]);
             }
-#pragma unroll
-            for (int j = 0; j < (16 * DC + 31) / 32; ++j) {
-                const int i = j * 32 + lane;                     // values: the upper half of 16 DC pieces
-                if (i < 16 * DC) {
-                    const int h = i / (4 * DC) % 2, v = i / (8 * DC);
-                    const int64_t at = (h ? row[1] : row[0]) * kBlocks + i % (4 * DC) * 16;
-                    copy16(to + v * (kStage / 2) + kCodes + i % (8 * DC) * 16, (v ? a.v.scales : a.k.scales) + at,
-                           h ? real[1] : real[0]);
-                }
+            if (lane < 8 * DC) {
+                const int h = lane / (4 * DC);
+                copy16(to + kCodes + lane * 16, a.k.scales + (h ? row[1] : row[0]) * kBlocks + lane % (4 * DC) * 16,
+                       h ? real[1] : real[0]);
             }
             if (lane < 16) {
-                const int h = lane / 4 % 2, v = lane / 8;
-                copy16(to + v * (kStage / 2) + kCodes + kScales + lane % 8 * 16,
-                       (v ? a.v.row_scale : a.k.row_scale) + (h ? row[1] : row[0]) + lane % 4 * 4,
+                const int h = lane / 4 % 2;
+                copy16(to + kKeyRs + lane * 16,
+                       (lane < 8 ? a.k.row_scale : a.v.row_scale) + (h ? row[1] : row[0]) + lane % 4 * 4,
                        h ? real[1] : real[0]);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const auto look = [&](int tile) {
-        next[0] = page_of(tile, 0);
-        next[1] = page_of(tile, 1);
+    const auto copy_values = [&](int tile, int slot) {
+        const uint32_t to = my_s + slot * kStage + kVal;
+        if (tile < tiles) {
+#pragma unroll
+            for (int j = 0; j < 2 * DC; ++j) {
+                const int h = j / DC;
+                copy16(to + (j * 32 + lane) * 16, a.v.codes + row[h] * kRow + ((j % DC) * 32 + lane) * 16, real[h]);
+            }
+            if (lane < 8 * DC) {
+                const int h = lane / (4 * DC);
+                copy16(to + kCodes + lane * 16, a.v.scales + (h ? row[1] : row[0]) * kBlocks + lane % (4 * DC) * 16,
+                       h ? real[1] : real[0]);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
     look(warp);
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-        copy(warp + s * kAttnWarps, s);
-        look(warp + (s + 1) * kAttnWarps);
+    for (int i = 0; i < 2; ++i) {
+        copy_keys(warp + i * kAttnWarps, i);
+        copy_values(warp + i * kAttnWarps, i);
+        look(warp + (i + 1) * kAttnWarps);
     }
 
     // ---- the queries as operands: [plane][word of a lane's elements][query][lane % 4]
@@ -362,9 +376,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32) k_attn(AttnArgs a) {
             }
             if (a.rht) rotate16(v, signs);
         }
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) top = max(top, finite_bits(v[j]));
+        uint32_t top = top_bits(v);
 #pragma unroll
         for (int d = 1; d < kBlocks; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         const int e = top_exponent(top);
@@ -396,6 +408,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32) k_attn(AttnArgs a) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
     int ve = -110;                                   // exponent of the largest row scale of the values
+    uint32_t vmost = __float_as_uint(exp2i(-110)) | 0x7FFFFFu;
     float qscale[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -404,32 +417,29 @@ __global__ void __launch_bounds__(kAttnWarps * 32) k_attn(AttnArgs a) {
     }
 
     int slot = 0;
-    for (int tile = warp; tile < tiles; tile += kAttnWarps) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    for (int tile = warp; tile < tiles; tile += kAttnWarps, slot ^= 1) {
+        // (after these keys, the tile's values and the next tile's two groups are under way)
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
         __syncwarp();
-        {
-            const int ahead = tile + (kStages - 1) * kAttnWarps;
-            copy(ahead, slot == 0 ? kStages - 1 : slot - 1);
-            look(ahead + kAttnWarps);
-        }
-        uint8_t *ks = my + slot * kStage, *vs = ks + kStage / 2;
-        slot = slot + 1 == kStages ? 0 : slot + 1;
+        uint8_t *const ks = my + slot * kStage, *const vs = ks + kVal;
         const int pos0 = first + tile * kTileKeys;
         const bool edge = pos0 + kTileKeys > len - (a.m > 1 || a.mask ? a.m : 0);
-        if (edge) {
-            // rows that nobody sees may never have been written: their scales
-            // become zero, so that whatever codes stand there count for nothing
-            const int pos = pos0 + lane, rel = pos - (len - a.m);
-            if (pos >= last || (rel >= 0 && !(seen >> rel & 1))) {
+        // rows that nobody sees may never have been written: their scales
+        // become zero, so that whatever codes stand there count for nothing
+        const int lane_rel = pos0 + lane - (len - a.m);
+        const bool unseen = edge && (pos0 + lane >= last || (lane_rel >= 0 && !(seen >> lane_rel & 1)));
+        const auto blank = [&](uint8_t *scales) {
+            if (unseen)
 #pragma unroll
-                for (int j = 0; j < kBlocks / 4; ++j) {
-                    reinterpret_cast<uint32_t *>(ks + kCodes + lane * kBlocks)[j] = 0;
-                    reinterpret_cast<uint32_t *>(vs + kCodes + lane * kBlocks)[j] = 0;
-                }
-                reinterpret_cast<float *>(ks + kCodes + kScales)[lane] = 0.0f;
-                reinterpret_cast<float *>(vs + kCodes + kScales)[lane] = 0.0f;
-            }
+                for (int j = 0; j < kBlocks / 4; ++j) reinterpret_cast<uint32_t *>(scales + lane * kBlocks)[j] = 0;
             __syncwarp();
+        };
+        if (edge) {
+            if (unseen) {
+                reinterpret_cast<float *>(ks + kKeyRs)[lane] = 0.0f;
+                reinterpret_cast<float *>(ks + kValRs)[lane] = 0.0f;
+            }
+            blank(ks + kCodes);
         }
 
         // ---- scores: keys 16 i + g (and + 8) by queries 8 n + 2 t (and + 1)
@@ -481,9 +491,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32) k_attn(AttnArgs a) {
         float krs[4], vrs[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            krs[r] = reinterpret_cast<const float *>(ks + kCodes + kScales)[8 * r + g];
-            vrs[r] = reinterpret_cast<const float *>(vs + kCodes + kScales)[8 * r + g];
+            krs[r] = reinterpret_cast<const float *>(ks + kKeyRs)[8 * r + g];
+            vrs[r] = reinterpret_cast<const float *>(ks + kValRs)[8 * r + g];
         }
+        __syncwarp();
+        copy_keys(tile + 2 * kAttnWarps, slot);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -505,42 +517,66 @@ __global__ void __launch_bounds__(kAttnWarps * 32) k_attn(AttnArgs a) {
                 }
         }
 
-        // ---- running maximum and sum; weights of the values
-        const uint32_t vtop = __reduce_max_sync(0xffffffffu, max(max(finite_bits(vrs[0]), finite_bits(vrs[1])),
-                                                                 max(finite_bits(vrs[2]), finite_bits(vrs[3]))));
-        const int ve_new = max(ve, top_exponent(vtop));
-        const float v_back = ve_new == ve ? 1.0f : exp2f((float)(ve - ve_new));
-        ve = ve_new;
-        const float vup = exp2i(14 - ve);
+        // ---- running maximum and sum; weights of the values.  The maximum
+        // follows the scores when one passes it by more than 2^3: until then
+        // probabilities are up to 8, and times 2^(11 - ve) of their row scales
+        // below 2^15.
+        float top[NT][2];
+        bool rise = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                top[n][c] = fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c]));
+                rise |= top[n][c] > mx[n][c] + 3.0f;
+            }
+        const uint32_t vtop = max(max(finite_bits(vrs[0]), finite_bits(vrs[1])),
+                                  max(finite_bits(vrs[2]), finite_bits(vrs[3])));
+        rise |= vtop > vmost;
+        if (__any_sync(0xffffffffu, rise)) {
+            const int ve_new = max(ve, top_exponent(__reduce_max_sync(0xffffffffu, vtop)));
+            const float v_back = exp2f((float)(ve - ve_new));
+            ve = ve_new;
+            vmost = __float_as_uint(exp2i(ve)) | 0x7FFFFFu;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v = top[n][c];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                    v = fmaxf(v, mx[n][c]);
+                    const float back = exp2f(mx[n][c] - (v == -INFINITY ? 0.0f : v));
+                    mx[n][c] = v;
+                    l[n][c] *= back;
+#pragma unroll
+                    for (int i = 0; i < 4 * DC; ++i) {
+                        o[i][n][c] *= back * v_back;
+                        o[i][n][2 + c] *= back * v_back;
+                    }
+                }
+        }
+        const float vup = exp2i(11 - ve);
 #pragma unroll
         for (int r = 0; r < 4; ++r) vrs[r] *= vup;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float top = fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c]));
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                top = fmaxf(top, mx[n][c]);
-                const float base = top == -INFINITY ? 0.0f : top;
-                const float back = exp2f(mx[n][c] - base);
-                mx[n][c] = top;
-                l[n][c] *= back;
-                const float ob = back * v_back;
-#pragma unroll
-                for (int i = 0; i < 4 * DC; ++i) {
-                    o[i][n][c] *= ob;
-                    o[i][n][2 + c] *= ob;
-                }
+                const float base = mx[n][c] == -INFINITY ? 0.0f : mx[n][c];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     float &x = s[r / 2][n][(r & 1) * 2 + c];
                     const bool hidden = x == -INFINITY;
-                    const float p = exp2f(x - base);
+                    const float p = exp2_fast(x - base);
                     l[n][c] += p;
                     x = hidden ? 0.0f : p * vrs[r];
                 }
             }
+
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+        __syncwarp();
+        if (edge) blank(vs + kCodes);
 
         // ---- values: elements of key 16 i + 2 t, + 1, + 8, + 9
 #pragma unroll
@@ -594,6 +630,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32) k_attn(AttnArgs a) {
                 }
             }
         }
+        __syncwarp();
+        copy_values(tile + 2 * kAttnWarps, slot);
+        look(tile + 3 * kAttnWarps);
     }
 
     // ---- the warps' parts together, in the stages' memory
@@ -601,7 +640,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32) k_attn(AttnArgs a) {
     __syncthreads();
     float *po = reinterpret_cast<float *>(stages);                 // [warp][query][kDim]
     float *pm = po + kAttnWarps * kQ * kDim, *pl = pm + kAttnWarps * kQ;
-    const float down = exp2i(ve - 14) * kDecoded<GRID>;
+    const float down = exp2i(ve - 11) * kDecoded<GRID>;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -654,64 +693,101 @@ __global__ void __launch_bounds__(kAttnWarps * 32) k_attn(AttnArgs a) {
     }
 }
 
-// Joins the splits' parts, a warp a query.
-__global__ void __launch_bounds__(128) k_attn_join(AttnArgs a, int kdim) {
+// Joins the splits' parts: W warps a query (of 8 in a CTA), each some of its
+// parts, in a fixed order.
+template <int W>
+__global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, int kdim) {
+    __shared__ float part[8][256 + 1];
     const uint32_t zero = begin_in_order();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % W;
     const int64_t queries = (int64_t)a.batch * a.kv * a.group * a.m;
-    const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (r >= queries) return;
-    const int per = a.group * a.m;
-    const int bh = (int)(r / per), q = (int)(r % per), kvh = bh % a.kv, b = bh / a.kv;
-    const int len = min(max(a.lens[zero + b], 0), a.width << a.page_shift);
+    const int64_t r = (int64_t)blockIdx.x * (8 / W) + warp / W;
     float top = -INFINITY, sum = 0.0f, v[8] = {};
-    int parts = 0;
-    for (int s = 0; s < a.splits; ++s) {
-        int first, last;
-        split_range(len, s, a.splits, first, last);
-        if (first < last) parts = s + 1;
-    }
-    for (int s = lane; s < parts; s += 32) top = fmaxf(top, a.part_m[s * queries + r + zero]);
+    int bh = 0, q = 0;
+    if (r < queries) {
+        const int per = a.group * a.m;
+        bh = (int)(r / per);
+        q = (int)(r % per);
+        const int len = min(max(a.lens[zero + bh / a.kv], 0), a.width << a.page_shift);
+        const int keys = split_keys(len, a.splits), parts = (len + keys - 1) / keys;
+        for (int s = lane; s < parts; s += 32) top = fmaxf(top, a.part_m[s * queries + r + zero]);
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const float base = top == -INFINITY ? 0.0f : top;
+        for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
-        const float f = exp2f(a.part_m[s * queries + r + zero] - base);
-        sum += a.part_l[s * queries + r + zero] * f;
-        if (lane * 8 < kdim) {
-            const float4 *from = reinterpret_cast<const float4 *>(a.part_o + (s * queries + r + zero) * kdim + lane * 8);
-            const float4 x = from[0], y = from[1];
-            v[0] += x.x * f; v[1] += x.y * f; v[2] += x.z * f; v[3] += x.w * f;
-            v[4] += y.x * f; v[5] += y.y * f; v[6] += y.z * f; v[7] += y.w * f;
+        for (int s = mine; s < parts; s += W) {
+            const float f = exp2f(a.part_m[s * queries + r + zero] - base);
+            sum += a.part_l[s * queries + r + zero] * f;
+            if (lane * 8 < kdim) {
+                const float4 *from =
+                    reinterpret_cast<const float4 *>(a.part_o + (s * queries + r + zero) * kdim + lane * 8);
+                const float4 x = from[0], y = from[1];
+                v[0] += x.x * f; v[1] += x.y * f; v[2] += x.z * f; v[3] += x.w * f;
+                v[4] += y.x * f; v[5] += y.y * f; v[6] += y.z * f; v[7] += y.w * f;
+            }
         }
     }
-    finish_row(a, v, top, sum, b, q, kvh, lane);
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[warp][i * 32 + lane] = v[i];
+        if (lane == 0) part[warp][256] = sum;
+        __syncthreads();
+        if (mine) return;
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+            sum += part[warp + w][256];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += part[warp + w][i * 32 + lane];
+        }
+    }
+    if (r < queries) finish_row(a, v, top, sum, bh / a.kv, q, bh % a.kv, lane);
+}
+cudaError_t join(const AttnArgs &a, int kdim, cudaStream_t s) {
+    const int64_t queries = (int64_t)a.batch * a.kv * a.group * a.m;
+    const auto with = [&](auto w) {
+        constexpr int W = decltype(w)::value, per = 8 / W;
+        return launch_in_order(k_attn_join<W>, (uint64_t)(queries + per - 1) / per, 256, s, a, kdim);
+    };
+    return a.splits <= 8 ? with(Int<1>()) : a.splits <= 32 ? with(Int<4>()) : with(Int<8>());
 }
 
-// CTAs that keep the card busy; a split has 256 keys at least.
-int splits_of(int64_t batch, int64_t kv, int64_t qtiles, int64_t most_keys) {
-    const int64_t ctas = batch * kv * qtiles, want = 3 * (int64_t)num_sms();
-    int64_t s = (want + ctas - 1) / ctas;
-    s = std::min(s, (most_keys + 255) / 256);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(s, 512));
+// The kernel's query groups, and how many of its CTAs share an SM.
+struct Shape {
+    int nt, qtiles, resident;
+};
+Shape shape_of(int64_t queries, int64_t padded) {
+    const int nt = queries <= 8 || padded > 128 ? 1 : 2;
+    return Shape{nt, (int)((queries + 8 * nt - 1) / (8 * nt)), nt == 1 && padded <= 128 ? 4 : 2};
 }
-int query_tiles(int64_t queries) { return queries <= 8 ? 1 : (int)((queries + 15) / 16); }
+// Splits of a sequence: what makes an SM's CTAs times the keys of one, and its
+// start and end (about 64 keys' time), the least; fewer CTAs than share an SM
+// leave it idle, and every split is read again when they are joined.
+int splits_of(int64_t batch, int64_t kv, const Shape &shape, int64_t most_keys) {
+    const int64_t ctas = batch * kv * shape.qtiles, sms = num_sms();
+    int64_t best = 1, least = INT64_MAX;
+    for (int64_t s = 1; s <= 512 && (s == 1 || (s - 1) * kSplitKeys < most_keys); ++s) {
+        const int64_t keys = (most_keys + s * kSplitKeys - 1) / (s * kSplitKeys) * kSplitKeys;
+        const int64_t cost = std::max<int64_t>((ctas * s + sms - 1) / sms, shape.resident) * (keys + 64) + 6 * s;
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return (int)best;
+}
 
 template <int GRID, int DC, int NT>
 cudaError_t attn(const AttnArgs &a, cudaStream_t s) {
     constexpr int kDim = 64 * DC, kQ = 8 * NT;
-    constexpr int kStages = DC == 4 ? 2 : 3;
     constexpr size_t kStage = 2 * (kTileKeys * (kDim / 2) + kTileKeys * (kDim / 16) + kTileKeys * 4);
     constexpr size_t parts = kAttnWarps * kQ * (kDim + 2) * sizeof(float);
-    constexpr size_t bytes = 2 * 2 * DC * kQ * 4 * 16 + kQ * 12 + std::max(kAttnWarps * kStages * kStage, parts);
+    constexpr size_t bytes = 2 * 2 * DC * kQ * 4 * 16 + kQ * 12 + std::max(kAttnWarps * 2 * kStage, parts);
     cudaError_t e = cudaFuncSetAttribute(k_attn<GRID, DC, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
     e = launch_in_order_smem(k_attn<GRID, DC, NT>, dim3((unsigned)(a.batch * a.kv * a.qtiles), (unsigned)a.splits),
                              kAttnWarps * 32, bytes, s, a);
     if (e != cudaSuccess || a.splits == 1) return e;
-    const int64_t queries = (int64_t)a.batch * a.kv * a.group * a.m;
-    return launch_in_order(k_attn_join, (uint64_t)(queries + 3) / 4, 128, s, a, kDim);
+    return join(a, kDim, s);
 }
 
 template <class F>
@@ -774,7 +850,7 @@ cudaError_t launch_cache_load(const CacheRows &l, cudaStream_t s) {
 
 size_t cache_attn_workspace(int64_t batch, int64_t m, int64_t heads, int64_t kv, int64_t padded, int64_t most_keys) {
     const int64_t queries = heads / kv * m;
-    const int64_t splits = splits_of(batch, kv, query_tiles(queries), most_keys);
+    const int64_t splits = splits_of(batch, kv, shape_of(queries, padded), most_keys);
     return splits == 1 ? 0 : (size_t)(splits * batch * m * heads * (padded + 2)) * sizeof(float);
 }
 
@@ -809,15 +885,18 @@ cudaError_t launch_cache_attn(const CacheAttn &l, cudaStream_t s) {
     a.out_fp32 = a.two_p = l.out_dtype == 1;
     a.lse = l.lse;
     const int64_t queries = (int64_t)a.group * a.m;
-    a.qtiles = query_tiles(queries);
-    a.splits = splits_of(a.batch, a.kv, a.qtiles, l.width << a.page_shift);
+    const Shape shape = shape_of(queries, l.cache.padded);
+    a.qtiles = shape.qtiles;
+    a.splits = splits_of(a.batch, a.kv, shape, l.width << a.page_shift);
     const int64_t all = (int64_t)a.batch * a.kv * queries * a.splits;
     a.part_o = static_cast<float *>(l.workspace);
     a.part_m = a.part_o + all * l.cache.padded;
     a.part_l = a.part_m + all;
     const auto with = [&](auto gr, auto dc) {
         constexpr int G = decltype(gr)::value, D = decltype(dc)::value;
-        return queries <= 8 ? attn<G, D, 1>(a, s) : attn<G, D, 2>(a, s);
+        if constexpr (D <= 2)
+            if (shape.nt == 2) return attn<G, D, 2>(a, s);
+        return attn<G, D, 1>(a, s);
     };
     const auto by_dim = [&](auto gr) {
         return l.cache.padded == 64 ? with(gr, Int<1>()) : l.cache.padded == 128 ? with(gr, Int<2>()) : with(gr, Int<4>());

@@ -85,6 +85,12 @@ __device__ __forceinline__ uint32_t f16_rest(float a, float b, uint32_t h) {
     return f16_pair(isinf(f.x) ? 0.0f : a - f.x, isinf(f.y) ? 0.0f : b - f.y);
 }
 
+// 16 bytes to shared memory without a register (zeros where `real` is false,
+// and nothing is read).
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(real ? 16 : 0) : "memory");
+}
+
 // D += A B: A 16 x 16 (a lane's rows lane/4 and lane/4 + 8), B 16 x 8 (its
 // column lane/4), D 16 x 8 fp32 (columns 2 (lane%4) and the next).
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -107,6 +113,18 @@ __device__ __forceinline__ int top_exponent(uint32_t bits) {
 __device__ __forceinline__ uint32_t finite_bits(float v) {
     const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
     return b < 0x7F800000u ? b : 0u;
+}
+
+// The bits of the largest finite magnitude of 16.
+__device__ __forceinline__ uint32_t top_bits(const float (&v)[16]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) top = max3_nan(top, fabsf(v[i]), fabsf(v[i + 1]));
+    if (top < __uint_as_float(0x7F800000u)) return __float_as_uint(top);
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) bits = max(bits, finite_bits(v[i]));
+    return bits;
 }
 
 // y = (1/4) H16 diag(d) x, in the order of ufp4_quantize's butterflies; and

@@ -21,8 +21,9 @@
 //  * The tokens are staged once per CTA in shared memory as FP16 operands, in
 //    the order in which lanes read them.  Each chunk of a token has its own
 //    power of two (its largest magnitude below 2^15), so BF16 tokens are exact
-//    down to 2^-29 of the chunk's largest; rotated or FP32 tokens are the sum
-//    of two FP16 values, within 2^-22 of each element.  The sum of a chunk's
+//    down to 2^-29 of the chunk's largest.  Rotated or FP32 tokens are, for an
+//    FP32 result, the sum of two FP16 values, within 2^-22 of each element; for
+//    a BF16 result (8 bits) one FP16 value (11 bits).  The sum of a chunk's
 //    products is scaled by that power and the weights' S when it is added to
 //    the fp32 sum.
 //  * Where the tokens do not fit, the inner dimension is gone through in
@@ -39,7 +40,7 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kChunk = 128;                    // elements of a row that 4 lanes hold
-constexpr uint32_t kStageBudget = 64 * 1024;   // staged tokens: two CTAs on an SM
+constexpr uint32_t kSharedBudget = 112 * 1024; // two CTAs on an SM
 constexpr uint32_t kSumsBudget = 16 * 1024;    // sums that wait between phases
 
 struct GemvArgs {
@@ -61,6 +62,9 @@ struct GemvArgs {
     const int32_t *src;
     int32_t n_experts, slots, topk, gather;
     int32_t wk, chunks, phase;   // warps along k; chunks of a row, and of a phase
+    int32_t factors;             // floats for the chunks' factors
+    int32_t red_two;             // whether the sums to be joined alternate between two places
+    int32_t stages, ring;        // chunks in flight (2 to 4), and where they lie in shared memory
     int32_t cpad;                // columns of a pass (power of two below 8, else 8 i)
     int32_t units;               // steps (wr tiles) of a matrix
     int32_t sums;                // steps a CTA may hold sums of (0: one phase)
@@ -71,15 +75,6 @@ struct Frag {
     uint4 c[2 * MT];
     uint32_t s[2 * MT];
 };
-
-// Weights are read once: they do not displace the tokens in L1.
-__device__ __forceinline__ uint4 load_stream(const uint8_t *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 
 // A step's columns: tokens [first, first + n) of its matrix, n <= 8 NT.
 struct Cols {
@@ -100,9 +95,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
 
     uint4 *xs = reinterpret_cast<uint4 *>(smem);                            // [PL][phase][4][cpad][4] x 16 bytes
     const uint32_t plane = (uint32_t)a.phase * 16u * a.cpad;                // 16-byte units
-    float *fac = reinterpret_cast<float *>(smem + (size_t)PL * plane * 16); // [phase][kCols]
-    float *red = fac + a.phase * kCols;                                     // [2][kWarps][kCols][kPitch]
-    float *sums = red + 2 * kWarps * kCols * kPitch;                        // [sums][wr][kCols][kRows]
+    float *fac = reinterpret_cast<float *>(smem + (size_t)PL * plane * 16); // [chunks of a phase][columns, 8 at least]
+    float *red = fac + a.factors;                                           // [1 or 2][kWarps][cpad][kPitch]
+    const int red_warp = a.cpad * kPitch;
+    float *sums = red + (a.red_two ? 2 : 1) * kWarps * red_warp;            // [sums][wr][kCols][kRows]
+    // the lane's own pieces of its warp's chunks in flight
+    constexpr int kSlot = (2 * MT + 1) * 512;
+    uint8_t *const ring = smem + a.ring + warp * a.stages * kSlot + lane * 16;
+    const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
 
     const int nseg = a.offsets ? a.n_experts : 1;
     int total;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
     if (begin >= end) return;
     const uint32_t signs = a.rht ? rht_sign_mask(a.rht_seed) : 0u;
     const int nkt = a.kpad >> 6;
-    const int64_t row_bytes = a.kpad >> 1;
+    const int64_t row_bytes = a.kpad >> 1, row_step = 32 * row_bytes;
 
     int seg = 0;
     if (a.offsets) {
@@ -189,40 +189,47 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
         const float ts = a.tensor_scale[zero + seg] * kDecoded<GRID>;
         const int64_t atom0 = (int64_t)seg * a.atoms;
 
-        for (int p0 = 0; p0 < a.chunks; p0 += a.phase) {
-            const int pch = min(a.phase, a.chunks - p0);
+        // chunks that fit beside this many columns, evenly over the phases
+        int phase = min(a.chunks, a.phase * a.cpad / cols.pad);
+        if (phase < a.chunks) {
+            const int n = (a.chunks + phase - 1) / phase, even = ((a.chunks + n - 1) / n + wk - 1) / wk * wk;
+            phase = min(phase, even);
+        }
+        const int fpitch = max(cols.pad, 8);
+        for (int p0 = 0; p0 < a.chunks; p0 += phase) {
+            const int pch = min(phase, a.chunks - p0);
             const int per = (pch + wk - 1) / wk;             // chunks of a warp
             const int items = steps * per;
-            Frag<MT> f[2];
-            auto load = [&](Frag<MT> &d, int it) {
-#pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) {
-                    d.c[i] = make_uint4(0, 0, 0, 0);
-                    d.s[i] = 0;
-                }
-                if (it >= items) return;
-                const int st = it / per, c = it - st * per;
-                const int in_phase = c * wk + my_k, chunk = p0 + in_phase;
-                if (in_phase >= pch || chunk * 2 + (t >> 1) >= nkt) return;
-                const int sub = (step0 + st) * wr + my_r;
+            // Where the next chunk to load lies: of the lane's rows of a step
+            // (row_count of 2 MT), chunk my_k + wk lc of the phase.
+            const int lane_chunks = (nkt + 1 - (t >> 1)) / 2 - p0;          // (a row may end with half a chunk)
+            const int lane_count = (min(pch, lane_chunks) - my_k + wk - 1) / wk;
+            int lc = 0, lst = 0, row_count = 0;
+            const uint8_t *cp = nullptr, *sp = nullptr;
+            const auto enter = [&] {
+                const int sub = (step0 + lst) * wr + my_r;
                 const int atom = sub / (8 / MT), w8 = (sub & 3) * 8 + g, i0 = MT == 1 ? (sub >> 2 & 1) * 2 : 0;
-                if (atom >= a.atoms) return;
-                const uint8_t *cp = a.codes + ((atom0 + atom) * 128 + w8 + i0 * 32) * row_bytes + chunk * 64 + t * 16;
                 const int row = atom * 128 + w8 + i0 * 32;
+                row_count = atom < a.atoms ? (a.rows - row + 31) >> 5 : 0;
+                cp = a.codes + (atom0 * 128 + row) * row_bytes + (p0 + my_k) * 64 + t * 16;
+                sp = a.scales + (((atom0 + atom) * nkt + (p0 + my_k) * 2 + (t >> 1)) << 9) + w8 * 16;
+            };
+            enter();
+            const auto copy = [&](int slot) {
+                const bool real = lst < steps && lc < lane_count;
+                const uint32_t to = ring_s + slot * kSlot;
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i)
-                    if (row + 32 * i < a.rows) d.c[i] = load_stream(cp + (int64_t)(32 * i) * row_bytes);
-                const uint8_t *sp = a.scales + (((atom0 + atom) * nkt + chunk * 2 + (t >> 1)) << 9) + w8 * 16;
-                if constexpr (MT == 2) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(sp);
-                    d.s[0] = v.x; d.s[1] = v.y; d.s[2] = v.z; d.s[3] = v.w;
-                } else {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(sp + i0 * 4);
-                    d.s[0] = v.x; d.s[1] = v.y;
+                for (int i = 0; i < 2 * MT; ++i) copy16(to + i * 512, cp + i * row_step, real && i < row_count);
+                copy16(to + 2 * MT * 512, sp, real && row_count > 0);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                cp += wk * 64;
+                sp += wk * 1024;
+                if (++lc == per) {
+                    lc = 0;
+                    if (++lst < steps) enter();
                 }
             };
-            load(f[0], 0);
-            load(f[1], 1);
+            for (int i = 0; i < a.stages; ++i) copy(i);
 
             // ---- the tokens' part of this phase
             __syncthreads();
@@ -267,16 +274,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
 #pragma unroll
                     for (int q = 0; q < 16; ++q) v[q] = 0.0f;
                 }
-                uint32_t top = 0;
-#pragma unroll
-                for (int q = 0; q < 16; ++q) top = max(top, finite_bits(v[q]));
+                uint32_t top = top_bits(v);
                 const uint32_t group = 0xffu << (lane & 24);     // the chunk's 8 lanes
                 top = max(top, __shfl_xor_sync(group, top, 1));
                 top = max(top, __shfl_xor_sync(group, top, 2));
                 top = max(top, __shfl_xor_sync(group, top, 4));
                 const int e = top_exponent(top);
                 const float m = exp2i(14 - e);
-                if (b == 0) fac[ch * kCols + col] = exp2i(e - 14) * ts;
+                if (b == 0) fac[ch * fpitch + col] = exp2i(e - 14) * ts;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t hi[4], lo[4];
@@ -296,19 +301,34 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
 
             // ---- the weights
             float sum[MT][NT][4] = {};
-            const int bcol = cols.pad < 8 ? g & (cols.pad - 1) : g;
+            const int x_word = cols.pad * 4;                 // 16-byte units from one word of the lanes to the next
+            const uint4 *const x_first = xs + my_k * 4 * x_word + (cols.pad < 8 ? g & (cols.pad - 1) : g) * 4 + t;
+            const uint4 *xp = x_first;
             int st = 0, c = 0;
-            auto use = [&](const Frag<MT> &d) {
+            const auto use = [&](int slot) {
                 const int ch = c * wk + my_k;
                 if (ch < pch) {
+                    Frag<MT> d;
+                    const uint8_t *from = ring + slot * kSlot;
+#pragma unroll
+                    for (int i = 0; i < 2 * MT; ++i) d.c[i] = *reinterpret_cast<const uint4 *>(from + i * 512);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(from + 2 * MT * 512);
+                    if constexpr (MT == 2) {
+                        d.s[0] = v.x; d.s[1] = v.y; d.s[2] = v.z; d.s[3] = v.w;
+                    } else {
+                        const bool upper = ((step0 + st) * wr + my_r) & 4;      // which 64 rows of the atom
+                        d.s[0] = upper ? v.z : v.x;
+                        d.s[1] = upper ? v.w : v.y;
+                    }
                     float acc[MT][NT][4] = {};
+                    uint32_t scale[2 * MT];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        const uint32_t sel = ((t & 1) * 2 + (u >> 1)) * 0x11u;
                         uint32_t h[2 * MT][4];
 #pragma unroll
                         for (int i = 0; i < 2 * MT; ++i) {
-                            const uint32_t s = scale_pair(d.s[i], sel);
+                            if (u % 2 == 0) scale[i] = scale_pair(d.s[i], ((t & 1) * 2 + u / 2) * 0x11u);
+                            const uint32_t s = scale[i];
                             decode8<GRID>(u == 0 ? d.c[i].x : u == 1 ? d.c[i].y : u == 2 ? d.c[i].z : d.c[i].w, h[i]);
 #pragma unroll
                             for (int q = 0; q < 4; ++q) h[i][q] = mul_pair(h[i][q], s);
@@ -316,10 +336,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             if (n > 0 && n * 8 >= cols.pad) break;
-                            const uint32_t at = ((uint32_t)(ch * 4 + u) * cols.pad + n * 8 + bcol) * 4 + t;
 #pragma unroll
                             for (int p = 0; p < PL; ++p) {
-                                const uint4 b = xs[p * plane + at];
+                                const uint4 b = xp[p * plane + u * x_word + n * 32];
 #pragma unroll
                                 for (int m = 0; m < MT; ++m) {
                                     const uint32_t(&r)[4] = h[2 * m];
@@ -332,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        const float2 w = *reinterpret_cast<const float2 *>(fac + ch * kCols + n * 8 + 2 * t);
+                        const float2 w = *reinterpret_cast<const float2 *>(fac + ch * fpitch + n * 8 + 2 * t);
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
                             sum[m][n][0] += acc[m][n][0] * w.x;
@@ -342,9 +361,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
                         }
                     }
                 }
+                xp += wk * 4 * x_word;
                 if (++c < per) return;
                 // ---- the end of a step: the warps' sums together
-                float *mine = red + (size_t)(parity * kWarps + warp) * kCols * kPitch;
+                float *mine = red + (parity * kWarps + warp) * red_warp;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -357,15 +377,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
                         }
                     }
                 __syncthreads();
-                for (int i = tid; i < wr * cols.n * kRows; i += kThreads) {
-                    const int r = i % kRows, rest = i / kRows, col = rest % cols.n, part = rest / cols.n;
-                    const float *from = red + (size_t)(parity * kWarps + part * wk) * kCols * kPitch + col * kPitch + r;
+                // a warp takes a column (two of 16 rows) of one of the step's tiles
+                constexpr int kPer = 32 / kRows;
+                const int r = lane % kRows;
+                for (int i = warp * kPer + lane / kRows, part = 0; part < wr; i += kWarps * kPer) {
+                    for (; i >= cols.n && part < wr; i -= cols.n) ++part;
+                    if (part >= wr) break;
+                    const int col = i;
+                    const float *from = red + (parity * kWarps + part * wk) * red_warp + col * kPitch + r;
                     float v = from[0];
-                    for (int w = 1; w < wk; ++w) v += from[(size_t)w * kCols * kPitch];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w)
+                        if (w < wk) v += from[w * red_warp];
                     if (a.sums) {
                         float *kept = sums + ((size_t)(st * wr + part) * kCols + col) * kRows + r;
                         if (p0 > 0) v += *kept;
-                        if (p0 + a.phase < a.chunks) {
+                        if (p0 + phase < a.chunks) {
                             *kept = v;
                             continue;
                         }
@@ -379,18 +406,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
                     if (a.y_fp32) static_cast<float *>(a.y)[at] = v;
                     else static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(v);
                 }
-                parity ^= 1;
+                if (a.red_two) parity ^= 1;
+                else __syncthreads();
                 c = 0;
+                xp = x_first;
                 ++st;
             };
-            for (int it = 0; it < items; it += 2) {
-                use(f[0]);
-                load(f[0], it + 2);
-                if (it + 1 < items) {
-                    use(f[1]);
-                    load(f[1], it + 3);
-                }
+            for (int it = 0, slot = 0; it < items; ++it) {
+                if (a.stages == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+                else if (a.stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+                else asm volatile("cp.async.wait_group 1;" ::: "memory");
+                use(slot);
+                copy(slot);
+                if (++slot == a.stages) slot = 0;
             }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");     // (the next phase's copies go to the same places)
         }
         u0 += steps;
     }
@@ -399,20 +429,42 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
 template <int GRID, int MT, int NT, int PL>
 cudaError_t launch(GemvArgs a, int most_cols, cudaStream_t s) {
     constexpr int kCols = 8 * NT, kRows = 16 * MT, kPitch = kRows + 4;
-    const int wr = kWarps / a.wk;
-    const int64_t steps = ((int64_t)a.atoms * (8 / MT) + wr - 1) / wr;
-    a.units = (int)steps;
     a.cpad = pad_cols(std::min(most_cols, kCols));
+    a.red_two = a.cpad <= 8;
     const uint32_t per_chunk = 256u * a.cpad * PL;
-    a.phase = std::max<int>(1, std::min<int>(a.chunks, kStageBudget / per_chunk));
-    if (a.phase < a.chunks && a.phase > a.wk) a.phase = a.phase / a.wk * a.wk;
+    const size_t red_bytes = (size_t)(a.red_two ? 2 : 1) * kWarps * a.cpad * kPitch * 4, slot = (2 * MT + 1) * 512;
+    // What the chunks in flight leave holds the tokens and their factors: all
+    // of them beside four, three or two chunks, else as many as go beside two
+    // (and the sums that then wait).
+    const auto room = [&](int stages, size_t others) {
+        const int64_t left = (int64_t)kSharedBudget - (int64_t)(kWarps * stages * slot + red_bytes + others + 512);
+        return (int)std::max<int64_t>(1, left / (per_chunk + 36 * a.cpad));
+    };
+    a.stages = 4;
+    while (a.stages > 2 && room(a.stages, 0) < a.chunks) --a.stages;
+    a.phase = room(a.stages, 0) >= a.chunks ? a.chunks : room(2, kSumsBudget);
     // upper bound on the steps of all passes (the device knows the counts)
     int64_t passes;
     if (a.offsets) passes = std::min<int64_t>(a.slots, (int64_t)a.n_experts + a.slots / a.cpad);
     else passes = (a.tokens + a.cpad - 1) / a.cpad;
-    const int64_t total = passes * steps;
-    if (total > 0x7fffffff) return cudaErrorNotSupported;
-    int64_t grid = std::min<int64_t>(total, 2 * (int64_t)num_sms());
+    const int64_t ctas = 2 * (int64_t)num_sms(), tiles = (int64_t)a.atoms * (8 / MT);
+    if (passes * tiles > 0x7fffffff) return cudaErrorNotSupported;
+    // Warps along k: what makes the CTAs' steps times the chunks of a warp,
+    // and the joining of the sums (about 3/4 of a chunk's time), the least.
+    const int64_t likely = a.offsets ? std::min<int64_t>(a.slots, a.n_experts) : passes;
+    int64_t least = INT64_MAX;
+    for (int wk = kWarps; wk >= 1; wk /= 2) {
+        const int64_t steps = likely * ((tiles * wk + kWarps - 1) / kWarps);
+        const int64_t cost = (steps + ctas - 1) / ctas * (4 * ((a.chunks + wk - 1) / wk) + 3);
+        if (cost < least) {
+            least = cost;
+            a.wk = wk;
+        }
+    }
+    const int wr = kWarps / a.wk;
+    const int64_t steps = (tiles + wr - 1) / wr, total = passes * steps;
+    a.units = (int)steps;
+    int64_t grid = std::min<int64_t>(total, ctas);
     size_t sum_bytes = 0;
     a.sums = 0;
     if (a.phase < a.chunks) {
@@ -422,8 +474,10 @@ cudaError_t launch(GemvArgs a, int most_cols, cudaStream_t s) {
         a.sums = (int)((total + grid - 1) / grid);
         sum_bytes = a.sums * one;
     }
-    const size_t bytes = (size_t)a.phase * per_chunk + (size_t)a.phase * kCols * 4 +
-                         2 * (size_t)kWarps * kCols * kPitch * 4 + sum_bytes;
+    // (a pass over fewer columns has as many more chunks in a phase)
+    a.factors = 8 * std::min(a.chunks, a.phase * a.cpad) + a.phase * a.cpad;
+    a.ring = (int)((a.phase * (size_t)per_chunk + a.factors * 4 + red_bytes + sum_bytes + 15) / 16 * 16);
+    const size_t bytes = a.ring + kWarps * a.stages * slot;
     cudaError_t e = cudaFuncSetAttribute(k_gemv<GRID, MT, NT, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)bytes);
     if (e != cudaSuccess) return e;
@@ -434,11 +488,12 @@ cudaError_t dispatch(const GemvArgs &a, int grid, int most_cols, cudaStream_t s)
     cudaError_t e = cudaSuccess;
     auto with = [&](auto gr, auto mt, auto nt) {
         constexpr int G = decltype(gr)::value, M = decltype(mt)::value, N = decltype(nt)::value;
-        if (a.rht || a.x_fp32) e = launch<G, M, N, 2>(a, most_cols, s);
+        if (a.y_fp32 && (a.rht || a.x_fp32)) e = launch<G, M, N, 2>(a, most_cols, s);
         else e = launch<G, M, N, 1>(a, most_cols, s);
     };
     auto by_cols = [&](auto gr) {
-        if (most_cols <= 8) with(gr, Int<2>(), Int<1>());
+        // (by expert: for as many tokens as one has on average)
+        if (most_cols <= 8 || (a.offsets && a.slots <= 8 * (int64_t)a.n_experts)) with(gr, Int<2>(), Int<1>());
         else if (most_cols <= 16 || a.offsets) with(gr, Int<2>(), Int<2>());
         else with(gr, Int<1>(), Int<4>());
     };
@@ -475,9 +530,6 @@ cudaError_t launch_gemv(const GemvLaunch &l, cudaStream_t s) {
     a.topk = l.topk;
     a.gather = l.gather;
     a.chunks = (a.kpad + kChunk - 1) / kChunk;
-    // Warps along k: as many as leave at most a quarter of their chunks empty.
-    a.wk = 8;
-    while (a.wk > 1 && a.chunks * 4 < (a.chunks + a.wk - 1) / a.wk * a.wk * 3) a.wk /= 2;
     // By expert, columns for what one mostly has: a token each.  (One that a
     // token names twice may have more, in further passes.)
     return dispatch(a, l.grid, (int)(l.offsets ? std::min(l.slots, l.tokens) : l.tokens), s);

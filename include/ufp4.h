@@ -573,7 +573,8 @@ UFP4_API ufp4_status ufp4_swiglu_bwd(const void *dh, int32_t dh_dtype, int64_t l
  * 16-block of x rotated by (1/4) H16 diag(d) with the signs of rht_seed: what
  * goes with weights quantized with rht = 1 and that seed.  x is not quantized:
  * a BF16 element not rotated enters exactly, one rotated or FP32 within 2^-22
- * of itself, each down to 2^-29 of the largest among the 128 it lies with.
+ * of itself where y is FP32 and 2^-11 where y is BF16 (which keeps 2^-8), each
+ * down to 2^-29 of the largest among the 128 it lies with.
  * Made for 1 to 32 tokens; further ones read w once more per 32.
  *   x : tokens x w->k;  y : tokens x w->rows.  w->k <= UFP4_MAX_WIDTH.
  * w->k = 0 writes zeros.  w->eplane is not read. */
@@ -674,7 +675,7 @@ UFP4_API ufp4_status ufp4_cache_load(const ufp4_cache *cache, const int64_t *slo
  *   workspace: ufp4_cache_attn_workspace_bytes(...) bytes, 16-byte aligned, of
  *            this call until it has run (NULL where that is 0).
  * heads a multiple of cache->heads; m 1 .. UFP4_MAX_NEW; width * page < 2^31.
- * Scores are fp32 of q as ufp4_gemv takes x; the probabilities enter the sum
+ * Scores are fp32, of q as ufp4_gemv takes x for an FP32 y; the probabilities enter the sum
  * over V as FP16 relative to the largest of their row scales (11 bits; 22 where
  * out is FP32). */
 UFP4_API size_t ufp4_cache_attn_workspace_bytes(int64_t batch, int32_t m, int32_t heads, int64_t width,

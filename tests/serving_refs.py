@@ -58,9 +58,9 @@ def rotate(x, seed, back=False):
     return (x.reshape(x.shape[:-1] + (x.shape[-1] // 16, 16)) @ (r if back else r.T)).reshape(x.shape)
 
 
-def gemv(x, w, rht, seed, exact):
+def gemv(x, w, rht, seed, unit):
     """y, and the bound of its error before the result's own rounding.  x
-    [t, k]; w [n, k]; exact: x enters exactly (BF16, not rotated)."""
+    [t, k]; w [n, k]; unit: relative error of an element of x (0: exact)."""
     x, w = np.asarray(x, np.float64), np.asarray(w, np.float64)
     t, k = x.shape
     blur = np.zeros(x.shape)
@@ -69,8 +69,7 @@ def gemv(x, w, rht, seed, exact):
         top = np.abs(x).reshape(t, k // 16, 16).sum(-1) / 4
         blur = np.repeat(top * 4 * U24, 16, axis=-1)
         x = rotate(x, seed)
-    if not exact:
-        blur = blur + np.abs(x) * 2.0 ** -22
+    blur = blur + np.abs(x) * unit
     for a in range(0, k, 128):
         blur[:, a:a + 128] += 2.0 ** -38 * np.abs(x[:, a:a + 128]).max(-1, keepdims=True)
     adds = 2 * 128 + k / 128 + 16
@@ -144,7 +143,7 @@ def attn(q, k, v, rows, sees, scale, planes_exact, out_two, top_v, dim):
     rel = np.expm1(de).max(-1, keepdims=True, initial=0.0)
     w_abs = w @ np.abs(v)
     tol = w_abs * (2 * rel + (2.0 ** -21 if out_two else 2.0 ** -11) + 2 * n * U23)
-    # probabilities below FP16's normal numbers, relative to the largest row
-    tol = tol + n * 2.0 ** -38 * top_v / np.where(z > 0, z, 1)
+    # probabilities below FP16's normal numbers: half a step of 2^-24, in units of 2^-11 of the largest row's scale
+    tol = tol + n * 2.0 ** -36 * top_v / np.where(z > 0, z, 1)
     lse_tol = rel[:, 0] + n[:, 0] * U23 + np.abs(np.where(np.isfinite(lse), lse, 0)) * 4 * U24 + 2.0 ** -20
     return out, lse, tol, lse_tol

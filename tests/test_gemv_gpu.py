@@ -48,7 +48,9 @@ def _x(g, shape, dtype, pad=0, shift=0, spread=0):
 
 
 def _check(y, x, w, rht, out, tag=""):
-    want, tol = R.gemv(_f64(x), w, rht, SEED, exact=x.dtype is BF and not rht)
+    # exact, one FP16 value (11 bits), or two
+    unit = 0.0 if x.dtype is BF and not rht else 2.0 ** -11 if out is BF else 2.0 ** -22
+    want, tol = R.gemv(_f64(x), w, rht, SEED, unit)
     got = _f64(y)
     tol = tol + R.half_step(out) * (np.abs(want) + tol) + 1e-44
     bad = ~(np.abs(got - want) <= tol)
