@@ -1,6 +1,7 @@
 // cache.cu -- keys and values kept in 4 bits: written row by row as they
 // come, read back, and attended over by new tokens.  (include/ufp4.h:
 // ufp4_cache_append, ufp4_cache_load, ufp4_cache_attn.)
+#include "attn.cuh"
 #include "common.cuh"
 #include "dequant.cuh"
 #include "internal.h"
@@ -161,49 +162,13 @@ __global__ void __launch_bounds__(128) k_load(RowArgs a) {
 // (11 bits; two of them for fp32 results), and the sums are fp32.  Keys of a
 // sequence are spread over warps, and over CTAs (splits) where sequences and
 // heads are too few; the parts are joined in a fixed order.
-struct AttnArgs {
-    const void *q;
-    int64_t q_token, q_head;
-    int32_t q_fp32, planes, two_p;
-    CacheHalf k, v;
-    const int32_t *table;
-    int64_t ld_table;
-    int32_t width, pages, page_shift;
-    const int32_t *lens;
-    const uint64_t *mask;
-    int32_t batch, m, heads, kv, group, dim, rht, qtiles, splits;
-    uint64_t rht_seed;
-    float scale;
-    void *out;
-    int64_t o_token, o_head;
-    int32_t out_fp32;
-    float *lse;
-    float *part_o, *part_m, *part_l;     // splits > 1: of each split and query
-};
+constexpr int kAttnWarps = 4, kTileKeys = 32;
 
-constexpr int kAttnWarps = 4, kTileKeys = 32, kSplitKeys = 128;   // a split's keys are a multiple of the last
-
-// 2^x, within 2 units in the last place; 0 below 2^-126.
-__device__ __forceinline__ float exp2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
-// Keys [first, last) of a sequence of `len` that split s of n takes.
-__device__ __forceinline__ int split_keys(int len, int n) {
-    return max((len + n - 1) / n + kSplitKeys - 1, kSplitKeys) / kSplitKeys * kSplitKeys;
-}
-__device__ __forceinline__ void split_range(int len, int s, int n, int &first, int &last) {
-    const int per = split_keys(len, n);
-    first = (int)min((int64_t)s * per, (int64_t)len);
-    last = min(first + per, len);
-}
-
 // Ends a row: O / l, back from the rotation, rounded once.  A lane has the 8
 // elements 8 lane .. 8 lane + 7 (lanes past the row none).
 __device__ __forceinline__ void finish_row(const AttnArgs &a, float (&o)[8], float m2, float l, int b, int q, int kvh,
@@ -751,23 +716,25 @@ cudaError_t join(const AttnArgs &a, int kdim, cudaStream_t s) {
     return a.splits <= 8 ? with(Int<1>()) : a.splits <= 32 ? with(Int<4>()) : with(Int<8>());
 }
 
-// The kernel's query groups, and how many of its CTAs share an SM.
+// The kernel's groups of queries (nt of 8; 0: the wide kernel's 128), how many
+// of its CTAs share an SM, and the keys' time that its start and end take.
 struct Shape {
-    int nt, qtiles, resident;
+    int nt, qtiles, resident, start;
 };
 Shape shape_of(int64_t queries, int64_t padded) {
+    if (queries > 16 && padded <= 128) return Shape{0, (int)((queries + kWideQueries - 1) / kWideQueries), 1, 512};
     const int nt = queries <= 8 || padded > 128 ? 1 : 2;
-    return Shape{nt, (int)((queries + 8 * nt - 1) / (8 * nt)), nt == 1 && padded <= 128 ? 4 : 2};
+    return Shape{nt, (int)((queries + 8 * nt - 1) / (8 * nt)), nt == 1 && padded <= 128 ? 4 : 2, 64};
 }
-// Splits of a sequence: what makes an SM's CTAs times the keys of one, and its
-// start and end (about 64 keys' time), the least; fewer CTAs than share an SM
+// Splits of a sequence: what makes an SM's CTAs times the keys of one, its start
+// and end among them, the least; fewer CTAs than share an SM
 // leave it idle, and every split is read again when they are joined.
 int splits_of(int64_t batch, int64_t kv, const Shape &shape, int64_t most_keys) {
     const int64_t ctas = batch * kv * shape.qtiles, sms = num_sms();
     int64_t best = 1, least = INT64_MAX;
     for (int64_t s = 1; s <= 512 && (s == 1 || (s - 1) * kSplitKeys < most_keys); ++s) {
         const int64_t keys = (most_keys + s * kSplitKeys - 1) / (s * kSplitKeys) * kSplitKeys;
-        const int64_t cost = std::max<int64_t>((ctas * s + sms - 1) / sms, shape.resident) * (keys + 64) + 6 * s;
+        const int64_t cost = std::max<int64_t>((ctas * s + sms - 1) / sms, shape.resident) * (keys + shape.start) + 6 * s;
         if (cost < least) {
             least = cost;
             best = s;
@@ -892,6 +859,10 @@ cudaError_t launch_cache_attn(const CacheAttn &l, cudaStream_t s) {
     a.part_o = static_cast<float *>(l.workspace);
     a.part_m = a.part_o + all * l.cache.padded;
     a.part_l = a.part_m + all;
+    if (shape.nt == 0) {
+        const cudaError_t e = launch_attn_wide(a, l.cache.grid, l.cache.padded, s);
+        return e != cudaSuccess || a.splits == 1 ? e : join(a, l.cache.padded, s);
+    }
     const auto with = [&](auto gr, auto dc) {
         constexpr int G = decltype(gr)::value, D = decltype(dc)::value;
         if constexpr (D <= 2)

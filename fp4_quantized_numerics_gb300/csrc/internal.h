@@ -237,5 +237,6 @@ cudaError_t launch_cache_attn(const CacheAttn &l, cudaStream_t s);
 // when it gives up (synchronises s).
 cudaError_t read_timeout_flag(uint32_t *flag, cudaStream_t s);
 cudaError_t read_quant_timeout_flag(uint32_t *flag, cudaStream_t s);
+cudaError_t read_attn_timeout_flag(uint32_t *flag, cudaStream_t s);
 
 }  // namespace ufp4

@@ -264,9 +264,9 @@ UFP4_API ufp4_status ufp4_quantize_noalloc(const void *x, int32_t dtype, int64_t
 /* Reports device-side problems (synchronises `stream`).  The pages have no
  * counterpart: this is the library's failure reporting for the kernels of
  * the calls above.  Returns the first that applies:
- *   UFP4_ERR_TIMEOUT   -- a bounded wait inside a GEMM kernel gave up since
- *                         the last check (the flag is then cleared); that
- *                         GEMM's output is unspecified;
+ *   UFP4_ERR_TIMEOUT   -- a bounded wait inside a GEMM or attention kernel
+ *                         gave up since the last check (the flag is then
+ *                         cleared); that call's output is unspecified;
  *   UFP4_ERR_NONFINITE -- the last ufp4_quantize that used `workspace` saw a
  *                         NaN/Inf input (computed-amax path) or a non-finite
  *                         amax_in; its outputs are unspecified.
