@@ -26,7 +26,8 @@ struct AttnArgs {
     int64_t o_token, o_head;
     int32_t out_fp32;
     float *lse;
-    float *part_o, *part_m, *part_l;     // splits > 1: of each split and query
+    int32_t clustered;                   // the splits of a sequence are a cluster, which joins them
+    float *part_o, *part_m, *part_l;     // else, splits > 1: of each split and query
 };
 
 constexpr int kSplitKeys = 128;      // a split's keys are a multiple of this

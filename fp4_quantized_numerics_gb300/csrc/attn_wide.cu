@@ -725,7 +725,7 @@ cudaError_t wide(const AttnArgs &a, cudaStream_t s) {
         cudaFuncSetAttribute(k_attn_wide<GRID, DC, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     return launch_in_order_smem(k_attn_wide<GRID, DC, TWO>,
-                                dim3((unsigned)(a.batch * a.kv * a.qtiles), (unsigned)a.splits), kThreads, bytes, s, a);
+                                dim3((unsigned)(a.batch * a.kv * a.qtiles), (unsigned)a.splits), kThreads, bytes, 1, s, a);
 }
 
 }  // namespace

@@ -163,6 +163,31 @@ __global__ void __launch_bounds__(128) k_load(RowArgs a) {
 // sequence are spread over warps, and over CTAs (splits) where sequences and
 // heads are too few; the parts are joined in a fixed order.
 constexpr int kAttnWarps = 4, kTileKeys = 32;
+constexpr int kCluster = 8;              // splits that a cluster joins
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// *p of the cluster's CTA `rank` (its y is its rank), p in this CTA's shared memory.
+__device__ __forceinline__ uint32_t cluster_at(const float *p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float cluster_load(const float *p, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_at(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 cluster_load4(const float *p, uint32_t rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_at(p, rank))
+                 : "memory");
+    return v;
+}
+
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
@@ -238,7 +263,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
     const int len = min(max(a.lens[zero + b], 0), most);
     int first, last;
     split_range(len, blockIdx.y, a.splits, first, last);
-    if (a.splits > 1 && first >= last) return;        // (the join does not look)
+    if (a.splits > 1 && first >= last && !a.clustered) return;        // (the join does not look)
     const int q0 = qt * kQ, nq = min(a.group * a.m - q0, kQ);
 
     // ---- the rows' copies
@@ -643,6 +668,18 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
         }
         if (a.splits == 1) {
             finish_row(a, v, top, sum, b, q0 + col, kvh, lane);
+        } else if (a.clustered) {
+            // (in the place of the first warp's part, which these lanes have read)
+            __syncwarp();
+            if (lane * 8 < kDim) {
+                float4 *to = reinterpret_cast<float4 *>(po + col * kDim + lane * 8);
+                to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                to[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+            if (lane == 0) {
+                pm[col] = top;
+                pl[col] = sum;
+            }
         } else {
             const int64_t r = ((int64_t)blockIdx.y * a.batch * a.kv + bh) * (a.group * a.m) + q0 + col;
             if (lane * 8 < kDim) {
@@ -656,6 +693,26 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
             }
         }
     }
+    if (!a.clustered) return;
+    // ---- the cluster's parts together: each CTA joins some of the queries
+    cluster_sync();
+    for (int col = blockIdx.y * kAttnWarps + warp; col < nq; col += a.splits * kAttnWarps) {
+        float top = -INFINITY, sum = 0.0f, v[8] = {};
+        for (int s = 0; s < a.splits; ++s) top = fmaxf(top, cluster_load(pm + col, s));
+        const float base = top == -INFINITY ? 0.0f : top;
+        for (int s = 0; s < a.splits; ++s) {
+            const float f = exp2f(cluster_load(pm + col, s) - base);
+            sum += cluster_load(pl + col, s) * f;
+            if (lane * 8 < kDim) {
+                const float4 x = cluster_load4(po + col * kDim + lane * 8, s),
+                             y = cluster_load4(po + col * kDim + lane * 8 + 4, s);
+                v[0] += x.x * f; v[1] += x.y * f; v[2] += x.z * f; v[3] += x.w * f;
+                v[4] += y.x * f; v[5] += y.y * f; v[6] += y.z * f; v[7] += y.w * f;
+            }
+        }
+        finish_row(a, v, top, sum, b, q0 + col, kvh, lane);
+    }
+    cluster_sync();                       // (the others have read this CTA's)
 }
 
 // Joins the splits' parts: W warps a query (of 8 in a CTA), each some of its
@@ -726,6 +783,8 @@ Shape shape_of(int64_t queries, int64_t padded) {
     const int nt = queries <= 8 || padded > 128 ? 1 : 2;
     return Shape{nt, (int)((queries + 8 * nt - 1) / (8 * nt)), nt == 1 && padded <= 128 ? 4 : 2, 64};
 }
+// Whether `splits` are joined within the kernel, by a cluster.
+bool clusters(int64_t splits, const Shape &shape) { return shape.nt && splits > 1 && splits <= kCluster; }
 // Splits of a sequence: what makes an SM's CTAs times the keys of one, its start
 // and end among them, the least; fewer CTAs than share an SM
 // leave it idle, and every split is read again when they are joined.
@@ -734,7 +793,8 @@ int splits_of(int64_t batch, int64_t kv, const Shape &shape, int64_t most_keys) 
     int64_t best = 1, least = INT64_MAX;
     for (int64_t s = 1; s <= 512 && (s == 1 || (s - 1) * kSplitKeys < most_keys); ++s) {
         const int64_t keys = (most_keys + s * kSplitKeys - 1) / (s * kSplitKeys) * kSplitKeys;
-        const int64_t cost = std::max<int64_t>((ctas * s + sms - 1) / sms, shape.resident) * (keys + shape.start) + 6 * s;
+        const int64_t joined = s == 1 || clusters(s, shape) ? 0 : 1600 + 6 * s;
+        const int64_t cost = std::max<int64_t>((ctas * s + sms - 1) / sms, shape.resident) * (keys + shape.start) + joined;
         if (cost < least) {
             least = cost;
             best = s;
@@ -752,8 +812,8 @@ cudaError_t attn(const AttnArgs &a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(k_attn<GRID, DC, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) return e;
     e = launch_in_order_smem(k_attn<GRID, DC, NT>, dim3((unsigned)(a.batch * a.kv * a.qtiles), (unsigned)a.splits),
-                             kAttnWarps * 32, bytes, s, a);
-    if (e != cudaSuccess || a.splits == 1) return e;
+                             kAttnWarps * 32, bytes, a.clustered ? a.splits : 1, s, a);
+    if (e != cudaSuccess || a.splits == 1 || a.clustered) return e;
     return join(a, kDim, s);
 }
 
@@ -800,8 +860,8 @@ cudaError_t launch_cache_append(const CacheRows &l, cudaStream_t s) {
     return by_threads(a.blocks, [&](auto g) {
         constexpr int G = decltype(g)::value;
         const dim3 grid((unsigned)((a.rows * G + 127) / 128), 2);
-        return a.fp32 ? launch_in_order_smem(k_append<float, G>, grid, 128, 0, s, a)
-                      : launch_in_order_smem(k_append<__nv_bfloat16, G>, grid, 128, 0, s, a);
+        return a.fp32 ? launch_in_order_smem(k_append<float, G>, grid, 128, 0, 1, s, a)
+                      : launch_in_order_smem(k_append<__nv_bfloat16, G>, grid, 128, 0, 1, s, a);
     });
 }
 
@@ -810,15 +870,16 @@ cudaError_t launch_cache_load(const CacheRows &l, cudaStream_t s) {
     return by_threads(a.blocks, [&](auto g) {
         constexpr int G = decltype(g)::value;
         const dim3 grid((unsigned)((a.rows * G + 127) / 128), 2);
-        return a.fp32 ? launch_in_order_smem(k_load<float, G>, grid, 128, 0, s, a)
-                      : launch_in_order_smem(k_load<__nv_bfloat16, G>, grid, 128, 0, s, a);
+        return a.fp32 ? launch_in_order_smem(k_load<float, G>, grid, 128, 0, 1, s, a)
+                      : launch_in_order_smem(k_load<__nv_bfloat16, G>, grid, 128, 0, 1, s, a);
     });
 }
 
 size_t cache_attn_workspace(int64_t batch, int64_t m, int64_t heads, int64_t kv, int64_t padded, int64_t most_keys) {
     const int64_t queries = heads / kv * m;
-    const int64_t splits = splits_of(batch, kv, shape_of(queries, padded), most_keys);
-    return splits == 1 ? 0 : (size_t)(splits * batch * m * heads * (padded + 2)) * sizeof(float);
+    const Shape shape = shape_of(queries, padded);
+    const int64_t splits = splits_of(batch, kv, shape, most_keys);
+    return splits == 1 || clusters(splits, shape) ? 0 : (size_t)(splits * batch * m * heads * (padded + 2)) * sizeof(float);
 }
 
 cudaError_t launch_cache_attn(const CacheAttn &l, cudaStream_t s) {
@@ -855,6 +916,7 @@ cudaError_t launch_cache_attn(const CacheAttn &l, cudaStream_t s) {
     const Shape shape = shape_of(queries, l.cache.padded);
     a.qtiles = shape.qtiles;
     a.splits = splits_of(a.batch, a.kv, shape, l.width << a.page_shift);
+    a.clustered = clusters(a.splits, shape);
     const int64_t all = (int64_t)a.batch * a.kv * queries * a.splits;
     a.part_o = static_cast<float *>(l.workspace);
     a.part_m = a.part_o + all * l.cache.padded;

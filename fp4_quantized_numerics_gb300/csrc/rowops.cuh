@@ -40,24 +40,29 @@ __device__ __forceinline__ uint32_t begin_in_order() {
     asm volatile("griddepcontrol.wait;\n\tmov.u32 %0, 0;" : "=r"(zero)::"memory");
     return zero;
 }
+// (grid: a multiple of `cluster` CTAs in y; 1: none)
 template <class... Params, class... Args>
-cudaError_t launch_in_order_smem(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem, cudaStream_t s,
-                                 Args... args) {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch_in_order_smem(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem, unsigned cluster,
+                                 cudaStream_t s, Args... args) {
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = cluster;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 template <class... Params, class... Args>
 cudaError_t launch_in_order(void (*kernel)(Params...), uint64_t grid, unsigned block, cudaStream_t s, Args... args) {
-    return launch_in_order_smem(kernel, dim3((unsigned)grid), block, 0, s, args...);
+    return launch_in_order_smem(kernel, dim3((unsigned)grid), block, 0, 1, s, args...);
 }
 
 // n / d by a multiplication: q = floor(n m / 2^64) with m = ceil(2^64 / d).

@@ -597,7 +597,7 @@ def _streams(stream, dev):
 
 
 def _empty(shape, dtype, dev, on=None):
-    """A fresh contiguous tensor (one or two dims) on the current device, for
+    """A fresh contiguous tensor (one to three dims) on the current device, for
     use on stream `on` (None: the current one)."""
     global _empty_strided_cuda
     if on is not None:
@@ -605,7 +605,8 @@ def _empty(shape, dtype, dev, on=None):
             return _empty(shape, dtype, dev)
     if _empty_strided_cuda is not None:
         try:
-            return _empty_strided_cuda(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
+            return _empty_strided_cuda(shape, (shape[1], 1) if len(shape) == 2 else (1,) if len(shape) == 1 else
+                                       (shape[1] * shape[2], shape[2], 1), dtype)
         except TypeError:
             pass
     out = torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
@@ -988,16 +989,15 @@ class Cache:
             raise ValueError("k_codes must be [pages, heads, page, width]")
         pages, heads, page, _ = k_codes.shape
         dev, pad = k_codes.get_device(), self._pad(head_dim)
-        for t, name, dtype, tail in ((k_codes, "k_codes", torch.uint8, (pad // 2,)),
-                                     (v_codes, "v_codes", torch.uint8, (pad // 2,)),
-                                     (k_scales, "k_scales", torch.uint8, (pad // 16,)),
-                                     (v_scales, "v_scales", torch.uint8, (pad // 16,)),
-                                     (k_row_scale, "k_row_scale", _FLOAT32, ()),
-                                     (v_row_scale, "v_row_scale", _FLOAT32, ())):
-            if t.get_device() != dev:
-                _same_place(t.get_device(), dev, name)
-            if t.dtype is not dtype or t.shape != (pages, heads, page) + tail or not t.is_contiguous():
-                raise ValueError("%s must be contiguous %s %s" % (name, dtype, (pages, heads, page) + tail))
+        rows = (pages, heads, page)
+        for shape, dtype, pair, names in ((rows + (pad // 2,), torch.uint8, (k_codes, v_codes), "codes"),
+                                          (rows + (pad // 16,), torch.uint8, (k_scales, v_scales), "scales"),
+                                          (rows, _FLOAT32, (k_row_scale, v_row_scale), "row_scale")):
+            for t in pair:
+                if t.get_device() != dev:
+                    _same_place(t.get_device(), dev, names)
+                if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+                    raise ValueError("%s must be contiguous %s %s" % (names, dtype, shape))
         self.k_codes, self.k_scales, self.k_row_scale = k_codes, k_scales, k_row_scale
         self.v_codes, self.v_scales, self.v_row_scale = v_codes, v_scales, v_row_scale
         self.pages, self.heads, self.page, self.head_dim, self._dev = pages, heads, page, head_dim, dev
@@ -1058,10 +1058,6 @@ def _slots(slots, dev, tokens=None):
     return slots.data_ptr()
 
 
-def _empty3(shape, dtype, dev, on):
-    return _empty((shape[0], shape[1] * shape[2]), dtype, dev, on).view(shape)
-
-
 def ufp4_cache_append(k, v, slots, cache, stream=None):
     """Quantizes k and v ([tokens, heads, head_dim], bf16 or fp32) into the
     cache at places slots ([tokens] int64, page number * page + offset, all
@@ -1089,14 +1085,21 @@ def ufp4_cache_load(cache, slots, dtype=None, k=None, v=None, stream=None):
         dtype = dtype or torch.bfloat16
         if dtype not in _DTYPES:
             raise TypeError("k and v must be bf16 or fp32, got %s" % dtype)
-        k, v = _empty3(shape, dtype, dev, on), _empty3(shape, dtype, dev, on)
+        k, v = _empty(shape, dtype, dev, on), _empty(shape, dtype, dev, on)
+        kp, vp, dt, kh = k.data_ptr(), v.data_ptr(), _DTYPES[dtype], shape[2]
+        kld = vld = shape[1] * kh
+        vh = kh
     elif k.dtype is not v.dtype or (dtype is not None and k.dtype is not dtype):
         raise TypeError("k and v must be %s" % (dtype or "of one dtype"))
-    kp, dt, kld, kh, _ = _heads3d(k, "k", dev, cache.heads, cache.head_dim, shape[0])
-    vp, _, vld, vh, _ = _heads3d(v, "v", dev, cache.heads, cache.head_dim, shape[0])
+    else:
+        kp, dt, kld, kh, _ = _heads3d(k, "k", dev, cache.heads, cache.head_dim, shape[0])
+        vp, _, vld, vh, _ = _heads3d(v, "v", dev, cache.heads, cache.head_dim, shape[0])
     st = lib().ufp4_cache_load(cc, sp, shape[0], kp, vp, dt, kld, kh, vld, vh, s)
     _check(st, "ufp4_cache_load")
     return k, v
+
+
+_attn_needs = {}     # scratch bytes by a call's sizes (and the device, by whose SMs the work is split)
 
 
 def ufp4_cache_attn(q, cache, table, lens, mask=None, scale=None, dtype=None, out=None, lse=None, ws=None,
@@ -1112,19 +1115,22 @@ def ufp4_cache_attn(q, cache, table, lens, mask=None, scale=None, dtype=None, ou
     (out, lse)."""
     dev = _place(q, "q")
     cc, (s, on) = _struct(cache, dev, "cache"), _streams(stream, dev)
-    if q.dim() != 3:
+    shape, span = q.shape, table.shape
+    if len(shape) != 3:
         raise ValueError("q must be [batch * m, heads, head_dim]")
-    tokens, heads, dim = q.shape
-    for t, name, dtypes in ((table, "table", _INT32), (lens, "lens", _INT32)):
-        if t.get_device() != dev:
-            _same_place(t.get_device(), dev, name)
-        if t.dtype is not dtypes:
-            raise TypeError("%s must be int32, got %s" % (name, t.dtype))
+    tokens, heads, dim = shape
+    if table.get_device() != dev:
+        _same_place(table.get_device(), dev, "table")
+    if lens.get_device() != dev:
+        _same_place(lens.get_device(), dev, "lens")
+    if table.dtype is not _INT32 or lens.dtype is not _INT32:
+        raise TypeError("table and lens must be int32, got %s and %s" % (table.dtype, lens.dtype))
     batch = lens.numel()
     if lens.dim() != 1 or not lens.is_contiguous():
         raise ValueError("lens must be a contiguous vector")
-    if table.dim() != 2 or table.shape[0] != batch or (table.shape[1] > 1 and table.stride(1) != 1):
+    if len(span) != 2 or span[0] != batch or (span[1] > 1 and table.stride(1) != 1):
         raise ValueError("table must be [batch, width] with unit stride in its last dim")
+    width = span[1]
     if tokens % batch if batch else tokens:
         raise ValueError("q must have the same number of tokens for each of the %d sequences" % batch)
     m = tokens // batch if batch else 1
@@ -1140,10 +1146,12 @@ def ufp4_cache_attn(q, cache, table, lens, mask=None, scale=None, dtype=None, ou
         dtype = dtype or q.dtype
         if dtype not in _DTYPES:
             raise TypeError("out must be bf16 or fp32, got %s" % dtype)
-        out = _empty3((tokens, heads, dim), dtype, dev, on)
+        out = _empty((tokens, heads, dim), dtype, dev, on)
+        op, odt, old, oh = out.data_ptr(), _DTYPES[dtype], heads * dim, dim
     elif dtype is not None and out.dtype is not dtype:
         raise TypeError("out must be %s, got %s" % (dtype, out.dtype))
-    op, odt, old, oh, _ = _heads3d(out, "out", dev, heads, dim, tokens)
+    else:
+        op, odt, old, oh, _ = _heads3d(out, "out", dev, heads, dim, tokens)
     lp, want = None, lse is not None and lse is not False
     if want:
         if lse is True:
@@ -1153,9 +1161,14 @@ def ufp4_cache_attn(q, cache, table, lens, mask=None, scale=None, dtype=None, ou
         if lse.dtype is not _FLOAT32 or lse.shape != (tokens, heads) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous fp32 [%d, %d]" % (tokens, heads))
         lp = lse.data_ptr()
-    L, width = lib(), table.shape[1]
+    L = lib()
     if ws is None:
-        need = L.ufp4_cache_attn_workspace_bytes(batch, m, heads, width, cc)
+        sizes = (dev, batch, m, heads, width, cache.heads, cache.page, dim)
+        need = _attn_needs.get(sizes)
+        if need is None:
+            if len(_attn_needs) >= 4096:
+                _attn_needs.clear()
+            need = _attn_needs[sizes] = L.ufp4_cache_attn_workspace_bytes(batch, m, heads, width, cc)
         ws = _empty((need,), torch.uint8, dev, on) if need else None
     elif ws.get_device() != dev:
         _same_place(ws.get_device(), dev, "ws")

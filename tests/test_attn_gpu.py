@@ -370,7 +370,7 @@ def test_refusals(U):
                dict(q=torch.randn(130, 4, 64, device="cuda"))):
         with pytest.raises(U.UFP4Error):
             call(**kw)
-    long = Case(U, g, [4000], 1, 2, 1, 64, 16, 1, False, BF)
+    long = Case(U, g, [4000], 1, 2, 1, 64, 16, 1, False, BF, extra=4000)
     need = U.lib().ufp4_cache_attn_workspace_bytes(1, 1, 2, long.table.shape[1], long.cache.c())
     assert need > 0
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
