@@ -642,7 +642,8 @@ def run_kernel(args):
     after `warmup` launches, the tensor amax given (quant_resident_e1m2: W,
     F x H, both ways with its maxima, the on-chip single pass; quant_grouped_dual_e1m2:
     the MoE-7.9B X both ways, its amax pass included; moe_*, ckpt_*, swiglu*:
-    the calls around that layer's grouped GEMMs).  --shape dense: T, H, F =
+    the calls around that layer's grouped GEMMs; gemv*, cache_*: those that
+    answer with a quantized model).  --shape dense: T, H, F =
     8192, 2048, 5632; moe124b: 65536, 8192, 2048.  Prints the mean event
     time."""
     import torch
@@ -665,6 +666,9 @@ def run_kernel(args):
         return _run_kernel_timing(args, kind, fn, work, unit, dev)
     if kind.startswith(("moe_", "ckpt_", "swiglu")):
         calls = moe_calls(U, torch, dev, kinds=(kind.split("_")[0],))
+        return _run_kernel_timing(args, kind, *calls[kind], "GB/s", dev)
+    if kind.startswith(("gemv", "cache_")):
+        calls = serving_calls(U, torch, dev, kinds=(kind.split("_")[0],))
         return _run_kernel_timing(args, kind, *calls[kind], "GB/s", dev)
     wl = WORKLOAD if args.shape == "moe124b" else DENSE
     T, H, F = wl["tokens"], wl["hidden"], wl["ffn"]
@@ -764,6 +768,46 @@ def moe_calls(U, torch, dev, kinds=("moe", "ckpt", "swiglu")):
     return calls
 
 
+def serving_calls(U, torch, dev, kinds=("gemv", "cache")):
+    """The calls that answer with a quantized model: the dense-1.5B and the
+    MoE-7.9B layer's products for a few tokens, and a cache of 32 sequences of
+    8192 tokens (8 heads of 128) with the attention over it, of one token a
+    sequence and of trees of 32: name -> (call, algorithmic bytes)."""
+    from fp4_quantized_numerics_gb300 import inputs
+    calls, rot = {}, dict(rht=True, rht_seed=2)
+    if "gemv" in kinds:
+        H, F, E, K, T = 2048, 5632, 64, 6, 64
+        x = inputs.device_normal((T, H), 1.0, 51, dev)
+        w = U.ufp4_quantize(inputs.device_normal((F, H), 0.02, 52, dev), U.UFP4_E1M2, **rot)
+        big = U.ufp4_quantize(inputs.device_normal((65536, 8192), 0.02, 53, dev), U.UFP4_E2M1)
+        xb = inputs.device_normal((1, 8192), 1.0, 54, dev)
+        we = U.ufp4_quantize_grouped(inputs.device_normal((E * 2816, H), 0.02, 55, dev), U.UFP4_E1M2, [2816] * E, **rot)
+        plan = U.ufp4_moe_sort(torch.topk(inputs.device_normal((T, E), 1.0, 56, dev, torch.float32), K, dim=1).indices, E)
+        calls.update({
+            "gemv": (lambda: U.ufp4_gemv(x[:1], w, **rot), F * H * 0.5625),
+            "gemv_8": (lambda: U.ufp4_gemv(x[:8], w, **rot), F * H * 0.5625),
+            "gemv_wide": (lambda: U.ufp4_gemv(xb, big), big.rows * 8192 * 0.5625),
+            "gemv_grouped": (lambda: U.ufp4_gemv_grouped(x, we, plan, 2816, gather=True, **rot), E * 2816 * H * 0.5625),
+        })
+    if "cache" in kinds:
+        B, L, KV, H, D, page, m = 32, 8192, 8, 64, 128, 64, 32
+        cache = U.Cache.empty(B * L // page, KV, page, D, U.UFP4_E1M2, device=dev, **rot)
+        slots = torch.randperm(B * L, device=dev)
+        k, v = (inputs.device_normal((B * L, KV, D), 1.0, 57 + i, dev) for i in range(2))
+        U.ufp4_cache_append(k, v, slots, cache)
+        table = torch.arange(B * L // page, dtype=torch.int32, device=dev).view(B, -1)
+        lens = torch.full((B,), L, dtype=torch.int32, device=dev)
+        q = inputs.device_normal((B * m, H, D), 1.0, 59, dev)
+        row = D / 2 + D / 16 + 4
+        calls.update({
+            "cache_append": (lambda: U.ufp4_cache_append(k, v, slots, cache), 2 * B * L * KV * (2 * D + row)),
+            "cache_load": (lambda: U.ufp4_cache_load(cache, slots, k=k, v=v), 2 * B * L * KV * (2 * D + row)),
+            "cache_attn": (lambda: U.ufp4_cache_attn(q[:B], cache, table, lens), 2 * B * L * KV * row),
+            "cache_attn_tree": (lambda: U.ufp4_cache_attn(q, cache, table, lens), 2 * B * L * KV * row),
+        })
+    return calls
+
+
 def _run_kernel_timing(args, kind, fn, work, unit, dev):
     import torch
     flush = L2Flush(dev)
@@ -853,6 +897,7 @@ def run_all_kernels(args):
          2.0 * sum(counts) * 1408 * H, "F"),
     ]
     calls += [(name + " (MoE-7.9B)", fn, work, "B") for name, (fn, work) in moe_calls(U, torch, dev).items()]
+    calls += [(name, fn, work, "B") for name, (fn, work) in serving_calls(U, torch, dev).items()]
     out = []
     for name, fn, work, kind in calls:
         ms = _timeit(torch, fn, flush, max(args.steps, 1))
@@ -1167,7 +1212,8 @@ def build_parser():
                              "quant_dual_sr_e1m2", "amax_dual_e1m2",
                              "quant_row_e2m1", "quant_col_e2m1", "quant_grouped_dual_e1m2", "quant_resident_e1m2",
                              "moe_sort", "moe_dispatch", "moe_combine", "moe_combine_bwd", "ckpt_save", "ckpt_load",
-                             "swiglu", "swiglu_bwd", "all"],
+                             "swiglu", "swiglu_bwd", "gemv", "gemv_8", "gemv_wide", "gemv_grouped", "cache_append",
+                             "cache_load", "cache_attn", "cache_attn_tree", "all"],
                     help="time one kernel of the step in isolation (profiling); all: every public call once")
     return ap
 

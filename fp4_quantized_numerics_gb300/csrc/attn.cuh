@@ -20,7 +20,7 @@ struct AttnArgs {
     const int32_t *lens;
     const uint64_t *mask;
     int32_t batch, m, heads, kv, group, dim, rht, qtiles, splits;
-    uint64_t rht_seed;
+    uint32_t signs;              // of the rotation
     float scale;
     void *out;
     int64_t o_token, o_head;

@@ -258,7 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
 
     // ---- the queries as the 128-row operand: through shared memory to TMEM
     {
-        const uint32_t signs = a.rht ? rht_sign_mask(a.rht_seed) : 0u;
         const uint32_t group = ((1u << kBlocks) - 1u) << (lane & ~(kBlocks - 1));
         constexpr int kTasks = (kQ * kBlocks + kThreads - 1) / kThreads;
         const auto place = [&](int i) -> int64_t {
@@ -307,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                     for (int j = 0; j < 16; ++j) v[j] = __uint_as_float((uint32_t)p[j] << 16);
                 }
             }
-            if (a.rht) rotate16(v, signs);
+            if (a.rht) rotate16(v, a.signs);
             uint32_t top = top_bits(v);
 #pragma unroll
             for (int d = 1; d < kBlocks; d <<= 1) top = max(top, __shfl_xor_sync(group, top, d));
@@ -658,7 +657,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
             const int q = q0 + r, node = q / a.group, head = kvh * a.group + q % a.group;
             const int64_t token = (int64_t)b * a.m + node;
             const int64_t part = ((int64_t)blockIdx.y * a.batch * a.kv + bh) * (a.group * a.m) + q;
-            const uint32_t signs = a.rht && a.splits == 1 ? rht_sign_mask(a.rht_seed) : 0u;
 #pragma unroll 1
             for (int h = half * DC; h < (half + 1) * DC; ++h) {
                 uint32_t o[32];
@@ -678,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                         continue;
                     }
                     if (col >= a.dim) continue;
-                    if (a.rht) rotate16_back(v, signs);
+                    if (a.rht) rotate16_back(v, a.signs);
                     const int64_t at = token * a.o_token + head * a.o_head + col;
                     if (a.out_fp32) {
                         float *p = static_cast<float *>(a.out) + at;

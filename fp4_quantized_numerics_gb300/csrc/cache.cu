@@ -26,7 +26,7 @@ struct RowArgs {
     const int64_t *slots;
     int64_t places;              // pages x page
     int32_t heads, page_shift, dim, blocks, grid, rht;
-    uint64_t rht_seed;
+    uint32_t signs;              // of the rotation
     RowDiv by_heads;
     uint64_t rows;               // tokens x heads
 };
@@ -56,7 +56,7 @@ __device__ __forceinline__ void store16(T *p, bool wide, const float (&v)[16]) {
     }
 }
 
-template <class T, int G>       // G threads a row
+template <class T, int G, int GRID>       // G threads a row
 __global__ void __launch_bounds__(128) k_append(RowArgs a) {
     const uint32_t zero = begin_in_order();
     const int which = blockIdx.y;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(128) k_append(RowArgs a) {
     if (mine) {
         const T *p = static_cast<const T *>(a.x[which]) + token * a.ld_token[which] + h * a.ld_head[which] + b * 16;
         load16(p, a.wide, v);
-        if (a.rht) rotate16(v, rht_sign_mask(a.rht_seed));
+        if (a.rht) rotate16(v, a.signs);
     }
     float top = 0.0f;
 #pragma unroll
@@ -92,15 +92,14 @@ __global__ void __launch_bounds__(128) k_append(RowArgs a) {
     const float ev = e4m3_to_f32(e), r = e ? __fdiv_rn(enc, ev) : 0.0f;
     uint32_t w[2] = {0u, 0u};
     if (e) {
+        const float most = (float)grid_top(a.grid);
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-            const float p = __fmul_rn(v[i], r), q = __fmul_rn(v[i + 1], r);
             uint32_t two;
-            if (a.grid == kE2M1) {
-                two = e2m1x2_rn(p, q);
+            if constexpr (GRID == kE2M1) {
+                two = e2m1x2_rn(__fmul_rn(v[i], r), __fmul_rn(v[i + 1], r));
             } else {
-                const float most = (float)grid_top(a.grid);
-                two = e1m2_rn(p, most) | (e1m2_rn(q, most) << 4);
+                two = e1m2_rn(__fmul_rn(v[i], r), most) | (e1m2_rn(__fmul_rn(v[i + 1], r), most) << 4);
             }
             w[i / 8] |= two << (4 * (i % 8));
         }
@@ -113,7 +112,7 @@ __global__ void __launch_bounds__(128) k_append(RowArgs a) {
     if (b == 0) c.row_scale[to] = finite ? dec : __uint_as_float(0x7FC00000u);
 }
 
-template <class T, int G>
+template <class T, int G, int GRID>
 __global__ void __launch_bounds__(128) k_load(RowArgs a) {
     const uint32_t zero = begin_in_order();
     const int which = blockIdx.y;
@@ -129,14 +128,21 @@ __global__ void __launch_bounds__(128) k_load(RowArgs a) {
         const CacheHalf c = a.half[which];
         const int64_t from = cache_row(slot, h, a.heads, a.page_shift);
         const uint2 w = *reinterpret_cast<const uint2 *>(c.codes + from * (a.blocks * 8) + b * 8);
-        const float e = e4m3_to_f32(c.scales[from * a.blocks + b]), s = c.row_scale[from];
+        // value times block scale is exact in FP16; one rounding, by the row's scale
+        const uint32_t e = scale_pair(c.scales[from * a.blocks + b], 0u);
+        const float s = c.row_scale[from] * kDecoded<GRID>;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t code = (i < 8 ? w.x : w.y) >> (4 * (i % 8));
-            const float m = __fmul_rn(grid_value(a.grid, code), e);
-            v[i] = __fmul_rn(code & 8u ? -m : m, s);
+        for (int i = 0; i < 2; ++i) {
+            uint32_t p[4];
+            decode8<GRID>(i ? w.y : w.x, p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = f16_unpair(mul_pair(p[j], e));
+                v[8 * i + code_order<GRID>(2 * j)] = __fmul_rn(f.x, s);
+                v[8 * i + code_order<GRID>(2 * j + 1)] = __fmul_rn(f.y, s);
+            }
         }
-        if (a.rht) rotate16_back(v, rht_sign_mask(a.rht_seed));
+        if (a.rht) rotate16_back(v, a.signs);
     }
     T *p = static_cast<T *>(a.y[which]) + token * a.ld_token[which] + h * a.ld_head[which] + b * 16;
     store16(p, a.wide, v);
@@ -204,7 +210,7 @@ __device__ __forceinline__ void finish_row(const AttnArgs &a, float (&o)[8], flo
     for (int i = 0; i < 8; ++i) o[i] *= inv;
     if (a.rht) {
         // the butterflies of 16 over two neighbouring lanes
-        const uint32_t signs = rht_sign_mask(a.rht_seed) >> (lane & 1) * 8;
+        const uint32_t signs = a.signs >> (lane & 1) * 8;
         fwht8(o);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -334,7 +340,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
     }
 
     // ---- the queries as operands: [plane][word of a lane's elements][query][lane % 4]
-    const uint32_t signs = a.rht ? rht_sign_mask(a.rht_seed) : 0u;
     uint64_t seen = 0;
     for (int i = tid; i < kQ * kBlocks; i += kAttnWarps * 32) {
         const int col = i / kBlocks, blk = i % kBlocks, q = q0 + col;
@@ -364,7 +369,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
                     for (int j = 0; j < 16; ++j) v[j] = __uint_as_float((uint32_t)p[j] << 16);
                 }
             }
-            if (a.rht) rotate16(v, signs);
+            if (a.rht) rotate16(v, a.signs);
         }
         uint32_t top = top_bits(v);
 #pragma unroll
@@ -847,7 +852,7 @@ RowArgs row_args(const CacheRows &l) {
     a.blocks = l.cache.padded / 16;
     a.grid = l.cache.grid;
     a.rht = l.cache.rht;
-    a.rht_seed = l.cache.rht_seed;
+    a.signs = l.cache.rht ? host_rht_sign_mask(l.cache.rht_seed) : 0u;
     a.by_heads = make_rowdiv((uint32_t)l.cache.heads);
     a.rows = (uint64_t)l.tokens * l.cache.heads;
     return a;
@@ -860,8 +865,13 @@ cudaError_t launch_cache_append(const CacheRows &l, cudaStream_t s) {
     return by_threads(a.blocks, [&](auto g) {
         constexpr int G = decltype(g)::value;
         const dim3 grid((unsigned)((a.rows * G + 127) / 128), 2);
-        return a.fp32 ? launch_in_order_smem(k_append<float, G>, grid, 128, 0, 1, s, a)
-                      : launch_in_order_smem(k_append<__nv_bfloat16, G>, grid, 128, 0, 1, s, a);
+        const auto with = [&](auto gr) {
+            constexpr int K = decltype(gr)::value;
+            return a.fp32 ? launch_in_order_smem(k_append<float, G, K>, grid, 128, 0, 1, s, a)
+                          : launch_in_order_smem(k_append<__nv_bfloat16, G, K>, grid, 128, 0, 1, s, a);
+        };
+        // (the clamped grid rounds as the uniform one does)
+        return a.grid == kE2M1 ? with(Int<kE2M1>()) : with(Int<kE1M2>());
     });
 }
 
@@ -870,8 +880,12 @@ cudaError_t launch_cache_load(const CacheRows &l, cudaStream_t s) {
     return by_threads(a.blocks, [&](auto g) {
         constexpr int G = decltype(g)::value;
         const dim3 grid((unsigned)((a.rows * G + 127) / 128), 2);
-        return a.fp32 ? launch_in_order_smem(k_load<float, G>, grid, 128, 0, 1, s, a)
-                      : launch_in_order_smem(k_load<__nv_bfloat16, G>, grid, 128, 0, 1, s, a);
+        const auto with = [&](auto gr) {
+            constexpr int K = decltype(gr)::value;
+            return a.fp32 ? launch_in_order_smem(k_load<float, G, K>, grid, 128, 0, 1, s, a)
+                          : launch_in_order_smem(k_load<__nv_bfloat16, G, K>, grid, 128, 0, 1, s, a);
+        };
+        return a.grid == kE1M2 ? with(Int<kE1M2>()) : with(Int<kE2M1>());
     });
 }
 
@@ -905,7 +919,7 @@ cudaError_t launch_cache_attn(const CacheAttn &l, cudaStream_t s) {
     a.group = l.heads / l.cache.heads;
     a.dim = l.cache.dim;
     a.rht = l.cache.rht;
-    a.rht_seed = l.cache.rht_seed;
+    a.signs = l.cache.rht ? host_rht_sign_mask(l.cache.rht_seed) : 0u;
     a.scale = l.scale;
     a.out = l.out;
     a.o_token = l.o_token;

@@ -77,6 +77,22 @@ __device__ __forceinline__ uint32_t rht_sign_mask(uint64_t seed) {
     return w.x & 0xFFFFu;
 }
 
+// The same on the host, for kernels that take the mask as an argument.
+inline uint32_t host_rht_sign_mask(uint64_t seed) {
+    uint32_t c[4] = {0u, 0u, 0u, 0u}, k[2] = {(uint32_t)seed, (uint32_t)(seed >> 32)};
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = 0xD2511F53ull * c[0], b = 0xCD9E8D57ull * c[2];
+        const uint32_t n0 = (uint32_t)(b >> 32) ^ c[1] ^ k[0], n2 = (uint32_t)(a >> 32) ^ c[3] ^ k[1];
+        c[1] = (uint32_t)b;
+        c[3] = (uint32_t)a;
+        c[0] = n0;
+        c[2] = n2;
+        k[0] += 0x9E3779B9u;
+        k[1] += 0xBB67AE85u;
+    }
+    return c[0] & 0xFFFFu;
+}
+
 // ------------------------------------------------------------- E4M3 codec
 // fp32 -> E4M3, round to nearest even, saturating to +-448 (hardware cvt).
 __device__ __forceinline__ uint32_t e4m3_from_f32(float v) {

@@ -49,7 +49,7 @@ struct GemvArgs {
     int64_t ld_x;
     int32_t x_fp32, x_wide;      // wide: 16-byte loads
     int32_t rht;
-    uint64_t rht_seed;
+    uint32_t signs;              // of the rotation
     const uint8_t *codes, *scales;
     const float *tensor_scale;
     int32_t k, kpad;
@@ -154,7 +154,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
     const int begin = a.offsets ? (int)((int64_t)total * blockIdx.x / gridDim.x) : 0;
     const int end = a.offsets ? (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x) : total;
     if (begin >= end) return;
-    const uint32_t signs = a.rht ? rht_sign_mask(a.rht_seed) : 0u;
     const int nkt = a.kpad >> 6;
     const int64_t row_bytes = a.kpad >> 1, row_step = 32 * row_bytes;
 
@@ -291,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
                             for (int q = 0; q < 16; ++q) v[q] = __uint_as_float((uint32_t)p[q] << 16);
                         }
                     }
-                    if (a.rht) rotate16(v, signs);
+                    if (a.rht) rotate16(v, a.signs);
                 } else {
 #pragma unroll
                     for (int q = 0; q < 16; ++q) v[q] = 0.0f;
@@ -531,7 +530,7 @@ cudaError_t launch_gemv(const GemvLaunch &l, cudaStream_t s) {
     a.x_fp32 = l.x_dtype == 1;
     a.x_wide = rows_by(l.x, l.ld_x, type_size(l.x_dtype), a.x_fp32 ? 4 : 8);
     a.rht = l.rht;
-    a.rht_seed = l.rht_seed;
+    a.signs = l.rht ? host_rht_sign_mask(l.rht_seed) : 0u;
     a.codes = l.codes;
     a.scales = l.scales;
     a.tensor_scale = l.tensor_scale;

@@ -141,7 +141,10 @@ CASES = [([1], 1, 1, 1, 16, 16), ([1, 0, 2], 1, 2, 1, 64, 16), ([15, 16, 17], 1,
          ([31, 32, 33, 64], 1, 8, 1, 64, 32), ([127, 128, 129, 300], 1, 8, 2, 128, 64), ([1000], 1, 32, 8, 128, 64),
          ([5000], 1, 3, 1, 80, 128), ([700, 3, 0, 257], 2, 6, 3, 128, 16), ([40, 90], 5, 10, 2, 128, 32),
          ([64, 65, 200], 64, 2, 2, 64, 16), ([500, 129], 17, 8, 2, 128, 64), ([300, 77], 3, 4, 2, 256, 32),
-         ([900], 1, 7, 1, 144, 64), ([150], 64, 8, 1, 128, 16), ([3, 10], 8, 4, 4, 64, 16)]
+         ([900], 1, 7, 1, 144, 64), ([150], 64, 8, 1, 128, 16), ([3, 10], 8, 4, 4, 64, 16),
+         # (more than 16 queries a head: one token of a wide group, groups past 128 queries, splits, short and empty ones)
+         ([333, 0, 64], 1, 20, 1, 128, 32), ([63, 64, 65, 129], 5, 8, 2, 64, 16), ([3000, 17], 9, 30, 2, 80, 64),
+         ([12000], 3, 32, 2, 128, 64)]
 
 
 @pytest.mark.parametrize("lens,m,heads,kv,dim,page", CASES)
