@@ -53,7 +53,7 @@ constexpr int kSoftWarps = 8, kDecodeWarps = 8, kThreads = (kSoftWarps + kDecode
 constexpr int kGroups = 2, kGroupWarps = kDecodeWarps / kGroups;   // decoding warps take every second tile,
 constexpr int kWarpKeys = kKeys / kGroupWarps;                     // 16 rows of it each
 constexpr long long kWaitBudget = 2000000000LL;          // SM clocks: about a second
-// TMEM: O, S of two tiles, Q's two FP16 values, P's.
+// TMEM: O, S of two tiles, Q's two FP16 values, P's of two tiles.
 constexpr uint32_t kTmemCols = 512, kColS = 128, kColQ = 256, kColP = 384;
 
 template <int DC>
@@ -72,7 +72,7 @@ struct Smem {
     static constexpr int kOffRow = kOffValues + kSoftWarps * kKeys * 4;             // of each query: mask, scale,
     static constexpr int kOffTop = kOffRow + kQ * 12;                               // its two threads' maxima or sums
     static constexpr int kOffBar = kOffTop + kQ * 8;
-    static constexpr int kBars = 2 * kStages + 4;
+    static constexpr int kBars = 2 * kStages + 6;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16;
 };
 
@@ -169,7 +169,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
     const auto full = [&](int s) { return bars + s * 8; };                          // a stage is decoded
     const auto empty = [&](int s) { return bars + (kStages + s) * 8; };             // its MMAs are done
     const auto s_full = [&](int i) { return bars + (2 * kStages + i) * 8; };        // scores are in TMEM
-    const uint32_t p_ready = bars + (2 * kStages + 2) * 8, pv_done = p_ready + 8;   // probabilities are; O has them
+    // of every second tile: its probabilities are in TMEM; O has them
+    const auto p_ready = [&](int i) { return bars + (2 * kStages + 2 + (i & 1)) * 8; };
+    const auto pv_done = [&](int i) { return bars + (2 * kStages + 4 + (i & 1)) * 8; };
     uint32_t *const slot = reinterpret_cast<uint32_t *>(smem + M::kOffBar + M::kBars * 8);
     volatile uint32_t *const stop = slot + 1;
     const uint32_t zero = begin_in_order();
@@ -186,16 +188,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
     if (warp == kSoftWarps + kDecodeWarps) {
         ptx::tmem_alloc(ptx::smem_u32(slot), kTmemCols);
         ptx::tmem_relinquish();
-        if (lane == 0) {
+        if (ptx::elect_one()) {
             *stop = 0;
             for (int s = 0; s < kStages; ++s) {
                 ptx::mbar_init(full(s), kGroupWarps);
                 ptx::mbar_init(empty(s), 1);
             }
-            ptx::mbar_init(s_full(0), 1);
-            ptx::mbar_init(s_full(1), 1);
-            ptx::mbar_init(p_ready, kSoftWarps * 32);
-            ptx::mbar_init(pv_done, 1);
+            for (int i = 0; i < 2; ++i) {
+                ptx::mbar_init(s_full(i), 1);
+                ptx::mbar_init(p_ready(i), kSoftWarps * 32);
+                ptx::mbar_init(pv_done(i), 1);
+            }
             ptx::fence_mbar_init();
         }
     }
@@ -440,10 +443,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else if (warp == kSoftWarps + kDecodeWarps) {
         // ------------------------------------------------------- the products
-        if (lane == 0) {
+        if (ptx::elect_one()) {
             // Descriptors of the first stage; a stage, panel or step further
-            // is an addition (of 16-byte units) to the low word.  One thread's
-            // instructions are what the products take, so they are few.
+            // is an addition (of 16-byte units) to the low word.
             const uint64_t keys = ptx::sdesc(smem_s, 16, 1024, 2);
             const uint64_t values = ptx::sdesc(smem_s + M::kHalf, M::kPanel, 1024, 2);
             const auto scores = [&](int i, int stage, uint32_t parity) -> bool {
@@ -476,20 +478,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                     ahead = 0;
                     ++ahead_round;
                 }
-                if (!(ok = wait(p_ready, i & 1))) break;
+                if (!(ok = wait(p_ready(i), (i >> 1) & 1))) break;
                 ptx::tc_fence_after();
                 const uint64_t vd = values + (uint32_t)stage * (M::kStage / 16);
-                if (i == 0) mma_f16_ts<false>(tmem, tmem + kColP, vd, idesc(kDim, true));
-                else mma_f16_ts<true>(tmem, tmem + kColP, vd, idesc(kDim, true));
+                const uint32_t p_col = tmem + kColP + (i & 1) * 64;
+                if (i == 0) mma_f16_ts<false>(tmem, p_col, vd, idesc(kDim, true));
+                else mma_f16_ts<true>(tmem, p_col, vd, idesc(kDim, true));
 #pragma unroll
                 for (int k = 1; k < kKeys / 16; ++k)
-                    mma_f16_ts<true>(tmem, tmem + kColP + k * 8, vd + k * 128, idesc(kDim, true));
+                    mma_f16_ts<true>(tmem, p_col + k * 8, vd + k * 128, idesc(kDim, true));
                 if constexpr (TWO)
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        mma_f16_ts<true>(tmem, tmem + kColP + 32 + k * 8, vd + k * 128, idesc(kDim, true));
+                        mma_f16_ts<true>(tmem, p_col + 32 + k * 8, vd + k * 128, idesc(kDim, true));
                 ptx::tc_commit(empty(stage));
-                ptx::tc_commit(pv_done);
+                ptx::tc_commit(pv_done(i));
                 if (++stage == kStages) stage = 0;
             }
             if (!ok) {       // what was issued ends before TMEM is given back
@@ -571,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                 other = max3(other, v.x, v.y);
             }
             top = fmaxf(top, other) * qscale;
-            // O and the place of the probabilities are the last tile's until its product is done
-            ok = i == 0 || wait(pv_done, (i - 1) & 1);
+            // the place of the probabilities was the last but one tile's
+            ok = i < 2 || wait(pv_done(i), ((i >> 1) - 1) & 1);
             const bool rise = either(top > mx + (float)slack || ve_new > ve || !ok);
             ptx::tc_fence_after();
             if (rise) {
@@ -585,6 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                 l *= back;
                 ve = ve_new;
                 if (i > 0) {
+                    // O has the last tile's product first
+                    if (either(!wait(pv_done(i - 1), ((i - 1) >> 1) & 1))) return false;
+                    ptx::tc_fence_after();
 #pragma unroll 1
                     for (int h = 0; h < kDim / 64; ++h) {
                         uint32_t o[32];
@@ -622,8 +628,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                         if constexpr (TWO) lo[j + e] = f16_rest(x.x, x.y, hi[j + e]);
                     }
                 }
-                tc_st_32x32b_x8(tm + kColP + half * 16 + c / 2, hi);
-                if constexpr (TWO) tc_st_32x32b_x8(tm + kColP + 32 + half * 16 + c / 2, lo);
+                const uint32_t to = tm + kColP + (i & 1) * 64 + half * 16 + c / 2;
+                tc_st_32x32b_x8(to, hi);
+                if constexpr (TWO) tc_st_32x32b_x8(to + 32, lo);
             }
             const float2 two = unpack2(add2(sums[0], sums[1]));
             l += two.x + two.y;
@@ -640,13 +647,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                 break;
             }
             ptx::tc_fence_before();
-            ptx::mbar_arrive(p_ready);
+            ptx::mbar_arrive(p_ready(i));
             if (++stage == kStages) {
                 stage = 0;
                 ++round;
             }
         }
-        if (ok && tiles > 0) ok = wait(pv_done, (tiles - 1) & 1);
+        if (ok && tiles > 0) ok = wait(pv_done(tiles - 1), ((tiles - 1) >> 1) & 1);
         tops[half * kQ + r] = l;
         ok = !either(!ok);
         ptx::tc_fence_after();
