@@ -520,10 +520,15 @@ cudaError_t dispatch(const GemvArgs &a, int grid, int most_cols, cudaStream_t s)
         if (a.y_fp32 && (a.rht || a.x_fp32)) e = launch<G, M, N, 2>(a, most_cols, s);
         else e = launch<G, M, N, 1>(a, most_cols, s);
     };
+    // Columns of a pass.  16384 x 4096 E1M2, rotated BF16 tokens, us: 8 tokens
+    // 23; 16 tokens 36 as 16 columns, 46 as two passes of 8; 32 tokens 67 as
+    // 32 columns of 16-row tiles (more would not leave registers for 32), 77 as
+    // two passes of 16, 137 as four of 8.  By expert, where columns are what an
+    // expert happens to have and passes after the first read L2, 8: 256 tokens x
+    // 6 of 64 experts of 2048 x 2048 157, with 16 columns 171.
     auto by_cols = [&](auto gr) {
-        // (by expert: for as many tokens as one has on average)
-        if (most_cols <= 8 || (a.offsets && a.slots <= 8 * (int64_t)a.n_experts)) with(gr, Int<2>(), Int<1>());
-        else if (most_cols <= 16 || a.offsets) with(gr, Int<2>(), Int<2>());
+        if (most_cols <= 8 || a.offsets) with(gr, Int<2>(), Int<1>());
+        else if (most_cols <= 16) with(gr, Int<2>(), Int<2>());
         else with(gr, Int<1>(), Int<4>());
     };
     if (grid == kE1M2) by_cols(Int<kE1M2>());
@@ -559,8 +564,8 @@ cudaError_t launch_gemv(const GemvLaunch &l, cudaStream_t s) {
     a.topk = l.topk;
     a.gather = l.gather;
     a.chunks = (a.kpad + kChunk - 1) / kChunk;
-    // By expert, columns for what one mostly has: a token each.  (One that a
-    // token names twice may have more, in further passes.)
+    // By expert: no more columns than tokens.  (An expert that a token names
+    // twice may have more, in further passes.)
     return dispatch(a, l.grid, (int)(l.offsets ? std::min(l.slots, l.tokens) : l.tokens), s);
 }
 

@@ -575,7 +575,8 @@ UFP4_API ufp4_status ufp4_swiglu_bwd(const void *dh, int32_t dh_dtype, int64_t l
  * a BF16 element not rotated enters exactly, one rotated or FP32 within 2^-22
  * of itself where y is FP32 and 2^-11 where y is BF16 (which keeps 2^-8), each
  * down to 2^-29 of the largest among the 128 it lies with.
- * Made for 1 to 32 tokens; further ones read w once more per 32.
+ * Made for 1 to 32 tokens; further ones read w once more per 32 (by expert,
+ * below, per 8).
  *   x : tokens x w->k;  y : tokens x w->rows.  w->k <= UFP4_MAX_WIDTH.
  * w->k = 0 writes zeros.  w->eplane is not read. */
 UFP4_API ufp4_status ufp4_gemv(const void *x, int32_t x_dtype, int64_t tokens, int64_t ld_x, const ufp4_qtensor *w,
