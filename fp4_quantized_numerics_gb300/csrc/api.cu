@@ -682,7 +682,7 @@ ufp4_status ufp4_gemv(const void *x, int32_t x_dtype, int64_t tokens, int64_t ld
     if (st != UFP4_OK) return st;
     if (!valid_rows(x, x_dtype, tokens, w->k, ld_x) || !valid_rows(y, y_dtype, tokens, w->rows, ld_y))
         return UFP4_ERR_INVALID;
-    if (std::max({tokens, ld_x, ld_y}) > UFP4_MAX_DIM) return UFP4_ERR_UNSUPPORTED;
+    if (tokens > UFP4_GEMV_MAX_TOKENS || std::max(ld_x, ld_y) > UFP4_MAX_DIM) return UFP4_ERR_UNSUPPORTED;
     if (tokens == 0 || w->rows == 0) return UFP4_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (w->k == 0) return write_zeros(y, y_dtype, tokens, w->rows, ld_y, s);

@@ -20,7 +20,7 @@
 //    there; it is scaled, and the two threads of a query speak, only when a
 //    maximum rises by more than 2^8 or a larger row scale appears.
 // Measured: trees of 32 tokens, 8 sequences of 8192 to 16384 keys, 32 heads over
-// 8, E1M2 rotated, 139 us (383 TFLOP/s of the definition's; twice the queries'
+// 8, E1M2 rotated, 140 us (380 TFLOP/s of the definition's; twice the queries'
 // product in fact).  A tile of 64 keys takes some 5400 instructions (softmax 2200,
 // decoding 1600, copies 400, the CTA's start 600) at 1.9 an SM and clock; without
 // the decoding 114 us.  A CTA's start and end take 8 us of that, three times over.

@@ -800,7 +800,7 @@ struct Shape {
     int nt, qtiles, resident, start;
 };
 Shape shape_of(int64_t queries, int64_t padded) {
-    if (queries > 16 && padded <= 128) return Shape{0, (int)((queries + kWideQueries - 1) / kWideQueries), 1, 256};
+    if (queries > 16 && padded <= 128) return Shape{0, (int)((queries + kWideQueries - 1) / kWideQueries), 1, 768};
     const int nt = queries <= 8 || padded > 128 ? 1 : 2;
     return Shape{nt, (int)((queries + 8 * nt - 1) / (8 * nt)), nt == 1 && padded <= 128 ? 4 : 2, 64};
 }

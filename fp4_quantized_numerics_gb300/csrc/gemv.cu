@@ -51,7 +51,7 @@ namespace {
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kChunk = 128;                    // elements of a row that 4 lanes hold
 constexpr int kAhead = 2;                      // chunks of a warp under way
-constexpr uint32_t kSharedBudget = 112 * 1024; // two CTAs on an SM
+constexpr uint32_t kSharedBudget = 110 * 1024; // two CTAs on an SM, with 1 KB each that is not dynamic, and the system's
 constexpr uint32_t kSumsBudget = 16 * 1024;    // sums that wait between phases
 
 struct GemvArgs {

@@ -577,8 +577,10 @@ UFP4_API ufp4_status ufp4_swiglu_bwd(const void *dh, int32_t dh_dtype, int64_t l
  * down to 2^-29 of the largest among the 128 it lies with.
  * Made for 1 to 32 tokens; further ones read w once more per 32 (by expert,
  * below, per 8).
- *   x : tokens x w->k;  y : tokens x w->rows.  w->k <= UFP4_MAX_WIDTH.
+ *   x : tokens x w->k;  y : tokens x w->rows.  w->k <= UFP4_MAX_WIDTH,
+ *   tokens <= UFP4_GEMV_MAX_TOKENS.
  * w->k = 0 writes zeros.  w->eplane is not read. */
+#define UFP4_GEMV_MAX_TOKENS (1LL << 30)
 UFP4_API ufp4_status ufp4_gemv(const void *x, int32_t x_dtype, int64_t tokens, int64_t ld_x, const ufp4_qtensor *w,
                                int32_t rht, uint64_t rht_seed, void *y, int32_t y_dtype, int64_t ld_y,
                                ufp4_stream_t stream);

@@ -143,7 +143,8 @@ def attn(q, k, v, rows, sees, scale, planes_exact, out_two, top_v, dim):
     rel = np.expm1(de).max(-1, keepdims=True, initial=0.0)
     w_abs = w @ np.abs(v)
     tol = w_abs * (2 * rel + (2.0 ** -21 if out_two else 2.0 ** -11) + 2 * n * U23)
-    # probabilities below FP16's normal numbers: half a step of 2^-24, in units of 2^-11 of the largest row's scale
-    tol = tol + n * 2.0 ** -36 * top_v / np.where(z > 0, z, 1)
+    # probabilities below FP16's normal numbers: half a step of 2^-24, in units of the power of two that they are
+    # multiplied by, 2^11 over the largest row's scale for fp32 results and 2^6 for bf16 ones of many queries
+    tol = tol + n * 2.0 ** (-36 if out_two else -31) * top_v / np.where(z > 0, z, 1)
     lse_tol = rel[:, 0] + n[:, 0] * U23 + np.abs(np.where(np.isfinite(lse), lse, 0)) * 4 * U24 + 2.0 ** -20
     return out, lse, tol, lse_tol

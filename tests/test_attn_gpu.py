@@ -194,17 +194,19 @@ def test_a_long_sequence_beside_short_ones(U, dim, page):
     c.check(*U.ufp4_cache_attn(**c.args(), lse=True), dtype=FP)
 
 
-def test_keys_and_values_of_differing_size(U):
+@pytest.mark.parametrize("heads", [8, 40])
+def test_keys_and_values_of_differing_size(U, heads):
     """Rows whose scales differ by 2^24, scores far apart."""
     g = np.random.default_rng(9)
-    c = Case(U, g, [777], 1, 8, 2, 128, 32, 0, False, FP, sizes=12)
+    c = Case(U, g, [777], 1, heads, 2, 128, 32, 0, False, FP, sizes=12)
     c.check(*U.ufp4_cache_attn(**c.args(), lse=True, scale=2.0 ** -12), scale=2.0 ** -12, dtype=FP)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.25, 1e-4, 3.0])
-def test_scales(U, scale):
+@pytest.mark.parametrize("heads", [8, 16])
+def test_scales(U, scale, heads):
     g = np.random.default_rng(10)
-    c = Case(U, g, [300], 3, 8, 2, 64, 32, 1, False, FP)
+    c = Case(U, g, [300], 3, heads, 2, 64, 32, 1, False, FP)
     c.check(*U.ufp4_cache_attn(**c.args(), lse=True, scale=scale), scale=scale, dtype=FP)
 
 
@@ -218,10 +220,11 @@ def test_lengths_past_the_table(U):
     assert torch.equal(got, want) and bool((got[1] == 0).all())
 
 
-def test_pages_outside_the_cache(U):
+@pytest.mark.parametrize("heads", [2, 20])
+def test_pages_outside_the_cache(U, heads):
     """They read as rows of zeros, whatever their number."""
     g = np.random.default_rng(12)
-    c = Case(U, g, [64], 1, 2, 1, 64, 16, 1, False, FP)
+    c = Case(U, g, [64], 1, heads, 1, 64, 16, 1, False, FP)
     for bad in (-1, c.cache.pages, 2 ** 31 - 1, -2 ** 31):
         c.table[0, 1] = bad
         out, lse = U.ufp4_cache_attn(**c.args(), lse=True)
@@ -229,44 +232,47 @@ def test_pages_outside_the_cache(U):
 
 
 @pytest.mark.parametrize("where", ["k", "v"])
-def test_non_finite_rows(U, where):
+@pytest.mark.parametrize("heads", [4, 16])         # (12 and 48 queries a head of the cache)
+def test_non_finite_rows(U, where, heads):
     """A NaN row reaches the queries that see it, and no other."""
     g = np.random.default_rng(13)
     mask = _tree(g, 2, 6)
-    c = Case(U, g, [70, 40], 6, 4, 2, 64, 16, 1, False, FP, mask=mask)
+    c = Case(U, g, [70, 40], 6, heads, 2, 64, 16, 1, False, FP, mask=mask)
     clean, _ = U.ufp4_cache_attn(**c.args(), lse=True)
     j, head = 40 - 6 + 2, 1                     # new token 2 of the second sequence, the cache's second head
     page, at = int(c.table[1, j // 16]), j % 16
     getattr(c.cache, where + "_row_scale")[page, head, at] = float("nan")
     out, _ = U.ufp4_cache_attn(**c.args(), lse=True)
-    hit = torch.zeros(12, 4, dtype=torch.bool, device="cuda")
+    hit = torch.zeros(12, heads, dtype=torch.bool, device="cuda")
     for i in range(6):
         if int(mask[1, i]) >> 2 & 1:
-            hit[6 + i, 2:] = True
+            hit[6 + i, heads // 2:] = True
     assert bool(hit.any()) and bool(torch.isnan(out[hit]).all()) and torch.equal(out[~hit], clean[~hit])
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_non_finite_queries(U, bad):
+@pytest.mark.parametrize("heads", [4, 24])
+def test_non_finite_queries(U, bad, heads):
     g = np.random.default_rng(14)
-    c = Case(U, g, [70, 40], 3, 4, 2, 64, 16, 1, True, FP)
+    c = Case(U, g, [70, 40], 3, heads, 2, 64, 16, 1, True, FP)
     clean = U.ufp4_cache_attn(**c.args())
     c.q[4, 1, 5] = bad
     out = U.ufp4_cache_attn(**c.args())
-    hit = torch.zeros(6, 4, dtype=torch.bool, device="cuda")
+    hit = torch.zeros(6, heads, dtype=torch.bool, device="cuda")
     hit[4, 1] = True
     assert bool(torch.isnan(out[hit]).all()) and torch.equal(out[~hit], clean[~hit])
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
-def test_strides(U, dtype):
+@pytest.mark.parametrize("m", [2, 9])              # (6 and 27 queries a head of the cache)
+def test_strides(U, dtype, m):
     """q and out inside wider tensors, off their alignment; the rest stays."""
     g = np.random.default_rng(15)
-    c = Case(U, g, [100, 33], 2, 6, 2, 48, 16, 0, True, dtype)
+    c = Case(U, g, [100, 33], m, 6, 2, 48, 16, 0, True, dtype)
     want = U.ufp4_cache_attn(**c.args())
-    wide = torch.full((4, 9, 51), 3.0, device="cuda", dtype=dtype)
+    wide = torch.full((2 * m, 9, 51), 3.0, device="cuda", dtype=dtype)
     wide[:, 2:8, 1:49] = c.q
-    res = torch.full((4, 7, 53), 4.0, device="cuda", dtype=dtype)
+    res = torch.full((2 * m, 7, 53), 4.0, device="cuda", dtype=dtype)
     args = dict(c.args(), q=wide[:, 2:8, 1:49], out=res[:, 1:, 3:51])
     table = torch.full((2, c.table.shape[1] + 5), 99, dtype=torch.int32, device="cuda")
     table[:, :c.table.shape[1]] = args["table"]

@@ -52,7 +52,7 @@ def test_gemv_refusals(U):
     assert L.ufp4_gemv(P, 0, 3, 64, None, 0, 7, P, 1, 128, None) == INV
     assert call(w=_w(U, grid=U.UFP4_MXFP4)) == UNS
     assert call(w=_w(U, k=1 << 25), ld=1 << 25) == UNS
-    assert call(ld=1 << 31) == UNS and call(ly=1 << 31) == UNS
+    assert call(ld=1 << 31) == UNS and call(ly=1 << 31) == UNS and call(t=(1 << 30) + 1) == UNS
     assert call(t=0, x=None, y=None) == U.UFP4_OK
     assert call(w=_w(U, rows=0, codes=None, scales=None, ts=None), y=None, ly=0) == U.UFP4_OK
 
