@@ -747,7 +747,7 @@ size_t ufp4_cache_attn_workspace_bytes(int64_t batch, int32_t m, int32_t heads, 
                                        const ufp4_cache *cache) {
     Cache c;
     if (check_cache(cache, &c) != UFP4_OK || batch <= 0 || m < 1 || m > UFP4_MAX_NEW || heads < 1 || width < 0 ||
-        heads % c.heads || width > UFP4_MAX_DIM >> c.page_shift || batch > UFP4_MAX_DIM / heads / m)
+        heads % c.heads || width > UFP4_MAX_KEYS >> c.page_shift || batch > UFP4_MAX_DIM / heads / m)
         return 0;
     return cache_attn_workspace(batch, m, heads, c.heads, c.padded, width << c.page_shift);
 }
@@ -769,7 +769,7 @@ ufp4_status ufp4_cache_attn(const void *q, int32_t q_dtype, int64_t ld_q, int64_
     if (batch > 0 && (!lens || !aligned(lens, 4) || (width > 0 && (!table || !aligned(table, 4)))))
         return UFP4_ERR_INVALID;
     if ((mask && !aligned(mask, 8)) || (lse && !aligned(lse, 4)) || !(scale - scale == 0.0f)) return UFP4_ERR_INVALID;
-    if (m > UFP4_MAX_NEW || width > UFP4_MAX_DIM >> l.cache.page_shift || ld_table > UFP4_MAX_DIM ||
+    if (m > UFP4_MAX_NEW || width > UFP4_MAX_KEYS >> l.cache.page_shift || ld_table > UFP4_MAX_DIM ||
         batch > UFP4_MAX_DIM / heads / m || !strides_within_limits(ld_q, head_q) ||
         !strides_within_limits(ld_out, head_out))
         return UFP4_ERR_UNSUPPORTED;

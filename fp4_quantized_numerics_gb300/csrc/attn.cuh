@@ -38,7 +38,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// Keys [first, last) of a sequence of `len` that split s of n takes.
+// Keys [first, last) of a sequence of `len` (at most UFP4_MAX_KEYS, so that a
+// tile past its end fits 32 bits) that split s of n takes.
 __device__ __forceinline__ int split_keys(int len, int n) {
     return max((len + n - 1) / n + kSplitKeys - 1, kSplitKeys) / kSplitKeys * kSplitKeys;
 }

@@ -656,6 +656,7 @@ UFP4_API ufp4_status ufp4_cache_load(const ufp4_cache *cache, const int64_t *slo
                                      ufp4_stream_t stream);
 
 #define UFP4_MAX_NEW 64
+#define UFP4_MAX_KEYS (1LL << 30)
 
 /* Attention of each sequence's last m tokens over its rows of the cache:
  *   out[b m + i][h] = sum over j of p_j V[j],  p = softmax(scale q . K[j]),
@@ -677,7 +678,7 @@ UFP4_API ufp4_status ufp4_cache_load(const ufp4_cache *cache, const int64_t *slo
  *            (-infinity where nothing is seen), or NULL;
  *   workspace: ufp4_cache_attn_workspace_bytes(...) bytes, 16-byte aligned, of
  *            this call until it has run (NULL where that is 0).
- * heads a multiple of cache->heads; m 1 .. UFP4_MAX_NEW; width * page < 2^31.
+ * heads a multiple of cache->heads; m 1 .. UFP4_MAX_NEW; width * page <= UFP4_MAX_KEYS.
  * Scores are fp32, of q as ufp4_gemv takes x for an FP32 y; the probabilities enter the sum
  * over V as FP16 relative to the largest of their row scales (11 bits; 22 where
  * out is FP32). */

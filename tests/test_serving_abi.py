@@ -130,6 +130,7 @@ def test_attn_refusals(U):
                dict(lens=None), dict(lens=P + 2), dict(table=P + 2), dict(mask=P + 4), dict(lse=P + 2),
                dict(scale=float("nan")), dict(scale=float("inf")), dict(q=P + 1), dict(to=1, out=P + 2)):
         assert call(**kw) == INV, kw
+    assert call(width=(1 << 26) + 1, lt=(1 << 26) + 1) == UNS       # pages of 16: one more than 2^30 positions
     assert call(m=65) == UNS and call(width=1 << 27, lt=1 << 27) == UNS and call(lq=1 << 31) == UNS
     assert call(ho=1 << 31) == UNS and call(batch=1 << 30) == UNS
     assert call(batch=0, q=None, out=None, lens=None, table=None) == U.UFP4_OK
