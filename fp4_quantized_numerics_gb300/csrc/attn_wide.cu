@@ -689,7 +689,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                             tiles == 0 ? 0.0f : __uint_as_float(o[blk * 16 + j]) * (a.splits > 1 ? down : inv);
                     const int col = h * 32 + blk * 16;
                     if (a.splits > 1) {
-                        store_whole<16>(a.part_o + part * kDim + col, v);
+                        float4 *to = reinterpret_cast<float4 *>(a.part_o + part * kDim + col);   // (16-byte aligned)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                         continue;
                     }
                     if (col >= a.dim) continue;

@@ -386,3 +386,16 @@ def test_refusals(U):
     assert torch.equal(U.ufp4_cache_attn(**long.args(), ws=ws), U.ufp4_cache_attn(**long.args()))
     with pytest.raises(U.UFP4Error):
         U.ufp4_cache_attn(**long.args(), ws=ws[:need - 1])
+
+
+@pytest.mark.parametrize("m", [1, 32])
+def test_workspace_on_16_bytes(U, m):
+    """Scratch that starts 16 bytes past a larger boundary, and what lies before and behind it stays."""
+    c = Case(U, np.random.default_rng(23), [4000], m, 2, 1, 128, 16, 1, True, BF, extra=4000)
+    need = U.lib().ufp4_cache_attn_workspace_bytes(1, m, 2, c.table.shape[1], c.cache.c())
+    assert need > 0
+    room = torch.full((need + 48,), 0x5A, dtype=torch.uint8, device="cuda")
+    assert room.data_ptr() % 32 == 0
+    got = U.ufp4_cache_attn(**c.args(), ws=room[16:16 + need])
+    assert torch.equal(got, U.ufp4_cache_attn(**c.args()))
+    assert bool((room[:16] == 0x5A).all()) and bool((room[16 + need:] == 0x5A).all())
