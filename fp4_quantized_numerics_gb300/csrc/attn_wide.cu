@@ -327,7 +327,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
             // (the scale's sign, or its being zero, goes with the queries)
             const float up = a.scale == 0.0f ? 0.0f : copysignf(exp2i(14 - e), a.scale);
             if (blk == 0) {
-                qf[r] = a.scale == 0.0f ? 1.0f : exp2i(e - 14) * kDecoded<GRID> * fabsf(a.scale) * 1.4426950408889634f;
+                // (not zero, by which a hidden key's -infinity would become NaN: where the factor underflows, 2^-149
+                // in its place moves no score by more than 2^-21)
+                qf[r] = a.scale == 0.0f ? 1.0f
+                                        : fmaxf(exp2i(e - 14) * kDecoded<GRID> * fabsf(a.scale) * 1.4426950408889634f,
+                                                __uint_as_float(1u));
                 const int node = q / a.group;
                 qm[r] = r >= nq ? 0ull : a.mask ? a.mask[(int64_t)b * a.m + node] : ~0ull >> (63 - node);
             }
