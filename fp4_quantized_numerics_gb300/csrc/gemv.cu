@@ -507,8 +507,11 @@ cudaError_t launch(GemvArgs a, int most_cols, cudaStream_t s) {
     a.factors = 8 * std::min(a.chunks, a.phase * a.cpad) + a.phase * a.cpad;
     a.ring = (int)((a.phase * (size_t)per_chunk + a.factors * 4 + red_bytes + sum_bytes + 15) / 16 * 16);
     const size_t bytes = a.ring + kWarps * kAhead * slot;
+    if (bytes > kSharedBudget) return cudaErrorNotSupported;       // (room() allows for none)
+    // The whole budget, at every call: a call of another thread leaves the
+    // kernel as this one needs it.
     cudaError_t e = cudaFuncSetAttribute(k_gemv<GRID, MT, NT, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)bytes);
+                                         (int)kSharedBudget);
     if (e != cudaSuccess) return e;
     return launch_in_order_smem(k_gemv<GRID, MT, NT, PL>, dim3((unsigned)grid), kThreads, bytes, 1, s, a);
 }
