@@ -295,6 +295,10 @@ class QTensor:
                         self.rows, self.k, self.grid, 0,
                         None if self.eplane is None else self.eplane.data_ptr())
 
+    def ungrouped(self):
+        """Forgets the segments of a grouped quantization that was kept here before."""
+        self.__dict__.pop("seg_rows", None)
+
     def codes_2d(self):
         """codes as uint8 [rows, kpad/2] (a view)."""
         return self.codes[: self.rows * (self.kpad // 2)].view(self.rows, self.kpad // 2)
@@ -336,6 +340,7 @@ def ufp4_quantize(x, grid, rht=False, rht_seed=0, round=UFP4_RTNE, sr_seed=0, sr
     st = lib().ufp4_quantize(x.data_ptr(), _dtype_code(x), rows, cols, x.stride(0), ctypes.byref(p),
                              ctypes.byref(qc), ws.data_ptr(), ws.numel(), _stream(stream))
     _check(st, "ufp4_quantize")
+    out.ungrouped()
     return out
 
 
@@ -362,6 +367,8 @@ def ufp4_quantize_dual(x, grid, rht=False, rht_seed=0, round=UFP4_RTNE, sr_seed=
                                   ctypes.byref(pc), ctypes.byref(qr), ctypes.byref(qc), ws.data_ptr(),
                                   ws.numel(), _stream(stream))
     _check(st, "ufp4_quantize_dual")
+    out_row.ungrouped()
+    out_col.ungrouped()
     return out_row, out_col
 
 
@@ -436,6 +443,7 @@ def ufp4_quantize_stats(x, grid, rht=False, rht_seed=0, round=UFP4_RTNE, sr_seed
                                    ctypes.byref(qc), ws.data_ptr(), ws.numel(), ctypes.byref(res),
                                    _stream(stream))
     _check(st, "ufp4_quantize_stats")
+    out.ungrouped()
     return out, {n: getattr(res, n) for n, _ in StatsC._fields_}
 
 
@@ -944,10 +952,12 @@ def _weights(w, dev):
 
 def ufp4_gemv(x, w, rht=False, rht_seed=0, dtype=None, out=None, stream=None):
     """x W^T for a few tokens: x [tokens, k] bf16 or fp32, not quantized, and w
-    a QTensor (rows x k).  rht: w was quantized with that rotation, and x's
-    16-blocks are rotated to match.  Returns [tokens, rows] of `dtype` (x's by
+    a QTensor (rows x k; not a grouped one of several segments).  rht: w was
+    quantized with that rotation, and x's 16-blocks are rotated to match.  Returns [tokens, rows] of `dtype` (x's by
     default)."""
     dev = _place(x, "x")
+    if len(getattr(w, "seg_rows", ())) > 1:
+        raise ValueError("w is a grouped tensor of %d segments, each with a tensor scale of its own" % len(w.seg_rows))
     xp, dt, ld, tokens = _tokens(x, "x", dev, w.k)
     wc, (s, on) = _weights(w, dev), _streams(stream, dev)
     out, yp, ydt, yld = _result(out, "out", tokens, w.rows, dtype, x.dtype, dev, on)

@@ -579,7 +579,8 @@ UFP4_API ufp4_status ufp4_swiglu_bwd(const void *dh, int32_t dh_dtype, int64_t l
  * below, per 8).
  *   x : tokens x w->k;  y : tokens x w->rows.  w->k <= UFP4_MAX_WIDTH,
  *   tokens <= UFP4_GEMV_MAX_TOKENS.
- * w->k = 0 writes zeros.  w->eplane is not read. */
+ * w->k = 0 writes zeros.  w->eplane is not read.  w is one matrix: of a
+ * grouped tensor every row would be given the first segment's tensor scale. */
 #define UFP4_GEMV_MAX_TOKENS (1LL << 30)
 UFP4_API ufp4_status ufp4_gemv(const void *x, int32_t x_dtype, int64_t tokens, int64_t ld_x, const ufp4_qtensor *w,
                                int32_t rht, uint64_t rht_seed, void *y, int32_t y_dtype, int64_t ld_y,
