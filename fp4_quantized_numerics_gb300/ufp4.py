@@ -1171,14 +1171,14 @@ def ufp4_cache_attn(q, cache, table, lens, mask=None, scale=None, dtype=None, ou
         if lse.dtype is not _FLOAT32 or lse.shape != (tokens, heads) or not lse.is_contiguous():
             raise ValueError("lse must be contiguous fp32 [%d, %d]" % (tokens, heads))
         lp = lse.data_ptr()
-    L = lib()
+    L, sizes = lib(), None
     if ws is None:
         sizes = (dev, batch, m, heads, width, cache.heads, cache.page, dim)
         need = _attn_needs.get(sizes)
         if need is None:
-            if len(_attn_needs) >= 4096:
-                _attn_needs.clear()
-            need = _attn_needs[sizes] = L.ufp4_cache_attn_workspace_bytes(batch, m, heads, width, cc)
+            need = L.ufp4_cache_attn_workspace_bytes(batch, m, heads, width, cc)
+        else:
+            sizes = None
         ws = _empty((need,), torch.uint8, dev, on) if need else None
     elif ws.get_device() != dev:
         _same_place(ws.get_device(), dev, "ws")
@@ -1188,4 +1188,8 @@ def ufp4_cache_attn(q, cache, table, lens, mask=None, scale=None, dtype=None, ou
                            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
                            s)
     _check(st, "ufp4_cache_attn")
+    if sizes is not None:                # (of a cache that is refused the library says 0)
+        if len(_attn_needs) >= 4096:
+            _attn_needs.clear()
+        _attn_needs[sizes] = need
     return (out, lse) if want else out

@@ -30,3 +30,44 @@ def test_a_tensor_that_was_grouped_before(machine):  # noqa: F811
     w.ungrouped()
     U.ufp4_gemv(_rows(4, 64)(On0), w)
     assert [n for n, _ in machine.calls] == ["ufp4_gemv"]
+
+
+class _Attention:
+    """The library's attention with `need` bytes of scratch, which answers the
+    size of a refused cache with 0; `given`: scratch of each call that ran."""
+
+    def __init__(self, need):
+        self.need, self.given, self.asked = need, [], 0
+
+    def ufp4_cache_attn_workspace_bytes(self, batch, m, heads, width, cache):
+        self.asked += 1
+        return self.need if cache._obj.grid == U.UFP4_E1M2 else 0
+
+    def ufp4_cache_attn(self, *args):
+        if args[7]._obj.grid != U.UFP4_E1M2:
+            return U.UFP4_ERR_UNSUPPORTED
+        if args[-2] < self.need:
+            return U.UFP4_ERR_INVALID
+        self.given.append(args[-2])
+        return U.UFP4_OK
+
+    def ufp4_status_string(self, status):
+        return b"refused"
+
+
+def test_a_refused_cache_leaves_no_scratch_size_behind(machine, monkeypatch):  # noqa: F811
+    """A call that was refused says nothing of the scratch that the next one of its sizes needs."""
+    monkeypatch.setattr(U, "_attn_needs", {})
+    fake = _Attention(512)
+    monkeypatch.setattr(U, "lib", lambda: fake)
+    new = lambda *tail, dtype=torch.uint8: _t(On0, 4, 2, 16, *tail, dtype=dtype)  # noqa: E731
+    parts = [new(32), new(4), new(dtype=torch.float32), new(32), new(4), new(dtype=torch.float32)]
+    call = lambda grid: U.ufp4_cache_attn(_t(On0, 4, 4, 64), U.Cache(*parts, 64, grid),  # noqa: E731
+                                          _t(On0, 2, 3, dtype=torch.int32), _t(On0, 2, dtype=torch.int32))
+    with pytest.raises(U.UFP4Error):
+        call(U.UFP4_MXFP4)
+    call(U.UFP4_E1M2)
+    call(U.UFP4_E1M2)
+    assert fake.given == [512, 512] and fake.asked == 2
+    with pytest.raises(U.UFP4Error):
+        call(U.UFP4_MXFP4)
