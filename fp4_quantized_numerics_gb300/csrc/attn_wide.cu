@@ -527,15 +527,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
         bool ok = true;
         float *const vt = reinterpret_cast<float *>(smem + M::kOffValues) + warp * kKeys;
         float *const tops = reinterpret_cast<float *>(smem + M::kOffTop);           // [2][kQ]
-        // over the two warps that have the same queries; a barrier
+        // over the two warps that have the same queries; a barrier of whole warps
         const auto either = [&](bool v) -> bool {
             uint32_t r;
             asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-                         "barrier.cta.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                         "barrier.cta.red.or.pred.aligned q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                          : "=r"(r)
                          : "r"((uint32_t)v), "r"(1 + (warp & 3))
                          : "memory");
             return r != 0;
+        };
+        // The lanes of a warp come out of a wait together: what accesses TMEM
+        // behind it are instructions of the whole warp.
+        const auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, wait(bar, parity));
         };
         // How far a maximum may pass the one that counts (exponents of 2):
         // probabilities are up to 2^slack, and FP16's normal numbers, times
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
             }
             top = fmaxf(top, other) * qscale;
             // the place of the probabilities was the last but one tile's
-            ok = i < 2 || wait(pv_done(i), ((i >> 1) - 1) & 1);
+            ok = i < 2 || wait_warp(pv_done(i), ((i >> 1) - 1) & 1);
             const bool rise = either(top > mx + (float)slack || ve_new > ve || !ok);
             ptx::tc_fence_after();
             if (rise) {
@@ -603,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                 ve = ve_new;
                 if (i > 0) {
                     // O has the last tile's product first
-                    if (either(!wait(pv_done(i - 1), ((i - 1) >> 1) & 1))) return false;
+                    if (either(!wait_warp(pv_done(i - 1), ((i - 1) >> 1) & 1))) return false;
                     ptx::tc_fence_after();
 #pragma unroll 1
                     for (int h = 0; h < kDim / 64; ++h) {
@@ -667,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                 ++round;
             }
         }
-        if (ok && tiles > 0) ok = wait(pv_done(tiles - 1), ((tiles - 1) >> 1) & 1);
+        if (ok && tiles > 0) ok = wait_warp(pv_done(tiles - 1), ((tiles - 1) >> 1) & 1);
         tops[half * kQ + r] = l;
         ok = !either(!ok);
         ptx::tc_fence_after();
@@ -681,11 +686,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
 #pragma unroll 1
             for (int h = half * DC; h < (half + 1) * DC; ++h) {
                 uint32_t o[32];
+                __syncwarp();
                 ptx::tc_ld_32x32b_x32(tm + h * 32, o);
                 ptx::tc_wait_ld();
-                if (r >= nq) continue;
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk) {
+                    if (r >= nq) break;
                     float v[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
