@@ -29,8 +29,8 @@
 // rises 147; the MMAs issued by an elected lane rather than by lane 0 139 (its
 // operands then need no moves to uniform registers).
 //
-// Waits are bounded: one that gives up raises the library's timeout flag, the
-// CTA drains its MMAs and ends.
+// Waits are bounded: one that gives up raises the library's timeout flag, every
+// role leaves, and the CTA waits for the MMAs that it issued and ends.
 #include "attn.cuh"
 #include "common.cuh"
 #include "dequant.cuh"
@@ -63,6 +63,10 @@ constexpr int kSoftWarps = 8, kDecodeWarps = 8, kThreads = (kSoftWarps + kDecode
 constexpr int kGroups = 2, kGroupWarps = kDecodeWarps / kGroups;   // decoding warps take every second tile,
 constexpr int kWarpKeys = kKeys / kGroupWarps;                     // 16 rows of it each
 constexpr long long kWaitBudget = 2000000000LL;          // SM clocks: about a second
+// What the waits are given (and the test-only stall switch); a test-only build
+// of the library can change them, libufp4 keeps the defaults.
+long long g_attn_wait_budget = kWaitBudget;
+int g_attn_stall = 0;
 // TMEM: O, S of two tiles, Q's two FP16 values, P's of two tiles.
 constexpr uint32_t kTmemCols = 512, kColS = 128, kColQ = 256, kColP = 384;
 
@@ -82,7 +86,7 @@ struct Smem {
     static constexpr int kOffRow = kOffValues + kSoftWarps * kKeys * 4;             // of each query: mask, scale,
     static constexpr int kOffTop = kOffRow + kQ * 12;                               // its two threads' maxima or sums
     static constexpr int kOffBar = kOffTop + kQ * 8;
-    static constexpr int kBars = 2 * kStages + 6;
+    static constexpr int kBars = 2 * kStages + 7;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16;
 };
 
@@ -167,7 +171,7 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n, bool b_n_major) {
 
 // TWO: the probabilities are two FP16 values (fp32 results).
 template <int GRID, int DC, bool TWO>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, long long budget, int stall) {
     using M = Smem<DC>;
     constexpr int kDim = M::kDim, kRow = M::kRow, kBlocks = M::kBlocks;
     extern __shared__ uint8_t raw_smem[];
@@ -182,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
     // of every second tile: its probabilities are in TMEM; O has them
     const auto p_ready = [&](int i) { return bars + (2 * kStages + 2 + (i & 1)) * 8; };
     const auto pv_done = [&](int i) { return bars + (2 * kStages + 4 + (i & 1)) * 8; };
+    const uint32_t drained = bars + (2 * kStages + 6) * 8;                          // after a failure: all MMAs are done
     uint32_t *const slot = reinterpret_cast<uint32_t *>(smem + M::kOffBar + M::kBars * 8);
     volatile uint32_t *const stop = slot + 1;
     const uint32_t zero = begin_in_order();
@@ -209,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                 ptx::mbar_init(p_ready(i), kSoftWarps * 32);
                 ptx::mbar_init(pv_done(i), 1);
             }
+            ptx::mbar_init(drained, 1);
             ptx::fence_mbar_init();
         }
     }
@@ -217,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
         const long long t0 = clock64();
         while (!*stop) {
             if (try_wait_long(bar, parity)) return true;
-            if (clock64() - t0 > kWaitBudget) {
+            if (clock64() - t0 > budget) {
                 atomicOr(&g_ufp4_attn_timeout, 1u);
                 *stop = 1;
             }
@@ -483,7 +489,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                 ptx::tc_commit(s_full(i & 1));
                 return true;
             };
-            bool ok = tiles == 0 || scores(0, 0, 0);
+            bool ok = true;
+#ifdef UFP4_PROBE
+            // test-only build: a wait that nothing ends (`drained` is committed
+            // only below), so that the way out runs
+            if (stall) ok = wait(drained, 0);
+#endif
+            ok = ok && (tiles == 0 || scores(0, 0, 0));
             int stage = 0, ahead = 1 % kStages, ahead_round = 0;
             for (int i = 0; ok && i < tiles; ++i) {
                 // (the place of S of the next tile: read before the probabilities of the last were ready)
@@ -509,9 +521,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
                 ptx::tc_commit(pv_done(i));
                 if (++stage == kStages) stage = 0;
             }
-            if (!ok) {       // what was issued ends before TMEM is given back
+            if (!ok) {       // TMEM is given back, and the operands' memory, when what was issued has ended
+                ptx::tc_commit(drained);
                 const long long t0 = clock64();
-                while (clock64() - t0 < kWaitBudget / 100) {}
+                while (!try_wait_long(drained, 0) && clock64() - t0 <= kWaitBudget) {}
             }
         }
         __syncwarp();
@@ -594,7 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a) {
             }
             top = fmaxf(top, other) * qscale;
             // the place of the probabilities was the last but one tile's
-            ok = i < 2 || wait_warp(pv_done(i), ((i >> 1) - 1) & 1);
+            // (or the scores never came)
+            ok = ok && (i < 2 || wait_warp(pv_done(i), ((i >> 1) - 1) & 1));
             const bool rise = either(top > mx + (float)slack || ve_new > ve || !ok);
             ptx::tc_fence_after();
             if (rise) {
@@ -753,7 +767,8 @@ cudaError_t wide(const AttnArgs &a, cudaStream_t s) {
         cudaFuncSetAttribute(k_attn_wide<GRID, DC, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     return launch_in_order_smem(k_attn_wide<GRID, DC, TWO>,
-                                dim3((unsigned)(a.batch * a.kv * a.qtiles), (unsigned)a.splits), kThreads, bytes, 1, s, a);
+                                dim3((unsigned)(a.batch * a.kv * a.qtiles), (unsigned)a.splits), kThreads, bytes, 1, s, a,
+                                g_attn_wait_budget, g_attn_stall);
 }
 
 }  // namespace
@@ -768,3 +783,7 @@ cudaError_t launch_attn_wide(const AttnArgs &a, int grid, int padded, cudaStream
 }
 
 }  // namespace ufp4
+
+#ifdef UFP4_PROBE
+#include "probe_attn.inc"
+#endif
