@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "dequant.cuh"
 #include "internal.h"
 
 namespace ufp4 {
@@ -37,6 +38,39 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+// The weights of the values are probabilities times row scales.  A query's are
+// brought into FP16's range by a power of two of its own, 2^-we, as its
+// probabilities are by 2^-mx: both follow what the query has seen, by steps.
+constexpr int kLeastExponent = -110;     // (of what is held: 2^(14 - e) and 2^(e - 14) are normal)
+// What stands for row scales within 2^kEvenScales of one another: the largest.
+constexpr int kEvenScales = 4;
+// (b >> 23) - 127 as fp32: floor(log2) of the positive number with the bits b.
+__device__ __forceinline__ float bits_exponent(uint32_t b) {
+    return __uint_as_float(0x4B000000u | b >> 23) - (8388608.0f + 127.0f);
+}
+// floor(log2) of a row scale (-127: zero, subnormal or not finite).
+__device__ __forceinline__ float scale_exponent(float v) { return bits_exponent(finite_bits(v)); }
+// The exponent of a power of two.
+__device__ __forceinline__ int power_of(float p) { return (int)(__float_as_uint(p) >> 23) - 127; }
+struct Rise {
+    float mx;
+    int we;
+    float l_back, o_back;                // what the sums so far are multiplied by
+};
+// mx and we after keys whose largest score is v and largest score plus scale's
+// exponent w, where one of them passes what counts by more than `slack`.
+__device__ __forceinline__ Rise rise_to(float mx, int we, float v, float w, float slack) {
+    if (!(v > mx + slack || w > mx + (float)we + slack)) return Rise{mx, we, 1.0f, 1.0f};
+    v = fmaxf(v, mx);
+    w = fmaxf(w, mx + (float)we);
+    // New weights end below 2^(to + 2); what the old ones are given is not less
+    // than before, so that sums only shrink.  (Held so that 2^(14 - we) is a
+    // normal number; where v is not finite, at a limit.)
+    const float most = fmaxf(floorf(w - v), ceilf(mx + (float)we - v));
+    const int to = (int)fminf(fmaxf(most, (float)kLeastExponent), 127.0f);
+    const float back = mx - v;
+    return Rise{v, to, exp2f(back), exp2f(back + (float)(we - to))};
 }
 // Keys [first, last) of a sequence of `len` (at most UFP4_MAX_KEYS, so that a
 // tile past its end fits 32 bits) that split s of n takes.

@@ -16,9 +16,10 @@
 //  * 8 warps do the softmax, two threads a query (a tile's chain of dependent
 //    steps, not the number of instructions, is what it takes), two keys an
 //    instruction where there is one: S from TMEM, the row scale of its key as a
-//    factor, the probabilities times their row's scale as FP16 to TMEM.  O stays
-//    there; it is scaled, and the two threads of a query speak, only when a
-//    maximum rises by more than 2^8 or a larger row scale appears.
+//    factor, the probabilities times their row's scale (and the query's own
+//    power of two) as FP16 to TMEM.  O stays there; it is scaled, and the two
+//    threads of a query speak, only when the largest score or weight of a query
+//    rises by more than 2^8 (2^3 for fp32 results).
 // Measured: trees of 32 tokens, 8 sequences of 8192 to 16384 keys, 32 heads over
 // 8, E1M2 rotated, 140 us (380 TFLOP/s of the definition's; twice the queries'
 // product in fact).  A tile of 64 keys takes some 5400 instructions (softmax 2200,
@@ -80,12 +81,11 @@ struct Smem {
     static constexpr int kQRow = kDim * 2 + 16, kQPlane = kQ * kQRow;
     static constexpr int kKvBytes = kStages * kStage > 2 * kQPlane ? kStages * kStage : 2 * kQPlane;
     static constexpr int kOffRaw = kKvBytes, kOffMeta = kOffRaw + kDecodeWarps * kRing * kRaw;
-    // of each stage: row scales of the keys and values, the warps' largest exponents
-    static constexpr int kMeta = kKeys * 8 + kGroupWarps * 4;
-    static constexpr int kOffValues = kOffMeta + kStages * kMeta;                   // of each softmax warp: factors
-    static constexpr int kOffRow = kOffValues + kSoftWarps * kKeys * 4;             // of each query: mask, scale,
+    // of each stage: row scales of the keys and values, the decoding warps' largest and least exponents of the latter
+    static constexpr int kMeta = kKeys * 8 + kGroupWarps * 8;
+    static constexpr int kOffRow = kOffMeta + kStages * kMeta;                      // of each query: mask, scale,
     static constexpr int kOffTop = kOffRow + kQ * 12;                               // its two threads' maxima or sums
-    static constexpr int kOffBar = kOffTop + kQ * 8;
+    static constexpr int kOffBar = kOffTop + kQ * 16;
     static constexpr int kBars = 2 * kStages + 7;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16;
 };
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, long long
             uint8_t *const meta = smem + M::kOffMeta + stage * M::kMeta;
             const int pos0 = first + i * kKeys + w * kWarpKeys;
             const bool edge = pos0 + kWarpKeys > len - tail || pos0 + kWarpKeys > last;
-            uint32_t vtop = 0;
+            uint32_t vtop = 0, vleast = ~0u;                 // (a scale of zero weighs nothing)
 #pragma unroll
             for (int part = 0; part < kWarpKeys / 8; ++part) {
                 const int key = part * 8 + r;
@@ -446,10 +446,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, long long
                 float rs = *reinterpret_cast<const float *>(from + (t & 1) * kVal + kCodes + kScales + key * 4);
                 if (unseen) rs = 0.0f;
                 if (t < 2) reinterpret_cast<float *>(meta)[t * kKeys + w * kWarpKeys + key] = rs;
-                vtop = max(vtop, t & 1 ? finite_bits(rs) : 0u);
+                const uint32_t bits = t & 1 ? finite_bits(rs) : 0u;
+                vtop = max(vtop, bits);
+                vleast = min(vleast, bits - 1);
             }
             vtop = __reduce_max_sync(0xffffffffu, vtop);
-            if (lane == 0) reinterpret_cast<int *>(meta + kKeys * 8)[w] = top_exponent(vtop);
+            vleast = __reduce_min_sync(0xffffffffu, vleast);
+            if (lane == 0) {
+                int *const exps = reinterpret_cast<int *>(meta + kKeys * 8);
+                exps[w] = (int)(vtop >> 23) - 127;
+                exps[kGroupWarps + w] = (int)(vleast >> 23) - 127;
+            }
             ptx::fence_proxy_async();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(full(stage));
@@ -536,10 +543,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, long long
         const float qscale = qf[r];
         const uint64_t qs2 = pack2(qscale, qscale);
         float mx = -INFINITY, l = 0.0f;
-        int ve = -110, stage = 0, round = 0;
+        int stage = 0, round = 0;
         bool ok = true;
-        float *const vt = reinterpret_cast<float *>(smem + M::kOffValues) + warp * kKeys;
-        float *const tops = reinterpret_cast<float *>(smem + M::kOffTop);           // [2][kQ]
+        float *const tops = reinterpret_cast<float *>(smem + M::kOffTop), *const wtops = tops + 2 * kQ;     // [2][kQ] each
         // over the two warps that have the same queries; a barrier of whole warps
         const auto either = [&](bool v) -> bool {
             uint32_t r;
@@ -555,24 +561,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, long long
         const auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, wait(bar, parity));
         };
-        // How far a maximum may pass the one that counts (exponents of 2):
-        // probabilities are up to 2^slack, and FP16's normal numbers, times
-        // their rows' scales, reach down to 2^(slack - 28).  A rise costs a pass
-        // over O, which BF16 results save more often (8 trees of 32 tokens: in
-        // most tiles some query of 128 rises by 3).
+        // How far a maximum may pass the one that counts (exponents of 2), of
+        // the scores and of the weights (attn.cuh): probabilities are up to
+        // 2^slack, and FP16's normal numbers reach down to 2^(slack - 28) of the
+        // query's largest weight.  A rise costs a pass over O, which BF16
+        // results save more often (8 trees of 32 tokens: in most tiles some query
+        // of 128 rises by 3).
         constexpr int slack = TWO ? 3 : 8;
+        int we = kLeastExponent;                             // of the query's weights
         // scores times their key's scale (-infinity where hidden), the running
         // maximum, and the probabilities
         const auto soften = [&](int i, auto edge_t) -> bool {
             constexpr bool kEdge = decltype(edge_t)::value != 0;
             const uint8_t *meta = smem + M::kOffMeta + stage * M::kMeta;
             const float *krs = reinterpret_cast<const float *>(meta) + half * kMine, *vrs = krs + kKeys;
-            const int4 exps = *reinterpret_cast<const int4 *>(meta + kKeys * 8);
-            const int ve_new = max(max(max(exps.x, exps.y), max(exps.z, exps.w)), ve);
-            // the values' scales as they will be multiplied by
-            const float mine = vrs[lane] * exp2i(14 - slack - ve_new);
-            __syncwarp();
-            vt[lane] = mine;
+            const int4 exps = *reinterpret_cast<const int4 *>(meta + kKeys * 8),
+                       least = *reinterpret_cast<const int4 *>(meta + kKeys * 8 + 16);
+            const int vmost = max(max(exps.x, exps.y), max(exps.z, exps.w));
+            const bool even = vmost - min(min(least.x, least.y), min(least.z, least.w)) <= kEvenScales;
             uint64_t z[kMine / 2];
             {
                 uint32_t raw[kMine];
@@ -606,20 +612,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, long long
                 other = max3(other, v.x, v.y);
             }
             top = fmaxf(top, other) * qscale;
+            float wtop = top + (float)vmost;
+            if (!even) {
+                wtop = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < kMine; j += 2) {
+                    const float2 v = *reinterpret_cast<const float2 *>(vrs + j), u = unpack2(z[j / 2]);
+                    wtop = max3(wtop, fmaf(u.x, qscale, scale_exponent(v.x)), fmaf(u.y, qscale, scale_exponent(v.y)));
+                }
+            }
             // the place of the probabilities was the last but one tile's
             // (or the scores never came)
             ok = ok && (i < 2 || wait_warp(pv_done(i), ((i >> 1) - 1) & 1));
-            const bool rise = either(top > mx + (float)slack || ve_new > ve || !ok);
+            const bool rise = either(top > mx + (float)slack || wtop > mx + (float)(we + slack) || !ok);
             ptx::tc_fence_after();
             if (rise) {
                 tops[half * kQ + r] = top;
+                wtops[half * kQ + r] = wtop;
                 if (either(!ok)) return false;
-                const float v = fmaxf(mx, fmaxf(tops[r], tops[kQ + r]));
-                const float back = exp2f(mx - (v == -INFINITY ? 0.0f : v));
-                const float ob = back * exp2f((float)(ve - ve_new));
-                mx = v;
-                l *= back;
-                ve = ve_new;
+                const Rise to =
+                    rise_to(mx, we, fmaxf(tops[r], tops[kQ + r]), fmaxf(wtops[r], wtops[kQ + r]), (float)slack);
+                mx = to.mx;
+                we = to.we;
+                l *= to.l_back;
                 if (i > 0) {
                     // O has the last tile's product first
                     if (either(!wait_warp(pv_done(i - 1), ((i - 1) >> 1) & 1))) return false;
@@ -631,14 +646,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, long long
                         ptx::tc_ld_32x32b_x32(col, o);
                         ptx::tc_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * ob);
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * to.o_back);
                         tc_st_32x32b_x32(col, o);
                     }
                 }
             }
-            __syncwarp();
-            const float base = mx == -INFINITY ? 0.0f : -mx;
-            const uint64_t base2 = pack2(base, base);
+            const float base = mx == -INFINITY ? 0.0f : -mx, up = exp2i(14 - slack - we);
+            const uint64_t base2 = pack2(base, base), up2 = pack2(up, up);
             uint64_t sums[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
 #pragma unroll
             for (int c = 0; c < kMine; c += 16) {
@@ -646,13 +660,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, long long
                 [[maybe_unused]] uint32_t lo[8];
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
-                    const float4 v4 = *reinterpret_cast<const float4 *>(vt + c + 2 * j);
+                    const float4 v4 = *reinterpret_cast<const float4 *>(vrs + c + 2 * j);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float2 y = unpack2(fma2(z[c / 2 + j + e], qs2, base2));
                         const uint64_t p = pack2(exp2_fast(y.x), exp2_fast(y.y));
                         sums[e] = add2(sums[e], p);
-                        float2 x = unpack2(mul2(p, e ? pack2(v4.z, v4.w) : pack2(v4.x, v4.y)));
+                        float2 x = unpack2(mul2(mul2(p, up2), e ? pack2(v4.z, v4.w) : pack2(v4.x, v4.y)));
                         if constexpr (kEdge) {
                             if (y.x == -INFINITY) x.x = 0.0f;
                             if (y.y == -INFINITY) x.y = 0.0f;
@@ -692,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, long long
         ptx::tc_fence_after();
         if (ok) {
             const float sum = tops[r] + tops[kQ + r];
-            const float down = exp2i(ve - 14 + slack) * kDecoded<GRID>;
+            const float down = exp2i(we - 14 + slack) * kDecoded<GRID>;
             const float inv = sum > 0.0f || sum != sum ? down / sum : 0.0f;
             const int q = q0 + r, node = q / a.group, head = kvh * a.group + q % a.group;
             const int64_t token = (int64_t)b * a.m + node;

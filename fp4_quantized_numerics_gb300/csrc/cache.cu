@@ -168,8 +168,10 @@ __global__ void __launch_bounds__(128) k_load(RowArgs a) {
 //  * O^T = V^T P^T: a lane decodes the same elements of four keys and pairs
 //    them up by permutes; P^T becomes the other operand by movmatrix.
 // The probabilities enter the product times their key's row scale, brought
-// below 2^15 by a power of two that follows the largest scale seen, as FP16
-// (11 bits; two of them for fp32 results), and the sums are fp32.  Keys of a
+// below 2^15 by a power of two of the query's own, which follows the largest of
+// these products that it has seen (no row of values, however large, costs the
+// others bits but for the queries in whose sum it counts), as FP16 (11 bits; two
+// of them for fp32 results), and the sums are fp32.  Keys of a
 // sequence are spread over warps, and over CTAs (splits) where sequences and
 // heads are too few; the parts are joined in a fixed order, by a cluster for up
 // to 8, else by a second kernel.
@@ -412,10 +414,13 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
 
     float o[4 * DC][NT][4] = {};
     float mx[NT][2], l[NT][2] = {};
+    float up[NT][2], wlim[NT][2];                    // 2^(11 - we), and what weights may reach
 #pragma unroll
-    for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
-    int ve = -110;                                   // exponent of the largest row scale of the values
-    uint32_t vmost = __float_as_uint(exp2i(-110)) | 0x7FFFFFu;
+    for (int n = 0; n < NT; ++n) {
+        mx[n][0] = mx[n][1] = -INFINITY;
+        wlim[n][0] = wlim[n][1] = -INFINITY;
+        up[n][0] = up[n][1] = exp2i(11 - kLeastExponent);
+    }
     float qscale[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -525,47 +530,65 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
         }
 
         // ---- running maximum and sum; weights of the values.  The maximum
-        // follows the scores when one passes it by more than 2^3: until then
-        // probabilities are up to 8, and times 2^(11 - ve) of their row scales
-        // below 2^15.
-        float top[NT][2];
+        // follows the scores when one passes it by more than 2^3, and so does
+        // the exponent of the weights: until then probabilities are up to 8,
+        // and weights times 2^(11 - we) below 2^15.  Only what passed is moved:
+        // a query's results do not depend on the others.
+        float top[NT][2], wtop[NT][2];
+        uint32_t vmost = 0, vleast = ~0u;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            vmost = max(vmost, __float_as_uint(vrs[r]));
+            vleast = min(vleast, __float_as_uint(vrs[r]));
+        }
+        const float vexp = bits_exponent(vmost & 0x7FFFFFFFu);
         bool rise = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 top[n][c] = fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c]));
-                rise |= top[n][c] > mx[n][c] + 3.0f;
+                wtop[n][c] = top[n][c] + vexp;
             }
-        const uint32_t vtop = max(max(finite_bits(vrs[0]), finite_bits(vrs[1])),
-                                  max(finite_bits(vrs[2]), finite_bits(vrs[3])));
-        rise |= vtop > vmost;
+        if (vmost - vleast > (uint32_t)kEvenScales << 23) {       // (NaN, too, unless all are)
+            float own[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) own[r] = scale_exponent(vrs[r]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    wtop[n][c] = fmaxf(fmaxf(s[0][n][c] + own[0], s[0][n][2 + c] + own[1]),
+                                       fmaxf(s[1][n][c] + own[2], s[1][n][2 + c] + own[3]));
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                rise |= top[n][c] > mx[n][c] + 3.0f || wtop[n][c] > wlim[n][c];
         if (__any_sync(0xffffffffu, rise)) {
-            const int ve_new = max(ve, top_exponent(__reduce_max_sync(0xffffffffu, vtop)));
-            const float v_back = exp2f((float)(ve - ve_new));
-            ve = ve_new;
-            vmost = __float_as_uint(exp2i(ve)) | 0x7FFFFFu;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float v = top[n][c];
+                    float v = top[n][c], w = wtop[n][c];
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                    v = fmaxf(v, mx[n][c]);
-                    const float back = exp2f(mx[n][c] - (v == -INFINITY ? 0.0f : v));
-                    mx[n][c] = v;
-                    l[n][c] *= back;
+                    for (int d = 4; d < 32; d <<= 1) {
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                        w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, d));
+                    }
+                    const Rise to = rise_to(mx[n][c], 11 - power_of(up[n][c]), v, w, 3.0f);
+                    mx[n][c] = to.mx;
+                    up[n][c] = exp2i(11 - to.we);
+                    wlim[n][c] = to.mx + (float)(to.we + 3);
+                    l[n][c] *= to.l_back;
 #pragma unroll
                     for (int i = 0; i < 4 * DC; ++i) {
-                        o[i][n][c] *= back * v_back;
-                        o[i][n][2 + c] *= back * v_back;
+                        o[i][n][c] *= to.o_back;
+                        o[i][n][2 + c] *= to.o_back;
                     }
                 }
         }
-        const float vup = exp2i(11 - ve);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) vrs[r] *= vup;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -577,7 +600,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
                     const bool hidden = x == -INFINITY;
                     const float p = exp2_fast(x - base);
                     l[n][c] += p;
-                    x = hidden ? 0.0f : p * vrs[r];
+                    x = hidden ? 0.0f : p * up[n][c] * vrs[r];
                 }
             }
 
@@ -647,11 +670,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
     __syncthreads();
     float *po = reinterpret_cast<float *>(stages);                 // [warp][query][kDim]
     float *pm = po + kAttnWarps * kQ * kDim, *pl = pm + kAttnWarps * kQ;
-    const float down = exp2i(ve - 11) * kDecoded<GRID>;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
+            const float down = exp2i(-power_of(up[n][c])) * kDecoded<GRID>;
             float sum = l[n][c];
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
