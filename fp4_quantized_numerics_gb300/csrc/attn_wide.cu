@@ -42,21 +42,6 @@
 #include <algorithm>
 
 namespace ufp4 {
-
-// Raised by a wait that gave up (read by ufp4_check).
-__device__ uint32_t g_ufp4_attn_timeout;
-
-cudaError_t read_attn_timeout_flag(uint32_t *flag, cudaStream_t s) {
-    cudaError_t e = cudaMemcpyFromSymbolAsync(flag, g_ufp4_attn_timeout, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess && *flag) {
-        const uint32_t zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_ufp4_attn_timeout, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    return e;
-}
-
 namespace {
 
 constexpr int kQ = kWideQueries, kKeys = 64, kStages = 3, kRing = 3;
@@ -171,7 +156,7 @@ __device__ __forceinline__ constexpr uint32_t idesc(int n, bool b_n_major) {
 
 // TWO: the probabilities are two FP16 values (fp32 results).
 template <int GRID, int DC, bool TWO>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, long long budget, int stall) {
+__global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t *timeout, long long budget, int stall) {
     using M = Smem<DC>;
     constexpr int kDim = M::kDim, kRow = M::kRow, kBlocks = M::kBlocks;
     extern __shared__ uint8_t raw_smem[];
@@ -224,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, long long
         while (!*stop) {
             if (try_wait_long(bar, parity)) return true;
             if (clock64() - t0 > budget) {
-                atomicOr(&g_ufp4_attn_timeout, 1u);
+                atomicOr(timeout, 1u);
                 *stop = 1;
             }
         }
@@ -777,12 +762,13 @@ template <int GRID, int DC, bool TWO>
 cudaError_t wide(const AttnArgs &a, cudaStream_t s) {
     constexpr int bytes = Smem<DC>::kBytes + 1024;
     static_assert(bytes <= 232448, "shared memory of a CTA");
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_attn_wide<GRID, DC, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(k_attn_wide<GRID, DC, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    uint32_t *timeout = nullptr;         // raised by a wait that gives up (read by ufp4_check)
+    if (e == cudaSuccess) e = timeout_flag(&timeout);
     if (e != cudaSuccess) return e;
     return launch_in_order_smem(k_attn_wide<GRID, DC, TWO>,
                                 dim3((unsigned)(a.batch * a.kv * a.qtiles), (unsigned)a.splits), kThreads, bytes, 1, s, a,
-                                g_attn_wait_budget, g_attn_stall);
+                                timeout, g_attn_wait_budget, g_attn_stall);
 }
 
 }  // namespace
