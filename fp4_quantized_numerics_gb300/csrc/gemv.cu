@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
                         d.s[0] = upper ? v.z : v.x;
                         d.s[1] = upper ? v.w : v.y;
                     }
-                    float acc[MT][NT][4] = {};
+                    float acc[PL][MT][NT][4] = {};
                     uint32_t scale[2 * MT];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
@@ -374,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
                                 for (int m = 0; m < MT; ++m) {
                                     const uint32_t(&r)[4] = h[2 * m];
                                     const uint32_t(&s)[4] = h[2 * m + 1];
-                                    mma_f16(acc[m][n], r[0], s[0], r[1], s[1], b.x, b.y);
-                                    mma_f16(acc[m][n], r[2], s[2], r[3], s[3], b.z, b.w);
+                                    mma_f16(acc[p][m][n], r[0], s[0], r[1], s[1], b.x, b.y);
+                                    mma_f16(acc[p][m][n], r[2], s[2], r[3], s[3], b.z, b.w);
                                 }
                             }
                         }
@@ -384,12 +384,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
                     for (int n = 0; n < NT; ++n) {
                         const float2 w = *reinterpret_cast<const float2 *>(fac + ch * fpitch + n * 8 + 2 * t);
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            sum[m][n][0] += acc[m][n][0] * w.x;
-                            sum[m][n][1] += acc[m][n][1] * w.y;
-                            sum[m][n][2] += acc[m][n][2] * w.x;
-                            sum[m][n][3] += acc[m][n][3] * w.y;
-                        }
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                float v = acc[0][m][n][j];
+                                if constexpr (PL == 2) v += acc[1][m][n][j];
+                                sum[m][n][j] += v * (j & 1 ? w.y : w.x);
+                            }
                     }
                 }
                 xp += wk * 4 * x_word;
