@@ -476,8 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t 
                                 mma_f16_ts<true>(d_col, q_col + d * 32 + k * 8, kd + d * (M::kPanel / 16) + k * 2,
                                                  idesc(kKeys, false));
                 };
-                plane(tmem + kColQ, false);
-                if (a.planes == 2) plane(tmem + kColQ + DC * 32, true);
+                // (the second values first: their sums are small, and the accumulator truncates)
+                if (a.planes == 2) plane(tmem + kColQ + DC * 32, false);
+                plane(tmem + kColQ, a.planes == 2);
                 ptx::tc_commit(s_full(i & 1));
                 return true;
             };

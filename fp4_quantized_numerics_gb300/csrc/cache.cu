@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
         }
 
         // ---- scores: keys 16 i + g (and + 8) by queries 8 n + 2 t (and + 1)
-        float s[2][NT][4] = {};
+        float s[2][NT][4] = {}, s2[2][NT][4] = {};      // s2: of the queries' second values
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             uint32_t kw[2][2 * DC], kb[2];
@@ -494,8 +494,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
                     mma_f16(s[i][n], h[0][2], h[1][2], h[0][3], h[1][3], x.z, x.w);
                     if (a.planes == 2) {
                         const uint4 y = qs[2 * DC * kQ * 4 + (u * kQ + n * 8 + g) * 4 + t];
-                        mma_f16(s[i][n], h[0][0], h[1][0], h[0][1], h[1][1], y.x, y.y);
-                        mma_f16(s[i][n], h[0][2], h[1][2], h[0][3], h[1][3], y.z, y.w);
+                        mma_f16(s2[i][n], h[0][0], h[1][0], h[0][1], h[1][1], y.x, y.y);
+                        mma_f16(s2[i][n], h[0][2], h[1][2], h[0][3], h[1][3], y.z, y.w);
                     }
                 }
             }
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[i][n][j] *= krs[2 * i + (j >> 1)] * qscale[n][j & 1];
+                for (int j = 0; j < 4; ++j) s[i][n][j] = (s[i][n][j] + s2[i][n][j]) * (krs[2 * i + (j >> 1)] * qscale[n][j & 1]);
         if (edge) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
