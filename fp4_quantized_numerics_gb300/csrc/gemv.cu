@@ -23,7 +23,8 @@
 //  * The tokens are staged once per CTA in shared memory as FP16 operands, in
 //    the order in which lanes read them.  Each chunk of a token has its own
 //    power of two (its largest magnitude below 2^15), so BF16 tokens are exact
-//    down to 2^-29 of the chunk's largest.  Rotated or FP32 tokens are, for an
+//    down to 2^-29 of the chunk's largest (less where its products come near
+//    fp32's lower end).  Rotated or FP32 tokens are, for an
 //    FP32 result, the sum of two FP16 values, within 2^-22 of each element; for
 //    a BF16 result (8 bits) one FP16 value (11 bits).  The sum of a chunk's
 //    products is scaled by that power and the weights' S when it is added to
@@ -204,6 +205,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
         cols.n = min(seg_tokens - cols.first, a.cpad);
         cols.pad = pad_cols(cols.n);
         const float ts = a.tensor_scale[zero + seg] * kDecoded<GRID>;
+        // exponent of a chunk below which its factor would not be a normal number
+        const int low = -112 - ((int)(__float_as_uint(ts) >> 23 & 0xFFu) - 127);
         const int64_t atom0 = (int64_t)seg * a.atoms;
 
         // chunks that fit beside this many columns, evenly over the phases
@@ -310,7 +313,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
                 top = max(top, __shfl_xor_sync(group, top, 1));
                 top = max(top, __shfl_xor_sync(group, top, 2));
                 top = max(top, __shfl_xor_sync(group, top, 4));
-                const int e = top_exponent(top);
+                // (small tokens by small weights: up to 2^16 less for the tokens'
+                // FP16 values, of which the largest keep their bits, rather
+                // than bits of the factor, which all products share)
+                const int own = top_exponent(top), e = max(own, min(own + 16, low));
                 const float m = exp2i(14 - e);
                 if (b == 0) fac[ch * fpitch + col] = exp2i(e - 14) * ts;
 #pragma unroll

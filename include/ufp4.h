@@ -574,7 +574,8 @@ UFP4_API ufp4_status ufp4_swiglu_bwd(const void *dh, int32_t dh_dtype, int64_t l
  * goes with weights quantized with rht = 1 and that seed.  x is not quantized:
  * a BF16 element not rotated enters exactly, one rotated or FP32 within 2^-22
  * of itself where y is FP32 and 2^-11 where y is BF16 (which keeps 2^-8), each
- * down to 2^-29 of the largest among the 128 it lies with.
+ * down to 2^-29 of the largest among the 128 it lies with (2^-13 where that
+ * one times w's tensor scale is below 2^-112).
  * Made for 1 to 32 tokens; further ones read w once more per 32 (by expert,
  * below, per 8).
  *   x : tokens x w->k;  y : tokens x w->rows.  w->k <= UFP4_MAX_WIDTH,
