@@ -527,7 +527,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t 
         constexpr int kMine = kKeys / 2;
         const uint32_t tm = tmem + lanes;
         const float qscale = qf[r];
-        const uint64_t qs2 = pack2(qscale, qscale);
         float mx = -INFINITY, l = 0.0f;
         int stage = 0, round = 0;
         bool ok = true;
@@ -565,11 +564,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t 
                        least = *reinterpret_cast<const int4 *>(meta + kKeys * 8 + 16);
             const int vmost = max(max(exps.x, exps.y), max(exps.z, exps.w));
             const bool even = vmost - min(min(least.x, least.y), min(least.z, least.w)) <= kEvenScales;
+            // (keys of 2^91 and more: a factor of 2^64 goes from the products, up
+            // to 2^34, to the query's)
+            const bool far = __any_sync(0xffffffffu, krs[lane] >= 0x1p80f);
+            const float qs = far ? qscale * 0x1p64f : qscale;
+            const uint64_t qs2 = pack2(qs, qs);
             uint64_t z[kMine / 2];
             {
                 uint32_t raw[kMine];
                 ptx::tc_ld_32x32b_x32(tm + kColS + (i & 1) * kKeys + half * kMine, raw);
                 ptx::tc_wait_ld();
+                if (far) {
+#pragma unroll
+                    for (int j = 0; j < kMine; ++j) raw[j] = __float_as_uint(__uint_as_float(raw[j]) * 0x1p-64f);
+                }
 #pragma unroll
                 for (int j = 0; j < kMine; j += 4) {
                     const float4 k4 = *reinterpret_cast<const float4 *>(krs + j);
@@ -597,14 +605,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t 
                 top = max3(top, u.x, u.y);
                 other = max3(other, v.x, v.y);
             }
-            top = fmaxf(top, other) * qscale;
+            top = fmaxf(top, other) * qs;
             float wtop = top + (float)vmost;
             if (!even) {
                 wtop = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < kMine; j += 2) {
                     const float2 v = *reinterpret_cast<const float2 *>(vrs + j), u = unpack2(z[j / 2]);
-                    wtop = max3(wtop, fmaf(u.x, qscale, scale_exponent(v.x)), fmaf(u.y, qscale, scale_exponent(v.y)));
+                    wtop = max3(wtop, fmaf(u.x, qs, scale_exponent(v.x)), fmaf(u.y, qs, scale_exponent(v.y)));
                 }
             }
             // the place of the probabilities was the last but one tile's

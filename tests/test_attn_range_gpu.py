@@ -130,3 +130,23 @@ def test_values_at_the_ends_of_fp32(U, size, heads, lens):  # noqa: F811
                        for b, n in enumerate(lens)]).cuda()
     U.ufp4_cache_append(k, v, slots, c.cache)
     c.check(*U.ufp4_cache_attn(**c.args(), lse=True), dtype=FP)
+
+
+@pytest.mark.parametrize("size", [1e-36, 1e-28, 1e-20, 1e20, 1e32, 1e35, 1e37])
+@pytest.mark.parametrize("heads", [2, 24])
+@pytest.mark.parametrize("grid", [0, 1])
+@pytest.mark.parametrize("by", ["queries", "scale"])
+def test_keys_at_the_ends_of_fp32(U, size, heads, grid, by):  # noqa: F811
+    """Keys far from 1, the queries or the scale as far on the other side: ordinary scores."""
+    g = np.random.default_rng(36)
+    c = Case(U, g, [300, 64], 1, heads, 1, 64, 64, grid, False, FP)
+    k = torch.from_numpy(c.k * np.float32(size / 8)).cuda()
+    slots = torch.cat([torch.from_numpy(c.table[b, np.arange(n) // 64].astype(np.int64) * 64 + np.arange(n) % 64)
+                       for b, n in enumerate(c.lens)]).cuda()
+    U.ufp4_cache_append(k, torch.from_numpy(c.v).cuda(), slots, c.cache)
+    scale = 0.125
+    if by == "queries":
+        c.q *= np.float32(1 / size)
+    else:
+        scale = float(np.float32(0.125 / size))
+    c.check(*U.ufp4_cache_attn(**c.args(), lse=True, scale=scale), scale=scale, dtype=FP)
