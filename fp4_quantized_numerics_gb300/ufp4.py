@@ -1120,7 +1120,8 @@ def ufp4_cache_attn(q, cache, table, lens, mask=None, scale=None, dtype=None, ou
     [batch, m], bit r of a token's word set where it sees new token r (None:
     those up to itself); scale: 1 / sqrt(head_dim) by default.  lse: True or an
     fp32 [batch * m, heads] to write for the logarithms of the softmax's sums.
-    ws: scratch of ufp4_cache_attn_workspace_bytes(...) (a new one by default).
+    ws: scratch of ufp4_cache_attn_workspace_bytes(...), contiguous and 16-byte
+    aligned (a new one by default).
     Returns out [batch * m, heads, head_dim] of `dtype` (q's by default), or
     (out, lse)."""
     dev = _place(q, "q")
@@ -1182,6 +1183,8 @@ def ufp4_cache_attn(q, cache, table, lens, mask=None, scale=None, dtype=None, ou
         ws = _empty((need,), torch.uint8, dev, on) if need else None
     elif ws.get_device() != dev:
         _same_place(ws.get_device(), dev, "ws")
+    elif not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
     st = L.ufp4_cache_attn(qp, dt, qld, qh, batch, m, heads, cc, table.data_ptr(),
                            table.stride(0) if batch > 1 else max(width, 1), width, lens.data_ptr(), mp,
                            dim ** -0.5 if scale is None else scale, op, odt, old, oh, lp,

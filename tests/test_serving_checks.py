@@ -71,3 +71,19 @@ def test_a_refused_cache_leaves_no_scratch_size_behind(machine, monkeypatch):  #
     assert fake.given == [512, 512] and fake.asked == 2
     with pytest.raises(U.UFP4Error):
         call(U.UFP4_MXFP4)
+
+
+def test_scratch_with_gaps_is_refused(machine):  # noqa: F811
+    """What lies between the elements of a strided view is not scratch."""
+    new = lambda *tail, dtype=torch.uint8: _t(On0, 4, 2, 16, *tail, dtype=dtype)  # noqa: E731
+    cache = U.Cache(new(32), new(4), new(dtype=torch.float32), new(32), new(4), new(dtype=torch.float32), 64, U.UFP4_E1M2)
+    call = lambda ws: U.ufp4_cache_attn(_t(On0, 4, 4, 64), cache, _t(On0, 2, 3, dtype=torch.int32),  # noqa: E731
+                                        _t(On0, 2, dtype=torch.int32), ws=ws)
+    room = _t(On0, 1024, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        call(room[::2])
+    with pytest.raises(ValueError):
+        call(room.view(32, 32)[:, :16])
+    assert not machine.calls
+    call(room[:512])
+    assert [n for n, _ in machine.calls] == ["ufp4_cache_attn"]
