@@ -39,6 +39,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// In a branch seldom taken: keeps its arithmetic, which has no effects, from
+// being done for every tile and chosen from.
+__device__ __forceinline__ void seldom() { asm volatile(""); }
+
 // The weights of the values are probabilities times row scales.  A query's are
 // brought into FP16's range by a power of two of its own, 2^-we, as its
 // probabilities are by 2^-mx: both follow what the query has seen, by steps.
@@ -58,18 +62,25 @@ struct Rise {
     int we;
     float l_back, o_back;                // what the sums so far are multiplied by
 };
-// mx and we after keys whose largest score is v and largest score plus scale's
-// exponent w, where one of them passes what counts by more than `slack`.
-__device__ __forceinline__ Rise rise_to(float mx, int we, float v, float w, float slack) {
-    if (!(v > mx + slack || w > mx + (float)we + slack)) return Rise{mx, we, 1.0f, 1.0f};
-    v = fmaxf(v, mx);
-    w = fmaxf(w, mx + (float)we);
+// Whether keys whose largest score is `top`, and largest weight 2^(top + w) (its
+// exponent, without the scale's fraction), pass what counts by more than
+// `slack`; limit: we + slack.  (Differences of scores first, beside which the
+// exponents would vanish where scores are large.)
+__device__ __forceinline__ bool passes(float mx, float limit, float top, float w, float slack) {
+    const float d = top - mx;            // (NaN where neither has seen anything)
+    return d > slack || d + w > limit;
+}
+// mx and we after such keys; or keys that do not pass, but raise the maximum and
+// have the largest weight (else a weight of old would be rounded up by each).
+__device__ __forceinline__ Rise rise_to(float mx, int we, float top, float w, float slack) {
+    const float v = fmaxf(top, mx), back = mx - v;
+    const float of_new = floorf(w + (top - v)), of_old = ceilf((float)we + back);
+    if (!passes(mx, (float)we + slack, top, w, slack) && !(top > mx && of_new >= of_old))
+        return Rise{mx, we, 1.0f, 1.0f};
     // New weights end below 2^(to + 2); what the old ones are given is not less
     // than before, so that sums only shrink.  (Held so that 2^(14 - we) is a
     // normal number; where v is not finite, at a limit.)
-    const float most = fmaxf(floorf(w - v), ceilf(mx + (float)we - v));
-    const int to = (int)fminf(fmaxf(most, (float)kLeastExponent), 127.0f);
-    const float back = mx - v;
+    const int to = (int)fminf(fmaxf(fmaxf(of_new, of_old), (float)kLeastExponent), 127.0f);
     return Rise{v, to, exp2f(back), exp2f(back + (float)(we - to))};
 }
 // Keys [first, last) of a sequence of `len` (at most UFP4_MAX_KEYS, so that a

@@ -48,6 +48,11 @@ constexpr int kQ = kWideQueries, kKeys = 64, kStages = 3, kRing = 3;
 constexpr int kSoftWarps = 8, kDecodeWarps = 8, kThreads = (kSoftWarps + kDecodeWarps + 1) * 32;
 constexpr int kGroups = 2, kGroupWarps = kDecodeWarps / kGroups;   // decoding warps take every second tile,
 constexpr int kWarpKeys = kKeys / kGroupWarps;                     // 16 rows of it each
+// Keys whose scales are 2^80 and more: their products, up to 2^34, would leave
+// fp32 times the scales.  A decoding warp marks their tile.
+constexpr uint32_t kFarKeys = (80u + 127u) << 23;
+constexpr int kFarMark = 1 << 16;
+constexpr float kFarScores = 0x1p20f;                     // scores that fp32 holds to within 2^-4
 constexpr long long kWaitBudget = 2000000000LL;          // SM clocks: about a second
 // What the waits are given (and the test-only stall switch); a test-only build
 // of the library can change them, libufp4 keeps the defaults.
@@ -381,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t 
             const int pos0 = first + i * kKeys + w * kWarpKeys;
             const bool edge = pos0 + kWarpKeys > len - tail || pos0 + kWarpKeys > last;
             uint32_t vtop = 0, vleast = ~0u;                 // (a scale of zero weighs nothing)
+            bool far = false;
 #pragma unroll
             for (int part = 0; part < kWarpKeys / 8; ++part) {
                 const int key = part * 8 + r;
@@ -431,15 +437,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t 
                 float rs = *reinterpret_cast<const float *>(from + (t & 1) * kVal + kCodes + kScales + key * 4);
                 if (unseen) rs = 0.0f;
                 if (t < 2) reinterpret_cast<float *>(meta)[t * kKeys + w * kWarpKeys + key] = rs;
-                const uint32_t bits = t & 1 ? finite_bits(rs) : 0u;
-                vtop = max(vtop, bits);
-                vleast = min(vleast, bits - 1);
+                const uint32_t bits = finite_bits(rs), value = t & 1 ? bits : 0u;
+                vtop = max(vtop, value);
+                vleast = min(vleast, value - 1);
+                far |= !(t & 1) && bits >= kFarKeys;
             }
             vtop = __reduce_max_sync(0xffffffffu, vtop);
             vleast = __reduce_min_sync(0xffffffffu, vleast);
+            far = __any_sync(0xffffffffu, far);
             if (lane == 0) {
                 int *const exps = reinterpret_cast<int *>(meta + kKeys * 8);
-                exps[w] = (int)(vtop >> 23) - 127;
+                exps[w] = (int)(vtop >> 23) - 127 + (far ? kFarMark : 0);
                 exps[kGroupWarps + w] = (int)(vleast >> 23) - 127;
             }
             ptx::fence_proxy_async();
@@ -554,27 +562,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t 
         // of 128 rises by 3).
         constexpr int slack = TWO ? 3 : 8;
         int we = kLeastExponent;                             // of the query's weights
-        // scores times their key's scale (-infinity where hidden), the running
-        // maximum, and the probabilities
-        const auto soften = [&](int i, auto edge_t) -> bool {
-            constexpr bool kEdge = decltype(edge_t)::value != 0;
+        bool large = false;                                  // some maximum of the warp's is 2^20 or more
+        // Scores times their key's scale (-infinity where hidden), the running
+        // maximum, and the probabilities.  kAll: of any tile; else of one without
+        // hidden or far keys, and given back where scores of 2^20 and more raise a
+        // maximum.  vmost: the largest exponent of the tile's row scales.
+        constexpr int kFailed = 0, kDone = 1, kOther = 2;
+        const auto soften = [&](int i, int vmost, bool far, auto all_t) -> int {
+            constexpr bool kAll = decltype(all_t)::value != 0;
             const uint8_t *meta = smem + M::kOffMeta + stage * M::kMeta;
             const float *krs = reinterpret_cast<const float *>(meta) + half * kMine, *vrs = krs + kKeys;
-            const int4 exps = *reinterpret_cast<const int4 *>(meta + kKeys * 8),
-                       least = *reinterpret_cast<const int4 *>(meta + kKeys * 8 + 16);
-            const int vmost = max(max(exps.x, exps.y), max(exps.z, exps.w));
+            const int4 least = *reinterpret_cast<const int4 *>(meta + kKeys * 8 + 16);
             const bool even = vmost - min(min(least.x, least.y), min(least.z, least.w)) <= kEvenScales;
-            // (keys of 2^91 and more: a factor of 2^64 goes from the products, up
-            // to 2^34, to the query's)
-            const bool far = __any_sync(0xffffffffu, krs[lane] >= 0x1p80f);
-            const float qs = far ? qscale * 0x1p64f : qscale;
+            // (far keys: a factor of 2^64 goes from the products to the query's)
+            const float qs = kAll && far ? qscale * 0x1p64f : qscale;
             const uint64_t qs2 = pack2(qs, qs);
             uint64_t z[kMine / 2];
             {
                 uint32_t raw[kMine];
                 ptx::tc_ld_32x32b_x32(tm + kColS + (i & 1) * kKeys + half * kMine, raw);
                 ptx::tc_wait_ld();
-                if (far) {
+                if (kAll && far) {
+                    seldom();
 #pragma unroll
                     for (int j = 0; j < kMine; ++j) raw[j] = __float_as_uint(__uint_as_float(raw[j]) * 0x1p-64f);
                 }
@@ -586,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t 
                     z[j / 2 + 1] = mul2(pack2(s(2), s(3)), pack2(k4.z, k4.w));
                 }
             }
-            if constexpr (kEdge) {
+            if constexpr (kAll) {
                 const uint64_t bits = qm[r];
                 const int pos0 = first + i * kKeys + half * kMine;
 #pragma unroll
@@ -606,32 +615,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t 
                 other = max3(other, v.x, v.y);
             }
             top = fmaxf(top, other) * qs;
-            float wtop = top + (float)vmost;
+            float wtop = (float)vmost;
             if (!even) {
+                seldom();
                 wtop = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < kMine; j += 2) {
                     const float2 v = *reinterpret_cast<const float2 *>(vrs + j), u = unpack2(z[j / 2]);
-                    wtop = max3(wtop, fmaf(u.x, qs, scale_exponent(v.x)), fmaf(u.y, qs, scale_exponent(v.y)));
+                    wtop = max3(wtop, fmaf(u.x, qs, -top) + scale_exponent(v.x), fmaf(u.y, qs, -top) + scale_exponent(v.y));
                 }
             }
             // the place of the probabilities was the last but one tile's
             // (or the scores never came)
             ok = ok && (i < 2 || wait_warp(pv_done(i), ((i >> 1) - 1) & 1));
-            const bool rise = either(top > mx + (float)slack || wtop > mx + (float)(we + slack) || !ok);
+            const bool rise = either(passes(mx, (float)(we + slack), top, wtop, (float)slack) || !ok);
             ptx::tc_fence_after();
             if (rise) {
                 tops[half * kQ + r] = top;
                 wtops[half * kQ + r] = wtop;
-                if (either(!ok)) return false;
-                const Rise to =
-                    rise_to(mx, we, fmaxf(tops[r], tops[kQ + r]), fmaxf(wtops[r], wtops[kQ + r]), (float)slack);
+                const bool other = !kAll && fabsf(top) >= kFarScores;
+                if (either(!ok || other)) return either(!ok) ? kFailed : kOther;
+                const float best = fmaxf(tops[r], tops[kQ + r]);
+                const Rise to = rise_to(mx, we, best, fmaxf(tops[r] - best + wtops[r], tops[kQ + r] - best + wtops[kQ + r]),
+                                        (float)slack);
                 mx = to.mx;
                 we = to.we;
+                if constexpr (kAll) large = __any_sync(0xffffffffu, fabsf(mx) >= kFarScores && mx != -INFINITY);
                 l *= to.l_back;
                 if (i > 0) {
                     // O has the last tile's product first
-                    if (either(!wait_warp(pv_done(i - 1), ((i - 1) >> 1) & 1))) return false;
+                    if (either(!wait_warp(pv_done(i - 1), ((i - 1) >> 1) & 1))) return kFailed;
                     ptx::tc_fence_after();
 #pragma unroll 1
                     for (int h = 0; h < kDim / 64; ++h) {
@@ -657,11 +670,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t 
                     const float4 v4 = *reinterpret_cast<const float4 *>(vrs + c + 2 * j);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float2 y = unpack2(fma2(z[c / 2 + j + e], qs2, base2));
+                        // (kAll: rounded as the maximum was, before that is taken off, which matters far from 0)
+                        float2 y;
+                        if constexpr (kAll) {
+                            const float2 u = unpack2(z[c / 2 + j + e]);
+                            y = make_float2(__fadd_rn(__fmul_rn(u.x, qs), base), __fadd_rn(__fmul_rn(u.y, qs), base));
+                        } else {
+                            y = unpack2(fma2(z[c / 2 + j + e], qs2, base2));
+                        }
                         const uint64_t p = pack2(exp2_fast(y.x), exp2_fast(y.y));
                         sums[e] = add2(sums[e], p);
                         float2 x = unpack2(mul2(mul2(p, up2), e ? pack2(v4.z, v4.w) : pack2(v4.x, v4.y)));
-                        if constexpr (kEdge) {
+                        if constexpr (kAll) {
                             if (y.x == -INFINITY) x.x = 0.0f;
                             if (y.y == -INFINITY) x.y = 0.0f;
                         }
@@ -676,14 +696,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t 
             const float2 two = unpack2(add2(sums[0], sums[1]));
             l += two.x + two.y;
             tc_wait_st();
-            return true;
+            return kDone;
         };
         for (int i = 0; i < tiles; ++i) {
             ok = wait(full(stage), round & 1) && wait(s_full(i & 1), (i >> 1) & 1);
             if (!(ok = __all_sync(0xffffffffu, ok))) *stop = 1;  // (the others stop at their next wait)
             ptx::tc_fence_after();
             const int end = first + (i + 1) * kKeys;
-            if (end > len - tail || end > last ? !soften(i, Int<1>()) : !soften(i, Int<0>())) {
+            const int4 exps = *reinterpret_cast<const int4 *>(smem + M::kOffMeta + stage * M::kMeta + kKeys * 8);
+            int vmost = max(max(exps.x, exps.y), max(exps.z, exps.w));
+            const bool far = vmost >= kFarMark / 2;
+            if (far) {
+                seldom();
+                const auto bare = [](int e) { return e >= kFarMark / 2 ? e - kFarMark : e; };
+                vmost = max(max(bare(exps.x), bare(exps.y)), max(bare(exps.z), bare(exps.w)));
+            }
+            int did = kOther;
+            if (end <= len - tail && end <= last && !far && !large) did = soften(i, vmost, false, Int<0>());
+            if (did == kOther) did = soften(i, vmost, far, Int<1>());
+            if (did != kDone) {
                 ok = false;
                 break;
             }

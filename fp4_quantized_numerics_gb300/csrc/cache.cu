@@ -414,11 +414,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
 
     float o[4 * DC][NT][4] = {};
     float mx[NT][2], l[NT][2] = {};
-    float up[NT][2], wlim[NT][2];                    // 2^(11 - we), and what weights may reach
+    float up[NT][2], limit[NT][2];                   // 2^(11 - we), and we + 3
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         mx[n][0] = mx[n][1] = -INFINITY;
-        wlim[n][0] = wlim[n][1] = -INFINITY;
+        limit[n][0] = limit[n][1] = kLeastExponent + 3;
         up[n][0] = up[n][1] = exp2i(11 - kLeastExponent);
     }
     float qscale[NT][2];
@@ -548,9 +548,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 top[n][c] = fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c]));
-                wtop[n][c] = top[n][c] + vexp;
+                wtop[n][c] = vexp;
             }
         if (vmost - vleast > (uint32_t)kEvenScales << 23) {       // (NaN, too, unless all are)
+            seldom();
             float own[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) own[r] = scale_exponent(vrs[r]);
@@ -558,29 +559,30 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    wtop[n][c] = fmaxf(fmaxf(s[0][n][c] + own[0], s[0][n][2 + c] + own[1]),
-                                       fmaxf(s[1][n][c] + own[2], s[1][n][2 + c] + own[3]));
+                    wtop[n][c] = fmaxf(
+                        fmaxf(s[0][n][c] - top[n][c] + own[0], s[0][n][2 + c] - top[n][c] + own[1]),
+                        fmaxf(s[1][n][c] - top[n][c] + own[2], s[1][n][2 + c] - top[n][c] + own[3]));
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-                rise |= top[n][c] > mx[n][c] + 3.0f || wtop[n][c] > wlim[n][c];
+                rise |= passes(mx[n][c], limit[n][c], top[n][c], wtop[n][c], 3.0f);
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float v = top[n][c], w = wtop[n][c];
+                    float v = top[n][c];
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) {
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                        w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, d));
-                    }
+                    for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                    float w = top[n][c] - v + wtop[n][c];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, d));
                     const Rise to = rise_to(mx[n][c], 11 - power_of(up[n][c]), v, w, 3.0f);
                     mx[n][c] = to.mx;
                     up[n][c] = exp2i(11 - to.we);
-                    wlim[n][c] = to.mx + (float)(to.we + 3);
+                    limit[n][c] = (float)(to.we + 3);
                     l[n][c] *= to.l_back;
 #pragma unroll
                     for (int i = 0; i < 4 * DC; ++i) {

@@ -150,3 +150,28 @@ def test_keys_at_the_ends_of_fp32(U, size, heads, grid, by):  # noqa: F811
     else:
         scale = float(np.float32(0.125 / size))
     c.check(*U.ufp4_cache_attn(**c.args(), lse=True, scale=scale), scale=scale, dtype=FP)
+
+
+@pytest.mark.parametrize("scale", [1e4, 1e8, 1e12])
+@pytest.mark.parametrize("size", [2.0 ** -40, 2.0 ** 30])
+@pytest.mark.parametrize("heads", [2, 24])
+@pytest.mark.parametrize("out", [FP, BF])
+def test_scores_so_large_that_one_key_has_all(U, scale, size, heads, out):  # noqa: F811
+    """Scores beside which the scales' exponents vanish in fp32: the result is
+    the values of the key with the largest score (of orthogonal keys here, so
+    that it is the same key in any precision).  Its probability is 1, its weight
+    within half a step of FP16 (2^-12; two values: 2^-22) of its row's scale."""
+    g = np.random.default_rng(37)
+    c = Case(U, g, [200, 70], 1, heads, 1, 64, 16, 1, False, FP)
+    c.q.zero_()
+    for h in range(heads):
+        c.q[:, h, h % 4] = 4.0
+    for b, n in enumerate(c.lens):
+        for j in range(n):
+            _put(c, b, j, k=np.eye(64)[j % 4] * (j + 1), v=g.standard_normal((1, 64)) * size)
+    o = _f64(U.ufp4_cache_attn(**c.args(), dtype=out, scale=scale))
+    for b, n in enumerate(c.lens):
+        v, _ = c.rows((c.cache.v_codes, c.cache.v_scales, c.cache.v_row_scale), b)
+        for h in range(heads):
+            want = v[0, max(j for j in range(n) if j % 4 == h % 4)]
+            assert np.all(np.abs(o[b, h] - want) <= (2.0 ** -20 if out is FP else 2.0 ** -8 + 2.0 ** -11) * np.abs(want)), (b, h)
