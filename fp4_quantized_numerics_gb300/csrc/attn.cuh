@@ -48,7 +48,9 @@ __device__ __forceinline__ void seldom() { asm volatile(""); }
 // probabilities are by 2^-mx: both follow what the query has seen, by steps.
 constexpr int kLeastExponent = -110;     // (of what is held: 2^(14 - e) and 2^(e - 14) are normal)
 // What stands for row scales within 2^kEvenScales of one another: the largest.
-constexpr int kEvenScales = 4;
+// (2^10 of the 2^25 to 2^28 that FP16 has below 2^11 to 2^14.  Tokens whose sizes
+// differ by 4 and channels by 6 often have more than 2^4 in a tile.)
+constexpr int kEvenScales = 10;
 // (b >> 23) - 127 as fp32: floor(log2) of the positive number with the bits b.
 __device__ __forceinline__ float bits_exponent(uint32_t b) {
     return __uint_as_float(0x4B000000u | b >> 23) - (8388608.0f + 127.0f);

@@ -622,7 +622,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_wide(AttnArgs a, uint32_t 
 #pragma unroll
                 for (int j = 0; j < kMine; j += 2) {
                     const float2 v = *reinterpret_cast<const float2 *>(vrs + j), u = unpack2(z[j / 2]);
-                    wtop = max3(wtop, fmaf(u.x, qs, -top) + scale_exponent(v.x), fmaf(u.y, qs, -top) + scale_exponent(v.y));
+                    // (scores rounded as the largest was)
+                    wtop = max3(wtop, __fadd_rn(__fmul_rn(u.x, qs), -top) + scale_exponent(v.x),
+                                __fadd_rn(__fmul_rn(u.y, qs), -top) + scale_exponent(v.y));
                 }
             }
             // the place of the probabilities was the last but one tile's

@@ -33,8 +33,8 @@ def test_queries_of_zeros_and_small_scales(U, scale, heads, grid):  # noqa: F811
 def _check(c, out, scale, dtype):
     """Case.check of `out`, with what falls below FP16's normal numbers counted
     from the largest probability times row scale that the query itself sees,
-    and not from the largest row scale of the sequence.  (Keys whose scales lie
-    within 2^4 of one another are taken with the largest of them.)"""
+    and not from the largest row scale of the sequence.  (Where it lies within
+    2^10 of that, that one counts.)"""
     cache, group, m, out = c.cache, c.heads // c.kv, c.m, _f64(out)
     for b in range(len(c.lens)):
         at = slice(b * m, (b + 1) * m)
@@ -50,7 +50,7 @@ def _check(c, out, scale, dtype):
             s = np.where(sees[:, some], (q @ kk.T) * scale, -np.inf)
             top = (np.exp(s - s.max(-1, keepdims=True)) * vss).max(-1, keepdims=True) * 448 * R.QMAX[c.grid]
             o, _, tol, _ = R.attn(q, kk, vv, None, sees[:, some], scale, c.q.dtype is BF and not c.rht, dtype is FP,
-                                  top * 16, c.dim)
+                                  top * 2 ** 10, c.dim)
             if c.rht:
                 spread = lambda t: np.repeat(t.reshape(m, -1, 16).sum(-1) / 4, 16, -1)  # noqa: E731
                 tol = spread(tol + 8 * R.U24 * np.abs(o))
@@ -156,7 +156,8 @@ def test_keys_at_the_ends_of_fp32(U, size, heads, grid, by):  # noqa: F811
 @pytest.mark.parametrize("size", [2.0 ** -40, 2.0 ** 30])
 @pytest.mark.parametrize("heads", [2, 24])
 @pytest.mark.parametrize("out", [FP, BF])
-def test_scores_so_large_that_one_key_has_all(U, scale, size, heads, out):  # noqa: F811
+@pytest.mark.parametrize("spread", [0, 20])
+def test_scores_so_large_that_one_key_has_all(U, scale, size, heads, out, spread):  # noqa: F811
     """Scores beside which the scales' exponents vanish in fp32: the result is
     the values of the key with the largest score (of orthogonal keys here, so
     that it is the same key in any precision).  Its probability is 1, its weight
@@ -168,7 +169,8 @@ def test_scores_so_large_that_one_key_has_all(U, scale, size, heads, out):  # no
         c.q[:, h, h % 4] = 4.0
     for b, n in enumerate(c.lens):
         for j in range(n):
-            _put(c, b, j, k=np.eye(64)[j % 4] * (j + 1), v=g.standard_normal((1, 64)) * size)
+            _put(c, b, j, k=np.eye(64)[j % 4] * (j + 1),
+                 v=g.standard_normal((1, 64)) * size * 2.0 ** g.integers(-spread, spread + 1))
     o = _f64(U.ufp4_cache_attn(**c.args(), dtype=out, scale=scale))
     for b, n in enumerate(c.lens):
         v, _ = c.rows((c.cache.v_codes, c.cache.v_scales, c.cache.v_row_scale), b)
