@@ -83,7 +83,7 @@ __device__ __forceinline__ Rise rise_to(float mx, int we, float top, float w, fl
     // than before, so that sums only shrink.  (Held so that 2^(14 - we) is a
     // normal number; where v is not finite, at a limit.)
     const int to = (int)fminf(fmaxf(fmaxf(of_new, of_old), (float)kLeastExponent), 127.0f);
-    return Rise{v, to, exp2f(back), exp2f(back + (float)(we - to))};
+    return Rise{v, to, exp2_fast(back), exp2_fast(back + (float)(we - to))};
 }
 // Keys [first, last) of a sequence of `len` (at most UFP4_MAX_KEYS, so that a
 // tile past its end fits 32 bits) that split s of n takes.

@@ -569,6 +569,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
             for (int c = 0; c < 2; ++c)
                 rise |= passes(mx[n][c], limit[n][c], top[n][c], wtop[n][c], 3.0f);
         if (__any_sync(0xffffffffu, rise)) {
+            // (where the tile's scales are close, the largest of all serves)
+            const uint32_t most = __reduce_max_sync(0xffffffffu, vmost & 0x7FFFFFFFu);
+            const bool close = most - __reduce_min_sync(0xffffffffu, vleast) <= (uint32_t)kEvenScales << 23;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -576,9 +579,13 @@ __global__ void __launch_bounds__(kAttnWarps * 32, NT == 1 && DC <= 2 ? 4 : 2) k
                     float v = top[n][c];
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                    float w = top[n][c] - v + wtop[n][c];
+                    float w = bits_exponent(most);
+                    if (!close) {
+                        seldom();
+                        w = top[n][c] - v + wtop[n][c];
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, d));
+                        for (int d = 4; d < 32; d <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, d));
+                    }
                     const Rise to = rise_to(mx[n][c], 11 - power_of(up[n][c]), v, w, 3.0f);
                     mx[n][c] = to.mx;
                     up[n][c] = exp2i(11 - to.we);
