@@ -21,10 +21,11 @@
 //    threads of a query speak, only when the largest score or weight of a query
 //    rises by more than 2^8 (2^3 for fp32 results).
 // Measured: trees of 32 tokens, 8 sequences of 8192 to 16384 keys, 32 heads over
-// 8, E1M2 rotated, 140 us (380 TFLOP/s of the definition's; twice the queries'
-// product in fact).  A tile of 64 keys takes some 5400 instructions (softmax 2200,
-// decoding 1600, copies 400, the CTA's start 600) at 1.9 an SM and clock; without
-// the decoding 114 us.  A CTA's start and end take 8 us of that, three times over.
+// 8, E1M2 rotated, 152 us (353 TFLOP/s of the definition's; twice the queries'
+// product in fact); 143 before the weights of the values followed each query
+// (attn.cuh), and then 114 without the decoding.  A tile of 64 keys took some 5400
+// instructions there (softmax 2200, decoding 1600, copies 400, the CTA's start 600)
+// at 1.9 an SM and clock.  A CTA's start and end take 8 us, three times over.
 // Steps on the way: operands in shared memory, one group of softmax warps 271 us;
 // Q and P in TMEM 168; a pair of threads a query that agree only when a maximum
 // rises 147; the MMAs issued by an elected lane rather than by lane 0 139 (its

@@ -177,11 +177,13 @@ __global__ void __launch_bounds__(128) k_load(RowArgs a) {
 // to 8, else by a second kernel.
 //
 // Measured: one token of 31 sequences of 4096 to 8192 keys, 64 heads over 8,
-// E1M2 rotated, 93 us (2.5 TB/s, 37 % of the copy bandwidth); of one sequence of
-// 262111 keys, 32 heads over 4, E2M1, 57 us (41 %).  Bound by the instructions of
-// decoding: some 1000 for 32 keys and values (58 % of the issue slots while all
-// SMs work, the integer pipe fullest: an E1M2 code costs 10 operations a word of
-// 8, an E2M1 one 4), where the copy bandwidth leaves 840; and by uneven lengths.
+// E1M2 rotated, 98 us (2.4 TB/s, 35 % of the copy bandwidth); of one sequence of
+// 262111 keys, 32 heads over 4, E2M1, 60 us (39 %); 93 and 57 before the weights
+// of the values followed each query and the second values had sums of their own.
+// Bound by the instructions of decoding: some 1100 for 32 keys and values (57 % of
+// the issue slots while all SMs work, the integer pipe fullest: an E1M2 code costs
+// 10 operations a word of 8, an E2M1 one 4), where the copy bandwidth leaves 840;
+// and by uneven lengths.
 constexpr int kAttnWarps = 4, kTileKeys = 32;
 constexpr int kCluster = 8;              // splits that a cluster joins
 
@@ -825,9 +827,13 @@ cudaError_t join(const AttnArgs &a, int kdim, cudaStream_t s) {
 // The kernel's groups of queries (nt of 8; 0: the wide kernel's 128), how many
 // of its CTAs share an SM, and the keys' time that its start and end take.
 // Measured, 8 sequences of 8192 to 16384 keys of 8 heads of 128, E1M2, us, for 16
-// / 20 / 32 queries a head: groups of 16 92 / 143 / 147, groups of 8 94 / 127 /
-// 163, wide 123 / 123 / 125.  (256-element rows leave no registers for 16, and
-// the wide kernel no TMEM.)
+// / 20 / 32 queries a head: groups of 16 101 / 155 / 162, groups of 8 97 / 130 /
+// 171, wide 142 / 141 / 145.  (256-element rows leave no registers for 16, and
+// the wide kernel no TMEM.)  The wide kernel's start and end take 8 us, as long
+// as 400 to 500 keys.  The number decides little: of 12 shapes (1 to 16 sequences
+// of 1000 to 131072 keys, 32 to 512 queries a head) two differ between 128 and
+// 1536: 8 of 8192 to 16384 keys with 64 queries take 139 us up to 256 and 146
+// from 512 on, one of 131072 keys with 512, fp32, 318 up to 512 and 310 from 768.
 struct Shape {
     int nt, qtiles, resident, start;
 };
@@ -837,7 +843,7 @@ Shape shape_of(int64_t queries, int64_t padded) {
     return Shape{nt, (int)((queries + 8 * nt - 1) / (8 * nt)), nt == 1 && padded <= 128 ? 4 : 2, 64};
 }
 // Whether `splits` are joined within the kernel, by a cluster: one sequence of
-// 1000 keys 7.9 us, with a second kernel 9.7 and a workspace.
+// 1000 keys 8.2 us, with a second kernel 10.0 and a workspace.
 bool clusters(int64_t splits, const Shape &shape) { return shape.nt && splits > 1 && splits <= kCluster; }
 // Splits of a sequence: what makes an SM's CTAs times the keys of one, its start
 // and end among them, the least; fewer CTAs than share an SM

@@ -32,13 +32,14 @@
 //  * Where the tokens do not fit, the inner dimension is gone through in
 //    phases, the sums of a CTA's rows waiting in shared memory.
 //
-// Measured (graph replay, inputs past L2): 131072 x 8192 E2M1, one token, 121 us
-// (5.0 TB/s, 73 % of the copy bandwidth; 114 us with the decoding and the products
+// Measured (graph replay, inputs past L2): 131072 x 8192 E2M1, one token, 123 us
+// (4.9 TB/s, 72 % of the copy bandwidth; 114 us with the decoding and the products
 // left out, so what is left is the loads: their start, the steps' joins and the
 // last, uneven round).  Other splits of the same: warps along k 8 / 4 / 2: 126 /
 // 122 / 138 us; tiles of 16 rows 149; one CTA of 16 warps an SM 128; three chunks
-// ahead 121; consecutive steps a CTA instead of every gridDim.x-th 125.  2048 x
-// 2048, one token, 4.7 us; 64 tokens x 6 of 64 experts of 2048 x 1408 61 us.
+// ahead 121; consecutive steps a CTA instead of every gridDim.x-th 125 (all of
+// these beside 121).  2048 x 2048, one token, 4.8 us; 64 tokens x 6 of 64 experts
+// of 2048 x 1408 59 us.
 #include "common.cuh"
 #include "dequant.cuh"
 #include "internal.h"
@@ -205,8 +206,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
         cols.n = min(seg_tokens - cols.first, a.cpad);
         cols.pad = pad_cols(cols.n);
         const float ts = a.tensor_scale[zero + seg] * kDecoded<GRID>;
-        // exponent of a chunk below which its factor would not be a normal number
-        const int low = -112 - ((int)(__float_as_uint(ts) >> 23 & 0xFFu) - 127);
         const int64_t atom0 = (int64_t)seg * a.atoms;
 
         // chunks that fit beside this many columns, evenly over the phases
@@ -316,7 +315,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_gemv(GemvArgs a) {
                 // (small tokens by small weights: up to 2^16 less for the tokens'
                 // FP16 values, of which the largest keep their bits, rather
                 // than bits of the factor, which all products share)
-                const int own = top_exponent(top), e = max(own, min(own + 16, low));
+                int e = top_exponent(top);
+                if (e < -32) {
+                    asm volatile("");            // (a branch: other tokens do not wait for the scale)
+                    e = max(e, min(e + 16, -112 - ((int)(__float_as_uint(ts) >> 23 & 0xFFu) - 127)));
+                }
                 const float m = exp2i(14 - e);
                 if (b == 0) fac[ch * fpitch + col] = exp2i(e - 14) * ts;
 #pragma unroll
@@ -486,6 +489,8 @@ cudaError_t launch(GemvArgs a, int most_cols, cudaStream_t s) {
     if (passes * tiles > 0x7fffffff) return cudaErrorNotSupported;
     // Warps along k: what makes the CTAs' steps times the chunks of a warp,
     // and the joining of the sums (about 3/4 of a chunk's time), the least.
+    // (Of whole rows: that some warps wait where a phase has fewer chunks than
+    // wk, or no multiple of it, is not priced.)
     const int64_t likely = a.offsets ? std::min<int64_t>(a.slots, a.n_experts) : passes;
     int64_t least = INT64_MAX;
     for (int wk = kWarps; wk >= 1; wk /= 2) {

@@ -684,8 +684,9 @@ UFP4_API ufp4_status ufp4_cache_load(const ufp4_cache *cache, const int64_t *slo
  * Scores are fp32, of q as ufp4_gemv takes x for an FP32 y.  A row's weight,
  * its probability times its scale, enters the sum over V as FP16 (11 bits; 22
  * where out is FP32) relative to the largest weight that the query sees (or up
- * to 2^4 times it, among rows whose scales lie within 2^4 of one another); rows
- * that weigh nothing for a query, however large, do not change its result. */
+ * to 2^10 times it, among rows whose scales lie within 2^10 of one another); rows
+ * that weigh nothing for a query, however large, do not change its result.  A
+ * probability below 2^-126 of the largest counts as none. */
 UFP4_API size_t ufp4_cache_attn_workspace_bytes(int64_t batch, int32_t m, int32_t heads, int64_t width,
                                                 const ufp4_cache *cache);
 UFP4_API ufp4_status ufp4_cache_attn(const void *q, int32_t q_dtype, int64_t ld_q, int64_t head_q, int64_t batch,
