@@ -39,7 +39,6 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cstring>
 #include <mutex>
 #include <type_traits>
@@ -1037,17 +1036,6 @@ bool make_input_tile_map(void *tmap, const void *x, int64_t rows, int64_t cols, 
     return r == CUDA_SUCCESS;
 }
 
-cudaError_t timeout_flag(uint32_t **flag) {
-    static std::atomic<uint32_t *> known[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const bool keep = dev >= 0 && dev < 64;
-    if (keep && (*flag = known[dev].load(std::memory_order_relaxed))) return cudaSuccess;
-    e = cudaGetSymbolAddress(reinterpret_cast<void **>(flag), g_ufp4_timeout);
-    if (e == cudaSuccess && keep) known[dev].store(*flag, std::memory_order_relaxed);
-    return e;
-}
 cudaError_t read_timeout_flag(uint32_t *flag, cudaStream_t s) {
     cudaError_t e = cudaMemcpyFromSymbolAsync(flag, g_ufp4_timeout, sizeof(uint32_t), 0,
                                               cudaMemcpyDeviceToHost, s);

@@ -236,8 +236,8 @@ cudaError_t launch_cache_attn(const CacheAttn &l, cudaStream_t s);
 // Reads and clears the sticky flag that a bounded device-side wait raises
 // when it gives up (synchronises s).
 cudaError_t read_timeout_flag(uint32_t *flag, cudaStream_t s);
-// Where that flag lies on the current device: other kernels' bounded waits raise it too.
-cudaError_t timeout_flag(uint32_t **flag);
 cudaError_t read_quant_timeout_flag(uint32_t *flag, cudaStream_t s);
+// Where the latter lies on the current device: other kernels' bounded waits raise it too.
+cudaError_t timeout_flag(uint32_t **flag);
 
 }  // namespace ufp4

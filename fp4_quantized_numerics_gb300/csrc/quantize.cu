@@ -32,6 +32,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <mutex>
 #include <type_traits>
@@ -3252,6 +3253,17 @@ int num_sms() {
     return cached[dev];
 }
 
+cudaError_t timeout_flag(uint32_t **flag) {
+    static std::atomic<uint32_t *> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep && (*flag = known[dev].load(std::memory_order_relaxed))) return cudaSuccess;
+    e = cudaGetSymbolAddress(reinterpret_cast<void **>(flag), g_quant_timeout);
+    if (e == cudaSuccess && keep) known[dev].store(*flag, std::memory_order_relaxed);
+    return e;
+}
 cudaError_t read_quant_timeout_flag(uint32_t *flag, cudaStream_t s) {
     cudaError_t e = cudaMemcpyFromSymbolAsync(flag, g_quant_timeout, sizeof(uint32_t), 0,
                                               cudaMemcpyDeviceToHost, s);
